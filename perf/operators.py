@@ -181,6 +181,11 @@ def _blocks(x, first, n, size):
     return torch.where((t < n[:, None, None])[..., None, None], y, 0.0), t
 
 
+def _by(x, n):
+    """x / n as one division of tensors (by a host number the GPU multiplies by its rounded inverse)."""
+    return x / torch.full_like(x, n)
+
+
 def _div_codes(x, lo, scale, top):
     c = torch.round((x - lo) / torch.where(scale == 0, 1.0, scale)).clamp(0, top)
     return torch.where(scale == 0, 0.0, c)
@@ -190,8 +195,8 @@ def _int8(y):
     """Codes and scales of blocks [..., 16, H, D]: one scale per block and head."""
     top = y.abs().amax((-3, -1))
     top = torch.where(top < 2.0 ** -100, 0.0, top)
-    inv = torch.where(top > 0, 127.0 / top, 0.0)
-    return torch.round(y * inv[..., None, :, None]).clamp(-127, 127).to(torch.int8), top / 127.0
+    inv = torch.where(top > 0, torch.full_like(top, 127.0) / top, 0.0)
+    return torch.round(y * inv[..., None, :, None]).clamp(-127, 127).to(torch.int8), _by(top, 127.0)
 
 
 def _fill(s, k, v):
@@ -217,7 +222,7 @@ def _fill(s, k, v):
         top = LEVELS[f]
         y, t = _blocks(k, s["first"], n, 32)
         lo, hi = y.amin(2, keepdim=True), y.amax(2, keepdim=True)
-        sc = (hi - lo) / top
+        sc = _by(hi - lo, top)
         codes = _div_codes(y, lo, sc, top).to(torch.uint8)
         whole = t[..., -1] < n[:, None]
         wide = torch.nn.functional.pad(s["bt"], (0, 2 * t.shape[1] - s["bt"].shape[1])) if s["bt"].shape[1] < 2 * t.shape[1] else s["bt"]
@@ -230,7 +235,7 @@ def _fill(s, k, v):
         y, t = _blocks(v, s["first"], n, P)
         y = y.view(*y.shape[:-1], 4, 32)
         lo, hi = y.amin(-1, keepdim=True), y.amax(-1, keepdim=True)
-        sc = (hi - lo) / top
+        sc = _by(hi - lo, top)
         codes = _div_codes(y, lo, sc, top).to(torch.uint8).flatten(-2)
         gone = t < old[:, None, None]
         page = s["bt"][:, :t.shape[1], None].expand(-1, -1, P)[gone].long()
@@ -393,8 +398,9 @@ def _exact_rows(x, form, n, residual, key):
         w = n // P * P
         b = x[:w].view(w // P, P, H, D)
         top = b.abs().amax((1, 3), keepdim=True)
-        code = torch.round(b * (127 / top))
-        y[:w] = (code.double() * (top / 127).double()).view(w, H, D)
+        most = torch.full_like(top, 127)
+        code = torch.round(b * (most / top))
+        y[:w] = (code.double() * (top / most).double()).view(w, H, D)
         return y
     if key:
         w = n // 32 * 32
@@ -403,7 +409,7 @@ def _exact_rows(x, form, n, residual, key):
         w = max(0, n - residual)
         b, dim = x[:w].view(w, H, 4, 32), 3
     lo, hi = b.amin(dim, keepdim=True), b.amax(dim, keepdim=True)
-    sc = (hi - lo) / LEVELS[form]
+    sc = (hi - lo) / torch.full_like(lo, LEVELS[form])
     code = torch.where(sc > 0, torch.round((b - lo) / sc), 0.0)
     y[:w] = (code.double() * sc.double() + lo.double()).view(w, H, D)
     return y
