@@ -90,6 +90,23 @@
  *     tile mt = 2kp + u: byte 8u + 4w + 2*up + r is token 2b + r + 8w.
  *   (Each byte pair is one f16x2 MMA operand register after conversion.)
  *   Bytes of a page past the sequence's length are undefined.
+ * INT8 block records (cfg.bits = S4KV_BITS_INT8), 4128 bytes: [0, 2048) key
+ *   codes, [2048, 4096) value codes, fp32 key scale at 4096 and value scale at
+ *   4100, 24 bytes unused. A block is one page's 16 tokens of one kv head; its
+ *   keys share one scale and its values another. With A the largest |x| of the
+ *   block (NaN if any element is), all binary32 with one rounding each:
+ *     scale = A / 127, inv = 127 / A;  c = round_half_even(x * inv) in -127..127
+ *     A < 2^-100: scale = 0 and every c = 0.  Restored x^ = c * scale.
+ *   A byte holds c + 128. Tokens of the unfinished block (the newest T mod 16)
+ *   wait in 16-bit rings of 16 rows and are quantized as the block fills; a
+ *   block with an element that is not finite restores to values that are not.
+ *   Lane L = 4a + b (a in 0..7, b in 0..3); word (kp, L), kp in 0..3, is the 16
+ *   bytes at kp*512 + L*16 of a half.
+ *   Keys: word (kp, L) holds channels 32b + 8kp + 0..7 of tokens a and a + 8;
+ *     bytes 4x .. 4x+3 are (token a, channel 2x), (a, 2x+1), (a+8, 2x), (a+8, 2x+1).
+ *   Values: bytes 8u .. 8u+7 of word (kp, L), m = 2kp + u: channels 8a + m (lo) and
+ *     64 + 8a + m (hi) as (token 2b, lo), (2b+1, lo), (2b, hi), (2b+1, hi),
+ *     (2b+8, lo), (2b+9, lo), (2b+8, hi), (2b+9, hi).
  * Residual rings (cache dtype): key ring [slot][kv head][32][128], token t at
  *   row t mod 32; value ring [slot][kv head][R][128], token t at row t mod R.
  * Canonical state of a sequence of length T: keys of tokens < 32*floor(T/32)
@@ -130,8 +147,12 @@ enum {
   S4KV_DEV_BAD_SLOT = 3,       /* slot id outside [0, max_slots) */
   S4KV_DEV_BAD_TABLE = 4,      /* table too narrow for the sequence */
   S4KV_DEV_BAD_CU = 5,         /* cu_new not non-decreasing / total mismatch */
-  S4KV_DEV_TIMEOUT = 6         /* an mbarrier wait exceeded its limit */
+  S4KV_DEV_TIMEOUT = 6,        /* an mbarrier wait exceeded its limit */
+  S4KV_DEV_BAD_POSITION = 7    /* a token past the rotation table, or a range past its sequence */
 };
+
+/* cfg.bits of INT8 pages with one scale per 16-token block, kv head and tensor. */
+enum { S4KV_BITS_INT8 = 0x108 };
 
 typedef struct {
   int num_layers;    /* layers sharing the pool (one page region per layer) */
@@ -145,7 +166,9 @@ typedef struct {
   int max_slots;     /* sequence slots (residual rings), 1..65536 */
   int dtype;         /* S4KV_F16 or S4KV_BF16: the K/V/Q input format */
   int bits;          /* code width: 4 (0 means 4) or 2, the pages' own KIVI
-                        settings; 8 selects FP8 E4M3 pages instead (below) */
+                        settings; 8 selects FP8 E4M3 pages instead (below),
+                        S4KV_BITS_INT8 integer pages with a scale per block
+                        (residual_v is not used by either) */
 } s4kv_config;
 
 typedef struct s4kv_cache s4kv_cache;
@@ -235,6 +258,39 @@ int s4kv_append(s4kv_cache* cache, int layer, const void* k, const void* v, int 
                 const int32_t* cu_new, const int32_t* slot_ids, const int32_t* seq_lens_before,
                 const int32_t* block_table, int bt_stride, int n, void* stream);
 
+/* Rotary position embedding. The first rotary_dim channels of a head turn in
+ * pairs; pair i of a row at position p turns by the angle whose cosine is
+ * table[p][i] and whose sine is table[p][rotary_dim/2 + i] (fp32, device,
+ * 16-byte aligned, [max_positions][rotary_dim]):
+ *     a' = a cos - b sin,  b' = b cos + a sin
+ * each product and the sum rounded to fp32 (no fused multiply-add), the result
+ * rounded once to the cache dtype. Pair i is channels (i, i + rotary_dim/2), or
+ * (2i, 2i + 1) with interleaved != 0. Channels from rotary_dim on are unchanged. */
+typedef struct {
+  const float* table;
+  int max_positions;   /* rows of the table, > 0 */
+  int rotary_dim;      /* 16..128, a multiple of 16 */
+  int interleaved;     /* 0 or 1 */
+} s4kv_rope;
+
+/* s4kv_append with the position rotation applied on the way: each new key row is
+ * turned by its token's position (its index in the sequence) before it is stored,
+ * so pages and rings end as s4kv_append would leave them for rows rotated
+ * beforehand. Every page format. Values are stored as they are.
+ *   q, q_out   optional (both NULL to leave out): [num_new_tokens][num_q_heads][128]
+ *              in the cache dtype, rows as those of k: the new tokens' queries,
+ *              turned by the same positions into q_out, which may be q itself but
+ *              must not overlap it otherwise. 16-byte aligned.
+ * A sequence whose length after the append passes max_positions is reported as
+ * S4KV_DEV_BAD_POSITION: nothing of it is stored and its q_out rows are left as
+ * they were. Other arguments and errors are those of s4kv_append; INVALID_ARG for
+ * a bad table, UNSUPPORTED for another rotary_dim or num_q_heads > 1024. One
+ * kernel launch. */
+int s4kv_append_rope(s4kv_cache* cache, int layer, const s4kv_rope* rope, const void* k, const void* v,
+                     int num_new_tokens, const int32_t* cu_new, const int32_t* slot_ids,
+                     const int32_t* seq_lens_before, const int32_t* block_table, int bt_stride, int n,
+                     const void* q, int num_q_heads, void* q_out, void* stream);
+
 /* Scratch needed by s4kv_decode_attention for B sequences (two partial results
  * per worker warp; it depends on B, the GQA group and the device, not on the
  * lengths; max_seq_len is accepted for symmetry with the decode call). */
@@ -294,6 +350,48 @@ int s4kv_multi_query_attention(s4kv_cache* cache, int layer, const void* q, int 
                                float sm_scale, void* out, int out_dtype, void* workspace,
                                size_t ws_bytes, int max_seq_len, void* stream);
 
+/* Causal attention of the last num_q_tokens tokens of each sequence within a
+ * sliding window, with the first tokens kept visible (sinks): the query at
+ * position p attends to the tokens t <= p with t > p - window or t < num_sinks.
+ *   window        W >= 1: the newest W tokens, the query's own included.
+ *   num_sinks     S >= 0.
+ *   num_q_tokens  nq, 1..16; nq * (num_q_heads / H_kv) <= 96. KIVI pages need
+ *                 nq <= R (UNSUPPORTED otherwise, as for s4kv_multi_query_attention).
+ *   q, out        [B][num_q_tokens][num_q_heads][128] (q in the cache dtype, out in
+ *                 out_dtype: S4KV_F32 or the cache dtype).
+ *   seq_lens[b]   T_b, equal to the slot's stored length: 0 gives zero rows, 0 < T_b <
+ *                 nq is reported as S4KV_DEV_BAD_LENGTH (zero rows).
+ * Only blocks with a visible token are read (a block: 32 tokens of KIVI pages, 16
+ * of the others), so table entries of pages whose blocks lie between the sinks and
+ * the window may hold anything: their pages can have been given away. (An append
+ * on KIVI pages still writes the page of token T - R - 1 and the newest key group.)
+ * A masked token contributes nothing, whatever its stored key and value hold.
+ * Every page format. Two kernel launches, as for s4kv_decode_attention; the
+ * workspace rule and the other arguments and errors are its too. */
+int s4kv_window_workspace_bytes(const s4kv_cache* cache, int B, int num_q_tokens, int num_q_heads,
+                                int max_seq_len, size_t* bytes);
+int s4kv_window_attention(s4kv_cache* cache, int layer, const void* q, int num_q_tokens, int num_q_heads,
+                          int window, int num_sinks, const int32_t* block_table, int bt_stride,
+                          const int32_t* seq_lens, const int32_t* slot_ids, int B, float sm_scale, void* out,
+                          int out_dtype, void* workspace, size_t ws_bytes, int max_seq_len, void* stream);
+
+/* Restores token ranges of n sequences into dense rows: what attention sees of
+ * them, for a dense kernel over a cached prefix or for moving a cache elsewhere.
+ *   cu_rows      int32 [n+1], non-decreasing, cu_rows[0] = 0, cu_rows[n] = num_rows:
+ *                sequence i owns output rows [cu_rows[i], cu_rows[i+1]).
+ *   first_token  int32 [n] or NULL (0): row cu_rows[i] + j is token first_token[i] + j.
+ *   seq_lens[i]  T_i, equal to the slot's stored length (else S4KV_DEV_BAD_LENGTH);
+ *                a range that leaves [0, T_i) is S4KV_DEV_BAD_POSITION. Rows of a
+ *                sequence that is reported, and of a page that is, are left as they were.
+ *   out_k, out_v [num_rows][H_kv][128] in out_dtype (S4KV_F32, or the cache dtype: the
+ *                restored fp32 value rounded once), 16-byte aligned.
+ * Every page format; one kernel launch; n up to 8192. Only the pages that the ranges
+ * need are read. */
+int s4kv_gather(s4kv_cache* cache, int layer, const int32_t* block_table, int bt_stride,
+                const int32_t* seq_lens, const int32_t* slot_ids, const int32_t* first_token,
+                const int32_t* cu_rows, int num_rows, int n, void* out_k, void* out_v, int out_dtype,
+                void* stream);
+
 /* One decode step in one launch: appends one token to every sequence and runs
  * decode attention over the state after the append, with the result of
  * s4kv_append (one row per sequence) followed by s4kv_decode_attention.
@@ -314,7 +412,8 @@ int s4kv_multi_query_attention(s4kv_cache* cache, int layer, const void* q, int 
  * out), then attend; a second, small launch combines split work. The barrier
  * words live in the cache's pool, so decode-step calls on one cache must not
  * overlap in time (order them on one stream). Not for the FFMA path
- * (S4KV_OPT_DECODE_IMPL = 1: S4KV_ERR_UNSUPPORTED). */
+ * (S4KV_OPT_DECODE_IMPL = 1: S4KV_ERR_UNSUPPORTED). INT8 pages: the append and
+ * the attention are launches of their own, in stream order. */
 int s4kv_decode_step(s4kv_cache* cache, int layer, const void* k_new, const void* v_new, const void* q,
                      int num_q_heads, const int32_t* block_table, int bt_stride, const int32_t* seq_lens,
                      const int32_t* slot_ids, int B, float sm_scale, void* out, int out_dtype, void* workspace,

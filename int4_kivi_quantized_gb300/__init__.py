@@ -29,6 +29,9 @@ S4KV_F16, S4KV_BF16, S4KV_F32 = 0, 1, 2
 
 S4KV_DEV_BAD_PAGE, S4KV_DEV_BAD_LENGTH, S4KV_DEV_BAD_SLOT = 1, 2, 3
 S4KV_DEV_BAD_TABLE, S4KV_DEV_BAD_CU, S4KV_DEV_TIMEOUT = 4, 5, 6
+S4KV_DEV_BAD_POSITION = 7
+
+S4KV_BITS_INT8 = 0x108
 
 S4KV_OPT_DECODE_WARPS, S4KV_OPT_DECODE_IMPL, S4KV_OPT_WAIT_NS, S4KV_OPT_TAIL_COST = 1, 2, 3, 4
 S4KV_OPT_KEY_SPLIT = 5
@@ -55,6 +58,11 @@ class s4kv_layout(ctypes.Structure):
         "vring_offset", "vring_slot_stride", "vring_head_stride", "vring_row_stride", "scale_offset")]
 
 
+class s4kv_rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("max_positions", ctypes.c_int), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int)]
+
+
 class s4kv_kv_bytes_report(ctypes.Structure):
     _fields_ = [(n, ctypes.c_double) for n in (
         "fp16_equiv_bytes", "code_bytes", "meta_bytes", "residual_bytes", "paged_bytes")]
@@ -78,6 +86,10 @@ def _load():
         "s4kv_decode_step": [P, I, P, P, P, I, P, I, P, P, I, ctypes.c_float, P, I, P, SZ, I, P],
         "s4kv_multi_query_workspace_bytes": [P, I, I, I, I, ctypes.POINTER(SZ)],
         "s4kv_multi_query_attention": [P, I, P, I, I, P, I, P, P, I, ctypes.c_float, P, I, P, SZ, I, P],
+        "s4kv_append_rope": [P, I, ctypes.POINTER(s4kv_rope), P, P, I, P, P, P, P, I, I, P, I, P, P],
+        "s4kv_window_workspace_bytes": [P, I, I, I, I, ctypes.POINTER(SZ)],
+        "s4kv_window_attention": [P, I, P, I, I, I, I, P, I, P, P, I, ctypes.c_float, P, I, P, SZ, I, P],
+        "s4kv_gather": [P, I, P, I, P, P, P, P, I, I, P, P, I, P],
         "s4kv_dequant_debug": [P, I, I, P, I, P, P, P],
         "s4kv_get_status": [P, P, ctypes.POINTER(I)],
         "s4kv_kv_bytes": [ctypes.POINTER(s4kv_config), ctypes.c_double, ctypes.c_double,
@@ -223,6 +235,41 @@ def s4kv_multi_query_attention(h, layer, q, num_q_tokens, num_q_heads, block_tab
            "s4kv_multi_query_attention")
 
 
+def s4kv_append_rope(h, layer, rope: s4kv_rope, k, v, num_new_tokens, cu_new, slot_ids, seq_lens_before, block_table,
+                     bt_stride, n, q=None, num_q_heads=0, q_out=None, stream=None):
+    """s4kv_append with the keys (and the queries q into q_out) rotated by their positions on the way."""
+    _check(_lib.s4kv_append_rope(h, int(layer), ctypes.byref(rope), _ptr(k), _ptr(v), int(num_new_tokens),
+                                 _ptr(cu_new), _ptr(slot_ids), _ptr(seq_lens_before), _ptr(block_table),
+                                 int(bt_stride), int(n), _ptr(q), int(num_q_heads), _ptr(q_out),
+                                 _stream(stream)), "s4kv_append_rope")
+
+
+def s4kv_window_workspace_bytes(h, B, num_q_tokens, num_q_heads, max_seq_len) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.s4kv_window_workspace_bytes(h, int(B), int(num_q_tokens), int(num_q_heads), int(max_seq_len),
+                                            ctypes.byref(out)), "s4kv_window_workspace_bytes")
+    return out.value
+
+
+def s4kv_window_attention(h, layer, q, num_q_tokens, num_q_heads, window, num_sinks, block_table, bt_stride,
+                          seq_lens, slot_ids, B, sm_scale, out, out_dtype, workspace, ws_bytes, max_seq_len,
+                          stream=None):
+    """Causal attention of the last tokens within a sliding window, the first tokens kept visible."""
+    _check(_lib.s4kv_window_attention(h, int(layer), _ptr(q), int(num_q_tokens), int(num_q_heads), int(window),
+                                      int(num_sinks), _ptr(block_table), int(bt_stride), _ptr(seq_lens),
+                                      _ptr(slot_ids), int(B), float(sm_scale), _ptr(out), int(out_dtype),
+                                      _ptr(workspace), int(ws_bytes), int(max_seq_len), _stream(stream)),
+           "s4kv_window_attention")
+
+
+def s4kv_gather(h, layer, block_table, bt_stride, seq_lens, slot_ids, first_token, cu_rows, num_rows, n, out_k, out_v,
+                out_dtype, stream=None):
+    """Restores token ranges of n sequences into dense rows."""
+    _check(_lib.s4kv_gather(h, int(layer), _ptr(block_table), int(bt_stride), _ptr(seq_lens), _ptr(slot_ids),
+                            _ptr(first_token), _ptr(cu_rows), int(num_rows), int(n), _ptr(out_k), _ptr(out_v),
+                            int(out_dtype), _stream(stream)), "s4kv_gather")
+
+
 def s4kv_decode_step(h, layer, k_new, v_new, q, num_q_heads, block_table, bt_stride, seq_lens, slot_ids, B,
                      sm_scale, out, out_dtype, workspace, ws_bytes, max_seq_len, stream=None):
     """One token appended per sequence and decode attention over the result, in one launch."""
@@ -254,8 +301,24 @@ def s4kv_get_status(h, stream=None):
     return rc, detail.value
 
 
+class Rope:
+    """A rotation table for append_rope: `table` [max_positions, rotary_dim] in fp32 on the cache's
+    device, the cosines of the rotary_dim / 2 angles of each position, then their sines. It is
+    used in place and kept alive by this object."""
+
+    def __init__(self, table, interleaved=False):
+        import torch
+        if table.dim() != 2 or table.dtype != torch.float32 or not table.is_contiguous():
+            raise ValueError("the rotation table is a contiguous fp32 tensor [max_positions, rotary_dim]")
+        self.table = table
+        self.interleaved = bool(interleaved)
+        self.c = s4kv_rope(table.data_ptr(), table.shape[0], table.shape[1], int(self.interleaved))
+
+
 class KVCache:
-    """A cache bound to a torch-allocated device pool (torch provides memory only)."""
+    """A cache bound to a torch-allocated device pool (torch provides memory only).
+
+    bits: 4 (default), 2, 8 (FP8 E4M3) or "int8" (one scale per 16-token block and head)."""
 
     def __init__(self, num_layers, num_pages, num_kv_heads, residual_v, max_slots, dtype="fp16",
                  device="cuda", bits=4):
@@ -263,6 +326,7 @@ class KVCache:
         self.dtype = dtype
         self.cdtype = S4KV_F16 if dtype == "fp16" else S4KV_BF16
         self.torch_dtype = torch.float16 if dtype == "fp16" else torch.bfloat16
+        bits = S4KV_BITS_INT8 if bits == "int8" else bits
         self.bits = bits
         self.cfg = make_config(num_layers, num_pages, num_kv_heads, residual_v, max_slots,
                                self.cdtype, bits=bits)
@@ -314,7 +378,11 @@ class KVCache:
         if out is None:
             dt = torch.float32 if out_dtype == S4KV_F32 else self.torch_dtype
             out = torch.empty((B, Hq, 128), dtype=dt, device=q.device)
-        ws, nbytes = self.workspace(B, Hq, max_seq_len)
+        if self.bits == S4KV_BITS_INT8:
+            nbytes = s4kv_decode_workspace_bytes(self.h, B, Hq, max_seq_len)
+            ws = self._scratch(nbytes, stream)
+        else:
+            ws, nbytes = self.workspace(B, Hq, max_seq_len)
         s4kv_decode_attention(self.h, layer, q, Hq, block_table, block_table.shape[1], seq_lens,
                               slot_ids, B, sm_scale, out, out_dtype, ws, nbytes, max_seq_len, stream)
         return out
@@ -328,11 +396,113 @@ class KVCache:
             dt = torch.float32 if out_dtype == S4KV_F32 else self.torch_dtype
             out = torch.empty((B, nq, Hq, 128), dtype=dt, device=q.device)
         nbytes = s4kv_multi_query_workspace_bytes(self.h, B, nq, Hq, max_seq_len)
+        if self.bits == S4KV_BITS_INT8:
+            s4kv_multi_query_attention(self.h, layer, q, nq, Hq, block_table, block_table.shape[1], seq_lens, slot_ids, B,
+                                       sm_scale, out, out_dtype, self._scratch(nbytes, stream), nbytes, max_seq_len,
+                                       stream)
+            return out
         if self._ws is None or self._ws.numel() < nbytes:
             self._ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self.pool.device)
         s4kv_multi_query_attention(self.h, layer, q, nq, Hq, block_table, block_table.shape[1], seq_lens,
                                    slot_ids, B, sm_scale, out, out_dtype, self._ws, nbytes, max_seq_len, stream)
         return out
+
+    # ---- calls that check their tensors and take scratch of their own ----
+    def _tensor(self, t, name, dtype, shape):
+        """t is a contiguous tensor of this cache's device; shape: sizes, None for any."""
+        if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+            raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} is wanted, got {t.dtype} {tuple(t.shape)}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} is not contiguous")
+        if t.device != self.pool.device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {self.pool.device}")
+        return t
+
+    def _scratch(self, nbytes, stream):
+        """Scratch of one call, allocated on its stream: calls on other streams and captured graphs share none of it."""
+        import torch
+        if stream is None:
+            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self.pool.device)
+        st = torch.cuda.ExternalStream(stream, device=self.pool.device) if isinstance(stream, int) else stream
+        with torch.cuda.stream(st):
+            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self.pool.device)
+
+    def _out(self, out, name, shape, out_dtype):
+        import torch
+        if out_dtype not in (S4KV_F32, self.cdtype):
+            raise ValueError("out_dtype is S4KV_F32 or the cache's dtype")
+        dt = torch.float32 if out_dtype == S4KV_F32 else self.torch_dtype
+        if out is None:
+            return torch.empty(shape, dtype=dt, device=self.pool.device)
+        return self._tensor(out, name, dt, shape)
+
+    def append_rope(self, layer, k, v, cu_new, seq_lens_before, block_table, rope, slot_ids=None, q=None, q_out=None,
+                    stream=None):
+        """append() with the new keys rotated by their positions on the way (rope: a Rope). With q
+        [tokens, H_q, 128], the new tokens' queries are rotated too, into q_out (a new tensor if
+        None; q itself is allowed), which is returned."""
+        import torch
+        i32, n = torch.int32, seq_lens_before.numel()
+        self._tensor(k, "k", self.torch_dtype, (None, self.H, 128))
+        self._tensor(v, "v", self.torch_dtype, tuple(k.shape))
+        self._tensor(cu_new, "cu_new", i32, (n + 1,))
+        self._tensor(seq_lens_before, "seq_lens_before", i32, (n,))
+        self._tensor(block_table, "block_table", i32, (None, None))
+        self._tensor(rope.table, "the rotation table", torch.float32, (None, None))
+        if block_table.shape[0] < n:
+            raise ValueError("block_table has fewer rows than there are sequences")
+        if slot_ids is not None:
+            self._tensor(slot_ids, "slot_ids", i32, (n,))
+        if q is not None:
+            self._tensor(q, "q", self.torch_dtype, (k.shape[0], None, 128))
+            q_out = torch.empty_like(q) if q_out is None else self._tensor(q_out, "q_out", self.torch_dtype, tuple(q.shape))
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        with torch.cuda.device(self.pool.device):
+            s4kv_append_rope(self.h, layer, rope.c, k, v, k.shape[0], cu_new, slot_ids, seq_lens_before, block_table,
+                             block_table.shape[1], n, q, 0 if q is None else q.shape[1], q_out, stream)
+        return q_out
+
+    def window(self, layer, q, block_table, seq_lens, max_seq_len, window, num_sinks=0, out=None, out_dtype=S4KV_F32,
+               slot_ids=None, sm_scale=0.0, stream=None):
+        """Causal attention of the last nq tokens, q [B, nq, H_q, 128], within the newest `window` tokens
+        of each query's position and the first `num_sinks` tokens -> out [B, nq, H_q, 128]."""
+        import torch
+        B, nq, Hq, _ = self._tensor(q, "q", self.torch_dtype, (None, None, None, 128)).shape
+        self._tensor(block_table, "block_table", torch.int32, (None, None))
+        self._tensor(seq_lens, "seq_lens", torch.int32, (B,))
+        if block_table.shape[0] < B:
+            raise ValueError("block_table has fewer rows than there are sequences")
+        if slot_ids is not None:
+            self._tensor(slot_ids, "slot_ids", torch.int32, (B,))
+        out = self._out(out, "out", (B, nq, Hq, 128), out_dtype)
+        with torch.cuda.device(self.pool.device):
+            nbytes = s4kv_window_workspace_bytes(self.h, B, nq, Hq, max_seq_len)
+            ws = self._scratch(nbytes, stream)
+            s4kv_window_attention(self.h, layer, q, nq, Hq, window, num_sinks, block_table, block_table.shape[1],
+                                  seq_lens, slot_ids, B, sm_scale, out, out_dtype, ws, nbytes, max_seq_len, stream)
+        return out
+
+    def gather(self, layer, block_table, seq_lens, cu_rows, num_rows, first=None, slot_ids=None, out_k=None, out_v=None,
+               out_dtype=S4KV_F32, stream=None):
+        """Restores tokens first[i] .. of sequence i (0 without first) into rows [cu_rows[i], cu_rows[i+1])
+        of two dense tensors [num_rows, H_kv, 128], which are returned as (k, v)."""
+        import torch
+        i32, n = torch.int32, seq_lens.numel()
+        self._tensor(block_table, "block_table", i32, (None, None))
+        self._tensor(seq_lens, "seq_lens", i32, (n,))
+        self._tensor(cu_rows, "cu_rows", i32, (n + 1,))
+        if block_table.shape[0] < n:
+            raise ValueError("block_table has fewer rows than there are sequences")
+        for t, name in ((first, "first"), (slot_ids, "slot_ids")):
+            if t is not None:
+                self._tensor(t, name, i32, (n,))
+        out_k = self._out(out_k, "out_k", (num_rows, self.H, 128), out_dtype)
+        out_v = self._out(out_v, "out_v", (num_rows, self.H, 128), out_dtype)
+        with torch.cuda.device(self.pool.device):
+            s4kv_gather(self.h, layer, block_table, block_table.shape[1], seq_lens, slot_ids, first, cu_rows, num_rows,
+                        n, out_k, out_v, out_dtype, stream)
+        return out_k, out_v
 
     def dequant(self, layer, slot, block_table_row, seq_len, stream=None):
         import torch

@@ -22,6 +22,9 @@ SOURCES = {
     "s4kv_decode.cu": [],
     "s4kv_mq.cu": [],
     "s4kv_noalloc.cu": [],
+    "s4kv_int8.cu": EXACT,
+    "s4kv_window.cu": [],
+    "s4kv_gather.cu": EXACT,
 }
 
 
@@ -49,6 +52,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     with open(stamp, "w") as f:
         f.write(" ".join(extra))
     headers = [os.path.join(CSRC, "s4kv_common.cuh"), os.path.join(CSRC, "s4kv_kernels.cuh"),
+               os.path.join(CSRC, "s4kv_rope.cuh"), os.path.join(CSRC, "s4kv_quant.cuh"),
                os.path.join(ROOT, "include", "s4kv.h"),
                __file__]
     jobs = []

@@ -14,6 +14,7 @@
 
 #include "s4kv_common.cuh"
 #include "s4kv_quant.cuh"
+#include "s4kv_rope.cuh"
 
 #include <cuda_fp8.h>
 #include <climits>
@@ -791,8 +792,10 @@ __device__ void fast_tile(const AppendArgs& a, const Item& it, const uint8_t* st
 // Copies the new rows bound for a ring: tokens [tb, T1) into rows t % mod. The
 // first 16-byte chunk of each thread was loaded early (first); the rest are
 // loaded four at a time before they are stored.
+// ROPE: the rows are keys to turn on the way (first is turned already).
+template <bool ROPE = false>
 __device__ __forceinline__ void ring_copy(uint16_t* ring, int mod, int tb, int T1, const uint16_t* src_base,
-                                          long long row_of_t0, int H, int h, uint4 first) {
+                                          long long row_of_t0, int H, int h, uint4 first, const RopeArgs& rope, int dtype) {
   const int n = (T1 - tb) * 16;
   int q = threadIdx.x;
   if (q < n) reinterpret_cast<uint4*>(ring + static_cast<long long>((tb + q / 16) % mod) * kD)[q % 16] = first;
@@ -802,7 +805,9 @@ __device__ __forceinline__ void ring_copy(uint16_t* ring, int mod, int tb, int T
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int qq = q + u * kThreads, t = tb + qq / 16;
-      v[u] = reinterpret_cast<const uint4*>(row_ptr(src_base, row_of_t0 + t, H, h))[qq % 16];
+      const uint16_t* row = row_ptr(src_base, row_of_t0 + t, H, h);
+      if constexpr (ROPE) v[u] = rope::turned_chunk(rope, row, t, qq % 16, dtype);
+      else v[u] = reinterpret_cast<const uint4*>(row)[qq % 16];
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -812,8 +817,11 @@ __device__ __forceinline__ void ring_copy(uint16_t* ring, int mod, int tb, int T
   }
   for (; q < n; q += kThreads) {
     const int t = tb + q / 16;
-    reinterpret_cast<uint4*>(ring + static_cast<long long>(t % mod) * kD)[q % 16] =
-        reinterpret_cast<const uint4*>(row_ptr(src_base, row_of_t0 + t, H, h))[q % 16];
+    const uint16_t* row = row_ptr(src_base, row_of_t0 + t, H, h);
+    uint4 x;
+    if constexpr (ROPE) x = rope::turned_chunk(rope, row, t, q % 16, dtype);
+    else x = reinterpret_cast<const uint4*>(row)[q % 16];
+    reinterpret_cast<uint4*>(ring + static_cast<long long>(t % mod) * kD)[q % 16] = x;
   }
 }
 
@@ -828,7 +836,7 @@ __device__ __forceinline__ bool ring_item_is_few(const AppendArgs& a, const Item
   return vend - Tv0 <= kThreads / 32 && !(Tk0 < it.T0 && Tk0 + kG <= it.T1);
 }
 
-template <int BITS>
+template <int BITS, bool ROPE = false>
 __device__ __forceinline__ void ring_item_few(const AppendArgs& a, const Item& it) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i = it.i, h = it.h, T0 = it.T0, T1 = it.T1, row0 = it.row0;
@@ -840,6 +848,12 @@ __device__ __forceinline__ void ring_item_few(const AppendArgs& a, const Item& i
   if (static_cast<long long>(a.bt_stride) * kP < T1) {
     if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_TABLE, i);
     return;
+  }
+  if constexpr (ROPE) {
+    if (T1 > a.rope.max_pos) {   // a token past the rotation table: nothing of the sequence is stored
+      if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_POSITION, i);
+      return;
+    }
   }
   Ctx c{&a, a.block_table + static_cast<long long>(i) * a.bt_stride, slot};
   uint16_t* kring = reinterpret_cast<uint16_t*>(a.kring) + slot * a.kring_slot + h * a.kring_head;
@@ -857,8 +871,11 @@ __device__ __forceinline__ void ring_item_few(const AppendArgs& a, const Item& i
   }
   const int kb = max(Tk1, T0), vb = max(T0, Tv1);
   uint4 kfirst = make_uint4(0u, 0u, 0u, 0u), vfirst = kfirst;
-  if (tid < (T1 - kb) * 16)
-    kfirst = reinterpret_cast<const uint4*>(row_ptr(a.k, row0 + (kb + tid / 16 - T0), a.H, h))[tid % 16];
+  if (tid < (T1 - kb) * 16) {
+    const uint16_t* row = row_ptr(a.k, row0 + (kb + tid / 16 - T0), a.H, h);
+    if constexpr (ROPE) kfirst = rope::turned_chunk(a.rope, row, kb + tid / 16, tid % 16, a.dtype);
+    else kfirst = reinterpret_cast<const uint4*>(row)[tid % 16];
+  }
   if (tid < (T1 - vb) * 16)
     vfirst = reinterpret_cast<const uint4*>(row_ptr(a.v, row0 + (vb + tid / 16 - T0), a.H, h))[tid % 16];
   if (T0 != 0 && stored != T0) {
@@ -868,14 +885,14 @@ __device__ __forceinline__ void ring_item_few(const AppendArgs& a, const Item& i
   }
   if (tv < vend) value_token_row<BITS>(c, h, tv, vraw, vpage);
   __syncthreads();
-  ring_copy(kring, kG, kb, T1, a.k, static_cast<long long>(row0) - T0, a.H, h, kfirst);
-  ring_copy(vring, a.R, vb, T1, a.v, static_cast<long long>(row0) - T0, a.H, h, vfirst);
+  ring_copy<ROPE>(kring, kG, kb, T1, a.k, static_cast<long long>(row0) - T0, a.H, h, kfirst, a.rope, a.dtype);
+  ring_copy(vring, a.R, vb, T1, a.v, static_cast<long long>(row0) - T0, a.H, h, vfirst, a.rope, a.dtype);
   if (tid == 0) *len_word = T1;
   __syncthreads();
 }
 
 // Ring items and the tiles that are not whole new key groups.
-template <int BITS>
+template <int BITS, bool ROPE = false>
 __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint8_t (*stage)[1536], const uint16_t** src,
                                        uint8_t* rows) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -888,6 +905,12 @@ __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint
   if (static_cast<long long>(a.bt_stride) * kP < T1) {
     if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_TABLE, i);
     return;
+  }
+  if constexpr (ROPE) {
+    if (T1 > a.rope.max_pos) {   // a token past the rotation table: nothing of the sequence is stored
+      if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_POSITION, i);
+      return;
+    }
   }
   Ctx c{&a, a.block_table + static_cast<long long>(i) * a.bt_stride, slot};
   uint16_t* kring = reinterpret_cast<uint16_t*>(a.kring) + slot * a.kring_slot + h * a.kring_head;
@@ -916,8 +939,11 @@ __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint
     }
     const int kb = max(Tk1, T0), vb = max(T0, Tv1);
     uint4 kfirst = make_uint4(0u, 0u, 0u, 0u), vfirst = kfirst;
-    if (tid < (T1 - kb) * 16)
-      kfirst = reinterpret_cast<const uint4*>(row_ptr(a.k, row0 + (kb + tid / 16 - T0), a.H, h))[tid % 16];
+    if (tid < (T1 - kb) * 16) {
+      const uint16_t* row = row_ptr(a.k, row0 + (kb + tid / 16 - T0), a.H, h);
+      if constexpr (ROPE) kfirst = rope::turned_chunk(a.rope, row, kb + tid / 16, tid % 16, a.dtype);
+      else kfirst = reinterpret_cast<const uint4*>(row)[tid % 16];
+    }
     if (tid < (T1 - vb) * 16)
       vfirst = reinterpret_cast<const uint4*>(row_ptr(a.v, row0 + (vb + tid / 16 - T0), a.H, h))[tid % 16];
     if (T0 != 0 && stored != T0) {
@@ -927,10 +953,19 @@ __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint
     }
     const int Tk0 = T0 & ~(kG - 1);
     if (Tk0 < T0 && Tk0 + kG <= T1) {   // first key group mixes ring and new rows
+      if constexpr (ROPE) {   // the group's new rows turned into the free tile stage
+        for (int q = tid; q < kG * 16; q += kThreads) {
+          const int t = Tk0 + q / 16;
+          if (t >= T0)
+            reinterpret_cast<uint4*>(rows)[q] =
+                rope::turned_chunk(a.rope, row_ptr(a.k, row0 + (t - T0), a.H, h), t, q % 16, a.dtype);
+        }
+      }
       if (tid < kG) {
         const int t = Tk0 + tid;
-        src[tid] = t < T0 ? kring + static_cast<long long>(t % kG) * kD
-                          : row_ptr(a.k, row0 + (t - T0), a.H, h);
+        src[tid] = t < T0   ? kring + static_cast<long long>(t % kG) * kD
+                   : ROPE   ? reinterpret_cast<const uint16_t*>(rows) + tid * kD
+                            : row_ptr(a.k, row0 + (t - T0), a.H, h);
       }
       __syncthreads();
       key_flush<BITS>(c, h, Tk0 / kG, src, stage);
@@ -985,14 +1020,14 @@ __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint
       }
     }
     __syncthreads();
-    ring_copy(kring, kG, kb, T1, a.k, static_cast<long long>(row0) - T0, a.H, h, kfirst);
-    ring_copy(vring, a.R, vb, T1, a.v, static_cast<long long>(row0) - T0, a.H, h, vfirst);
+    ring_copy<ROPE>(kring, kG, kb, T1, a.k, static_cast<long long>(row0) - T0, a.H, h, kfirst, a.rope, a.dtype);
+    ring_copy(vring, a.R, vb, T1, a.v, static_cast<long long>(row0) - T0, a.H, h, vfirst, a.rope, a.dtype);
     if (tid == 0) *len_word = T1;
     __syncthreads();
   } else {
     const int tile = it.tile;
     const int t0 = tile * 32;
-    if (t0 >= T0 && t0 + kG <= T1) {      // a key group made only of new rows
+    if (!ROPE && t0 >= T0 && t0 + kG <= T1) {      // a key group made only of new rows (with a rotation always a fast tile)
       if (tid < kG) src[tid] = row_ptr(a.k, row0 + (t0 + tid - T0), a.H, h);
       __syncthreads();
       key_flush<BITS>(c, h, tile, src, stage);
@@ -1004,7 +1039,46 @@ __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint
   }
 }
 
-template <int BITS, int DT>
+// The staged key rows of a fast tile (t0: its first token) turned in place: a
+// thread holds a chunk and its partner, reads both, then writes both.
+template <int DT>
+__device__ __forceinline__ void turn_tile(const RopeArgs& r, uint8_t* Ks, int t0) {
+  const int half = r.dim >> 4, units = r.interleaved ? 2 * half : half;   // chunks, or chunk pairs, of a row
+  for (int q = threadIdx.x; q < kG * units; q += kThreads) {
+    const int t = q / units, c = q - t * units, p = rope::partner(r, c);
+    uint4* pc = reinterpret_cast<uint4*>(Ks + sw_off(t, c));
+    uint4* pp = reinterpret_cast<uint4*>(Ks + sw_off(t, p));
+    const uint4 x = *pc, y = *pp;
+    *pc = rope::turn(r, t0 + t, c, x, y, DT);
+    if (p != c) *pp = rope::turn(r, t0 + t, p, y, x, DT);
+  }
+}
+
+// Query rows row0, row0 + step, ... of the call turned (s4kv_append_rope), one warp each.
+__device__ __forceinline__ void turn_queries(const AppendArgs& a, int row0, int step) {
+  const int lane = threadIdx.x & 31;
+  for (int row = row0; row < a.num_new; row += step) {
+    int lo = 0, hi = a.n;   // the last i with cu_new[i] <= row, 32 probes a round
+    while (hi - lo > 1) {
+      const int gap = (hi - lo + 31) / 32, at = lo + gap * (lane + 1);
+      const int k = __ffs(__ballot_sync(0xffffffffu, at >= hi || a.cu_new[at] > row)) - 1;
+      lo += gap * k;
+      hi = min(hi, lo + gap);
+    }
+    const int T0 = a.seq_lens_before[lo], c0 = a.cu_new[lo];
+    if (T0 + a.cu_new[lo + 1] - c0 <= a.rope.max_pos) rope::query_row(a.rope, row, T0 + row - c0, a.dtype);
+  }
+}
+
+// CTAs of a rotating append that turn queries: the last ones of the grid (KIVI and
+// FP8 pages), a warp for every row up to a resident wave.
+__host__ __device__ inline int query_ctas(const AppendArgs& a) {
+  if (!a.rope.q) return 0;
+  const int want = (a.num_new + kThreads / 32 - 1) / (kThreads / 32);
+  return want < 608 ? want : 608;
+}
+
+template <int BITS, int DT, bool ROPE = false>
 __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArgs a) {
   extern __shared__ __align__(128) uint8_t dsm[];
   __shared__ int warp_tot[kThreads / 32];
@@ -1017,12 +1091,21 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArg
   float* prm = reinterpret_cast<float*>(staging + kStagingBytes);
 
   if (!build_prefix(a, pre, warp_tot, seq, cpre)) return;
+  int grid = gridDim.x;   // CTAs that share the items
+  if constexpr (ROPE) {
+    const int nq = query_ctas(a);
+    grid -= nq;
+    if (static_cast<int>(blockIdx.x) >= grid) {
+      turn_queries(a, (blockIdx.x - grid) * (kThreads / 32) + (threadIdx.x >> 5), nq * (kThreads / 32));
+      return;
+    }
+  }
   // A CTA takes the items that start in its slice of the work line, in order;
   // whole new tiles are loaded kNumStages - 1 items ahead (one cp.async group per
   // item, empty for other items).
   const long long C = cpre[a.n];
-  int item = item_from_cost(a, pre, seq, cpre, C * blockIdx.x / gridDim.x);
-  const int total = item_from_cost(a, pre, seq, cpre, C * (blockIdx.x + 1) / gridDim.x);   // this CTA's end
+  int item = item_from_cost(a, pre, seq, cpre, C * blockIdx.x / grid);
+  const int total = item_from_cost(a, pre, seq, cpre, C * (blockIdx.x + 1) / grid);   // this CTA's end
   if (item >= total) return;
   constexpr int kAhead = kNumStages - 1;
   const int step = 1;
@@ -1055,13 +1138,17 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArg
     if (i0.fast) {
       cp_async_wait_prev();
       __syncthreads();
-      fast_tile<BITS, DT>(a, i0, stages + s * kStageBytes, tile_refs[s], staging, prm);
+      if constexpr (ROPE) {
+        if (i0.T1 <= a.rope.max_pos) turn_tile<DT>(a.rope, stages + s * kStageBytes, kG * i0.tile);
+        __syncthreads();
+      }
+      if (!ROPE || i0.T1 <= a.rope.max_pos) fast_tile<BITS, DT>(a, i0, stages + s * kStageBytes, tile_refs[s], staging, prm);
     } else if (ring_item_is_few(a, i0)) {
       __syncthreads();
-      ring_item_few<BITS>(a, i0);
+      ring_item_few<BITS, ROPE>(a, i0);
     } else {
       __syncthreads();
-      other_item<BITS>(a, i0, reinterpret_cast<uint8_t (*)[1536]>(staging), src, stages + s * kStageBytes);
+      other_item<BITS, ROPE>(a, i0, reinterpret_cast<uint8_t (*)[1536]>(staging), src, stages + s * kStageBytes);
     }
     if constexpr (kAhead == 2) {
       i0 = i1;
@@ -1085,13 +1172,23 @@ __device__ __forceinline__ uint32_t e4m3_of(float x, float scale) {
   return static_cast<uint32_t>(__nv_cvt_float_to_fp8(__fdiv_rn(x, scale), __NV_SATFINITE, __NV_E4M3));
 }
 
+template <bool ROPE>
 __global__ void __launch_bounds__(kThreads) append_fp8_kernel(AppendArgs a) {
   extern __shared__ int pre[];   // [n + 1]
   __shared__ int warp_tot[kThreads / 32];
   if (!build_prefix(a, pre, warp_tot)) return;
   const int total = pre[a.n];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+  int grid = gridDim.x;   // CTAs that share the items
+  if constexpr (ROPE) {
+    const int nq = query_ctas(a);
+    grid -= nq;
+    if (static_cast<int>(blockIdx.x) >= grid) {
+      turn_queries(a, (blockIdx.x - grid) * (kThreads / 32) + warp, nq * (kThreads / 32));
+      return;
+    }
+  }
+  for (int item = blockIdx.x; item < total; item += grid) {
     int lo_i = 0, hi_i = a.n - 1;   // last i with pre[i] <= item
     while (lo_i < hi_i) {
       const int mid = (lo_i + hi_i + 1) >> 1;
@@ -1114,6 +1211,10 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(AppendArgs a) {
       if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_TABLE, i);
       continue;
     }
+    if (ROPE && T1 > a.rope.max_pos) {
+      if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_POSITION, i);
+      continue;
+    }
     const int* bt_row = a.block_table + static_cast<long long>(i) * a.bt_stride;
     if (j == 0) {
       int* len_word = a.lens + slot * a.H + h;
@@ -1130,7 +1231,11 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(AppendArgs a) {
     for (int idx = 32 * j + warp; idx < n1; idx += kThreads / 32) {
       const int t = T0 + idx;
       const int pp = bt_row[t / kP];
-      const uint2 kr = *reinterpret_cast<const uint2*>(row_ptr(a.k, row0 + idx, a.H, h) + 4 * lane);
+      uint2 kr = *reinterpret_cast<const uint2*>(row_ptr(a.k, row0 + idx, a.H, h) + 4 * lane);
+      if constexpr (ROPE) {   // lanes 2c and 2c + 1 share chunk c; each keeps its half
+        const uint4 x = rope::turned_chunk(a.rope, row_ptr(a.k, row0 + idx, a.H, h), t, lane >> 1, a.dtype);
+        kr = (lane & 1) ? make_uint2(x.z, x.w) : make_uint2(x.x, x.y);
+      }
       const uint2 vr = *reinterpret_cast<const uint2*>(row_ptr(a.v, row0 + idx, a.H, h) + 4 * lane);
       if (pp < 0 || pp >= a.num_pages) {
         if (lane == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, pp);
@@ -1280,14 +1385,18 @@ cudaError_t launch_append(const AppendArgs& a, int grid, cudaStream_t st) {
   if (a.n > kMaxSeqsPerCall) return cudaErrorInvalidValue;
   if (a.bits == 8) {
     const size_t smem = static_cast<size_t>(a.n + 1) * sizeof(int);
-    const cudaError_t c = prefer_max_shared(reinterpret_cast<const void*>(append_fp8_kernel));
+    void (*f)(AppendArgs) = a.rope.table ? append_fp8_kernel<true> : append_fp8_kernel<false>;
+    const cudaError_t c = prefer_max_shared(reinterpret_cast<const void*>(f));
     if (c != cudaSuccess) return c;
-    append_fp8_kernel<<<grid, kThreads, smem, st>>>(a);
+    f<<<grid + query_ctas(a), kThreads, smem, st>>>(a);
     return cudaGetLastError();
   }
   const int smem = append_smem_bytes(a.n);
   void (*kern)(AppendArgs);
-  if (a.bits == 2) kern = a.dtype == S4KV_BF16 ? append_kernel<2, S4KV_BF16> : append_kernel<2, S4KV_F16>;
+  const bool rope = a.rope.table != nullptr, bf = a.dtype == S4KV_BF16;
+  if (rope && a.bits == 2) kern = bf ? append_kernel<2, S4KV_BF16, true> : append_kernel<2, S4KV_F16, true>;
+  else if (rope) kern = bf ? append_kernel<4, S4KV_BF16, true> : append_kernel<4, S4KV_F16, true>;
+  else if (a.bits == 2) kern = a.dtype == S4KV_BF16 ? append_kernel<2, S4KV_BF16> : append_kernel<2, S4KV_F16>;
   else kern = a.dtype == S4KV_BF16 ? append_kernel<4, S4KV_BF16> : append_kernel<4, S4KV_F16>;
   {
     const cudaError_t c = prefer_max_shared(reinterpret_cast<const void*>(kern));
@@ -1296,10 +1405,10 @@ cudaError_t launch_append(const AppendArgs& a, int grid, cudaStream_t st) {
   if (smem > 48 * 1024) {
     // raise the kernel's dynamic shared memory limit once per device and size
     static std::mutex lock;
-    static int raised[kMaxAppendDevices][4] = {};
+    static int raised[kMaxAppendDevices][8] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxAppendDevices) return cudaErrorInvalidDevice;
-    const int v = (a.bits == 2 ? 2 : 0) + (a.dtype == S4KV_BF16 ? 1 : 0);
+    const int v = (rope ? 4 : 0) + (a.bits == 2 ? 2 : 0) + (a.dtype == S4KV_BF16 ? 1 : 0);
     std::lock_guard<std::mutex> guard(lock);
     if (raised[dev][v] < smem) {
       const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -1307,13 +1416,14 @@ cudaError_t launch_append(const AppendArgs& a, int grid, cudaStream_t st) {
       raised[dev][v] = smem;
     }
   }
-  kern<<<grid, kThreads, smem, st>>>(a);
+  kern<<<grid + query_ctas(a), kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 
 cudaError_t launch_dequant(const DequantArgs& a, cudaStream_t st) {
   if (a.T <= 0) return cudaSuccess;
   dim3 grid((a.T + 7) / 8, a.H);
+  if (a.bits == S4KV_BITS_INT8) return launch_dequant_int8(a, st);
   if (a.bits == 8) dequant_fp8_kernel<<<grid, kThreads, 0, st>>>(a);
   else if (a.bits == 2) dequant_kernel<2><<<grid, kThreads, 0, st>>>(a);
   else dequant_kernel<4><<<grid, kThreads, 0, st>>>(a);

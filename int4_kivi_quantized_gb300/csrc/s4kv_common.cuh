@@ -40,10 +40,24 @@ struct Rec<8> {
   static constexpr int kKc = 0;
   static constexpr int kVc = 2048;
 };
+// INT8 block record (bits = S4KV_BITS_INT8): key codes, value codes (one byte
+// each), the block's key and value scale. 4128 bytes is whole 32-byte sectors.
+template <>
+struct Rec<S4KV_BITS_INT8> {
+  static constexpr int kBytes = 4128;
+  static constexpr int kKc = 0;
+  static constexpr int kVc = 2048;
+  static constexpr int kKs = 4096;
+  static constexpr int kVs = 4100;
+  static constexpr int kCopy = 4112;   // bytes that hold something, whole 16-byte units
+};
 constexpr int kRec = Rec<4>::kBytes;
 constexpr int kKc = Rec<4>::kKc, kKm = Rec<4>::kKm, kVc = Rec<4>::kVc, kVm = Rec<4>::kVm;
 inline int rec_bytes(int bits) {
-  return bits == 2 ? Rec<2>::kBytes : bits == 8 ? Rec<8>::kBytes : Rec<4>::kBytes;
+  return bits == 2                ? Rec<2>::kBytes
+         : bits == 8              ? Rec<8>::kBytes
+         : bits == S4KV_BITS_INT8 ? Rec<S4KV_BITS_INT8>::kBytes
+                                  : Rec<4>::kBytes;
 }
 constexpr int kMaxGroup = 8;     // largest GQA group (query heads per kv head)
 
@@ -65,13 +79,21 @@ struct s4kv_cache {
   int decode_impl;          // 0 tensor-core, 1 FFMA
   int key_split;            // S4KV_OPT_KEY_SPLIT
   int mq_kernel;            // S4KV_OPT_MQ_KERNEL
-  int bits;                 // code width of the pages: 4, 2, or 8 (FP8 E4M3)
+  int bits;                 // page format: 4, 2, 8 (FP8 E4M3) or S4KV_BITS_INT8
   long long wait_ns;
   int num_sms;
   int device;
 };
 
 namespace s4kv {
+
+// Position rotation of an append (s4kv_append_rope); table null: none.
+struct RopeArgs {
+  const float* table;       // [max_pos][dim]: cosines, then sines
+  const uint16_t* q;        // queries to turn, or null
+  uint16_t* q_out;
+  int max_pos, dim, interleaved, Hq;
+};
 
 struct AppendArgs {
   char* pages;              // layer page region
@@ -88,8 +110,30 @@ struct AppendArgs {
   long long kring_slot, kring_head;   // element strides
   long long vring_slot, vring_head;
   int bt_stride, n, num_new, H, R, num_pages, max_slots, dtype;
-  int bits;                 // code width: 4, 2 or 8 (FP8)
+  int bits;                 // code width: 4, 2 or 8 (FP8), or S4KV_BITS_INT8
   const float* fp8_scale;   // FP8: this layer's scales, key [H] then value [H]
+  RopeArgs rope;
+  int step;                 // INT8 pages, decode step: one row per sequence, seq_lens_before holds the
+  int max_len;              // lengths after it, each at most max_len
+};
+
+// Restore of token ranges (s4kv_gather) and, for INT8 pages, of one slot.
+struct GatherArgs {
+  const char* pages;
+  const char* kring;
+  const char* vring;
+  const int* lens;
+  int* status;
+  const int* block_table;
+  const int* seq_lens;
+  const int* slot_ids;
+  const int* first;         // or null: 0
+  const int* cu_rows;
+  void* out_k;
+  void* out_v;
+  const float* fp8_scale;
+  long long kring_slot, kring_head, vring_slot, vring_head;
+  int bt_stride, n, num_rows, H, R, num_pages, max_slots, dtype, out_dtype, bits;
 };
 
 struct DequantArgs {
@@ -142,6 +186,13 @@ struct DecodeArgs {
   unsigned* gbar;           // grid barrier words (arrivals, generation)
 };
 
+// Attention within a window (s4kv_window_attention), and every attention call on
+// INT8 pages (window wider than any sequence, no sinks).
+struct WindowArgs : DecodeArgs {
+  int window, sinks;        // token t is visible at position p: t <= p, t > p - window or t < sinks
+  int tiles;                // column tiles of a (sequence, kv head): nq g columns, pcols each
+};
+
 // Asks for the largest shared-memory carve-out for `func`, once per device and
 // kernel: every kernel of the library then runs with the same L1/shared split, so
 // an SM needs no reconfiguration between back-to-back launches of different
@@ -178,6 +229,12 @@ inline cudaError_t prefer_max_shared(const void* func) {
 cudaError_t launch_append(const AppendArgs& a, int grid, cudaStream_t st);
 int append_ctas_per_sm();   // resident CTAs per SM the append kernel is sized for
 cudaError_t launch_dequant(const DequantArgs& a, cudaStream_t st);
+cudaError_t launch_append_int8(const AppendArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_dequant_int8(const DequantArgs& a, cudaStream_t st);
+cudaError_t launch_gather(const GatherArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_window(const WindowArgs& a, int grid, cudaStream_t st);
+int window_cols(int bits, int cols);      // columns of one warp's tile for a call of `cols` columns
+int window_warps_per_cta();
 cudaError_t launch_decode(const DecodeArgs& a, int impl, int grid, cudaStream_t st);
 // the decode step: a cooperative launch of the decode kernel with the append phase
 cudaError_t launch_decode_step(const DecodeArgs& a, int impl, int grid, cudaStream_t st);

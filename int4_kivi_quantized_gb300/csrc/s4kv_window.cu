@@ -1,0 +1,1292 @@
+// Attention within a sliding window with sinks (s4kv_window_attention), on every
+// page format, and all attention on INT8 block pages (a window wider than any
+// sequence): the last nq tokens of each sequence as queries, nq >= 1.
+//
+// The query at position p sees the tokens t <= p with t > p - W or t < S:
+//   z_t = scale q . k_t,  P = softmax over the visible t,  out = sum_t P_t v_t.
+// Decode attention reads each visible token's record once and does little with
+// it, so the bound is the cache's bytes, and for short windows the latency of one
+// pass through lengths, table, records and the combine.
+//
+// Units of work are blocks (32 tokens of KIVI pages, whose key metadata spans two
+// pages; 16 tokens of the others). A (sequence, kv head, tile of query columns)
+// segment has a list of blocks with a visible token: blocks that every query sees
+// whole (sinks, then the window's inside) come first and run without masks, then
+// the few that the window's start, the last sink, the queries' own positions or
+// the residual cut. All segments' blocks form one line cut into equal slices, one
+// per warp, as in decode attention; split segments leave partials that a second
+// kernel, a programmatic dependent of the first, combines by the log-sum-exp rule.
+// Consecutive slices go to different SMs, so a small call spreads over the GPU.
+//
+//  * 8-bit pages: a warp streams records through a ring of stages (bulk copies,
+//    bounded waits). Scores take the query columns as MMA rows, so what a lane
+//    ends with is the operand of P V. An INT8 code enters an MMA as the f16
+//    subnormal (c + 128) 2^-24, one byte permute for two codes and no arithmetic;
+//    128 times the query's sum comes off the scores, and the P V accumulators
+//    start at -128 2^-24 times the sum of the rounded P (one MMA against a
+//    constant tile), so what a block adds is exact codes times its own fp32 scale.
+//  * KIVI pages: whole blocks run through the decode kernel's group arithmetic,
+//    8 columns a warp; cut blocks and the residual through a masked form of it.
+//
+// A masked token's key and value never meet arithmetic that could carry an
+// infinity or a NaN of theirs into the result: scores are selected, probabilities
+// scaled only where they are positive, 16-bit and FP8 value rows that no column
+// sees read as zeros, and where columns of one tile see different tokens and such
+// a row is not finite, the block is done query by query.
+
+#include "s4kv_kernels.cuh"
+
+namespace s4kv {
+namespace {
+
+constexpr int kI8 = S4KV_BITS_INT8;
+constexpr int kWinWarps = 12;
+constexpr int kStages8 = 3;
+constexpr int kRegion8 = (kStages8 * Rec<kI8>::kBytes + 127) / 128 * 128;   // 12416
+template <int FMT> constexpr bool kByte = FMT == 8 || FMT == kI8;
+template <int FMT> constexpr int kBlock = kByte<FMT> ? kP : kG;             // tokens of a block
+template <int FMT> constexpr int kRegionOf = kByte<FMT> ? kRegion8 : kRegion;
+template <int FMT> constexpr int kMinUnits8 = kByte<FMT> ? 4 : 3;           // least work per warp
+
+template <int FMT>
+struct WSmem {
+  alignas(128) uint8_t region[kWinWarps][kRegionOf<FMT>];
+  alignas(16) float ptile[kByte<FMT> ? 1 : kWinWarps][32 * kPRow];
+  alignas(8) uint64_t bar[kWinWarps][4];
+};
+template <int FMT>
+__host__ __device__ constexpr size_t prefix_at() { return (sizeof(WSmem<FMT>) + 15) / 16 * 16; }
+
+__device__ __forceinline__ bool visible(int t, int pos, int window, int sinks) {
+  return t <= pos && (t > pos - window || t < sinks);
+}
+
+// Visible blocks of a sequence of T tokens: whole ones [0, A0) and [F0, F1), cut
+// ones [A0, A1), [W0, F0) and [F1, E). One plan serves every tile of the sequence.
+struct Plan {
+  int A0, A1, W0, F0, F1, E, nf, nx;
+  long long cost;
+  __device__ __forceinline__ int block_of(int u) const {   // unit u: whole blocks first
+    if (u < A0) return u;
+    if (u < nf) return F0 + u - A0;
+    u -= nf;
+    if (u < A1 - A0) return A0 + u;
+    u -= A1 - A0;
+    if (u < F0 - W0) return W0 + u;
+    return F1 + u - (F0 - W0);
+  }
+};
+
+template <int FMT>
+__device__ __forceinline__ Plan plan_of(int T, const WindowArgs& a) {
+  constexpr int BT = kBlock<FMT>;
+  Plan p;
+  if (T < a.nq || T <= 0) {   // nothing to attend to (T = 0), or a bad length
+    p.A0 = p.A1 = p.W0 = p.F0 = p.F1 = p.E = p.nf = p.nx = 0;
+    p.cost = 1;
+    return p;
+  }
+  // blocks that are quantized whole
+  const int main = FMT == kI8 ? T / BT : FMT == 8 ? T / BT : (min(T & ~(kG - 1), max(0, T - a.R)) / kG);
+  const int first = T - a.nq;                               // position of the first query
+  const int w_first = max(0, first - a.window + 1), w_last = max(0, T - a.window);
+  p.E = (T - 1) / BT + 1;
+  p.W0 = w_first / BT;
+  p.A1 = min((a.sinks + BT - 1) / BT, p.W0);
+  p.A0 = min(min(a.sinks / BT, p.A1), main);
+  p.F0 = (w_last + BT - 1) / BT;
+  p.F1 = min(main, (first + 1) / BT);
+  if (p.F0 >= p.F1) p.F0 = p.F1 = p.W0;
+  p.nf = p.A0 + p.F1 - p.F0;
+  p.nx = (p.A1 - p.A0) + (p.F0 - p.W0) + (p.E - p.F1);
+  p.cost = p.nf + static_cast<long long>(kByte<FMT> ? 1 : a.tail_cost) * p.nx;
+  return p;
+}
+
+__device__ __forceinline__ void mma16816_c(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                           const float (&c)[4]) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+// ---- 8-bit pages -------------------------------------------------------------------------
+
+// State of a warp's NC columns: column 8 ct + gi is row r = ct of m and l (this
+// lane's part of the sum); o[mt][ct] holds columns 8 ct + 2ti, + 2ti + 1 of the
+// channels that rows gi and gi + 8 of tile mt stand for.
+template <int NC>
+struct ByteState {
+  static constexpr int CT = NC / 8;
+  float o[8][CT][4];
+  float m[CT], l[CT];
+};
+
+template <int NC>
+__device__ __forceinline__ void byte_init(ByteState<NC>& s) {
+#pragma unroll
+  for (int c = 0; c < NC / 8; ++c) {
+    s.m[c] = -INFINITY;
+    s.l[c] = 0.0f;
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s.o[mt][c][e] = 0.0f;
+  }
+}
+
+// Online softmax over 16 tokens: z[ct][x], x = tokens 2ti, 2ti+1, 2ti+8, 2ti+9 of
+// the block (-inf: masked), becomes p; accumulators are rescaled when a maximum
+// rises by more than kLazy. kMask: a column may have seen nothing so far.
+template <int NC, bool kMask>
+__device__ __forceinline__ void byte_softmax(ByteState<NC>& s, float (&z)[NC / 8][4]) {
+  constexpr int CT = NC / 8;
+  const int ti = threadIdx.x & 3;
+  float mx[CT];
+  bool up = false;
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    mx[c] = fmaxf(fmaxf(z[c][0], z[c][1]), fmaxf(z[c][2], z[c][3]));
+    mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 1));
+    mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 2));
+    up = up || mx[c] > s.m[c] + kLazy;
+  }
+  if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      const float mn = fmaxf(s.m[c], mx[c]);
+      const float al = mn == -INFINITY ? 1.0f : ex2(s.m[c] - mn);
+      s.m[c] = mn;
+      s.l[c] *= al;
+      // output columns 8c + 2ti and + 1 keep their state in lanes 8ti and 8ti + 4
+      const float a0 = __shfl_sync(0xffffffffu, al, 8 * ti), a1 = __shfl_sync(0xffffffffu, al, 8 * ti + 4);
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        s.o[mt][c][0] *= a0;
+        s.o[mt][c][1] *= a1;
+        s.o[mt][c][2] *= a0;
+        s.o[mt][c][3] *= a1;
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) z[c][x] = kMask && z[c][x] == -INFINITY ? 0.0f : ex2(z[c][x] - s.m[c]);
+    s.l[c] += (z[c][0] + z[c][1]) + (z[c][2] + z[c][3]);
+  }
+}
+
+// What a masked block needs to know: the lane's columns' positions in the score
+// layout (row 8 ct + gi), the tile's first and last query position.
+struct Cut {
+  int tok0, window, sinks, first, last;
+};
+
+// Adds a product to the accumulator columns of one position only (columns 2ti and
+// 2ti + 1 have positions opos): where a value row is not finite, the other
+// columns' zeros would meet it.
+template <class F>
+__device__ __forceinline__ void add_only(float (&o)[4], const int (&opos)[2], int only, F product) {
+  float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  product(t);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = opos[e & 1] == only ? o[e] + t[e] : o[e];
+}
+
+// One staged record of 16 tokens. Keys: lane (gi, ti) reads its words as the B
+// operand of tokens gi and gi + 8; q as A. qa: f16 queries, rows gi (and gi + 8);
+// zoff[ct] = -128 scale sum_c q_c (INT8). scale = sm_scale log2(e) (times the
+// key scale on FP8). kMask: tokens are masked by `cut` and the columns' positions.
+template <int FMT, int NC, bool kMask>
+__device__ __forceinline__ void byte_block(const char* rec, ByteState<NC>& s, const uint32_t (&qa)[8][NC / 4],
+                                           const float (&zoff)[NC / 8], float scale, const Cut& cut,
+                                           const int (&pos)[NC / 8], const int (&opos)[NC / 8][2]) {
+  constexpr int CT = NC / 8;
+  const int lane = threadIdx.x & 31, ti = lane & 3;
+  float z[CT][4];
+  float vscale = 1.0f;
+  {
+    float s0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kp = 0; kp < 4; ++kp) {
+      const uint4 w = *reinterpret_cast<const uint4*>(rec + kp * 512 + lane * 16);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t w0 = u ? w.z : w.x, w1 = u ? w.w : w.y;
+        const int kk = 2 * kp + u;
+        const uint32_t a[4] = {qa[kk][0], NC == 16 ? qa[kk][NC / 8 - 1] : 0u, qa[kk][NC / 8], NC == 16 ? qa[kk][NC / 4 - 1] : 0u};
+        if constexpr (FMT == kI8) {
+          mma16816(s0, a, __byte_perm(w0, 0u, 0x4140), __byte_perm(w1, 0u, 0x4140));
+          mma16816(s1, a, __byte_perm(w0, 0u, 0x4342), __byte_perm(w1, 0u, 0x4342));
+        } else {
+          mma16816(s0, a, fp8x2_to_f16x2(w0 & 0xffffu), fp8x2_to_f16x2(w1 & 0xffffu));
+          mma16816(s1, a, fp8x2_to_f16x2(w0 >> 16), fp8x2_to_f16x2(w1 >> 16));
+        }
+      }
+    }
+    if constexpr (FMT == kI8) {
+      const float2 sc = *reinterpret_cast<const float2*>(rec + Rec<kI8>::kKs);
+      vscale = sc.y;
+      const float c1 = sc.x * (scale * 16777216.0f);
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const float c2 = sc.x * zoff[c];
+        z[c][0] = fmaf(s0[2 * c], c1, c2);
+        z[c][1] = fmaf(s0[2 * c + 1], c1, c2);
+        z[c][2] = fmaf(s1[2 * c], c1, c2);
+        z[c][3] = fmaf(s1[2 * c + 1], c1, c2);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        z[c][0] = s0[2 * c] * scale;
+        z[c][1] = s0[2 * c + 1] * scale;
+        z[c][2] = s1[2 * c] * scale;
+        z[c][3] = s1[2 * c + 1] * scale;
+      }
+    }
+  }
+  if (kMask) {
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int t = cut.tok0 + 2 * ti + (x & 1) + 8 * (x >> 1);
+        z[c][x] = visible(t, pos[c], cut.window, cut.sinks) ? z[c][x] : -INFINITY;
+      }
+  }
+  byte_softmax<NC, kMask>(s, z);
+  uint32_t b[CT][2];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    b[c][0] = pack_f16x2(z[c][0], z[c][1]);
+    b[c][1] = pack_f16x2(z[c][2], z[c][3]);
+  }
+  if constexpr (FMT == kI8) {
+    float bias[CT][4], f[CT][2];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      // -2^-17 = -128 2^-24 in every element (f16 subnormal 0x8080)
+      const uint32_t k[4] = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
+      const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      mma16816_c(bias[c], k, b[c][0], b[c][1], zero);
+      const float vs = vscale * 16777216.0f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        bool any = true;
+        if (kMask) any = cut.tok0 <= opos[c][e] && (cut.tok0 + kP - 1 > opos[c][e] - cut.window || cut.tok0 < cut.sinks);
+        f[c][e] = any ? vs : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int kp = 0; kp < 4; ++kp) {
+      const uint4 w = *reinterpret_cast<const uint4*>(rec + 2048 + kp * 512 + lane * 16);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t w0 = u ? w.z : w.x, w1 = u ? w.w : w.y;
+        const uint32_t a[4] = {__byte_perm(w0, 0u, 0x4140), __byte_perm(w0, 0u, 0x4342), __byte_perm(w1, 0u, 0x4140),
+                               __byte_perm(w1, 0u, 0x4342)};
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          float t[4];
+          mma16816_c(t, a, b[c][0], b[c][1], bias[c]);
+          float(&o)[4] = s.o[2 * kp + u][c];
+          o[0] = fmaf(t[0], f[c][0], o[0]);
+          o[1] = fmaf(t[1], f[c][1], o[1]);
+          o[2] = fmaf(t[2], f[c][0], o[2]);
+          o[3] = fmaf(t[3], f[c][1], o[3]);
+        }
+      }
+    }
+  } else {
+    uint4 vw[4];
+#pragma unroll
+    for (int kp = 0; kp < 4; ++kp) vw[kp] = *reinterpret_cast<const uint4*>(rec + 2048 + kp * 512 + lane * 16);
+    // only: the position whose columns take the product, -1 for all
+    auto pv = [&](uint32_t m01, uint32_t m23, int only) {
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        const uint32_t w0 = (mt & 1) ? vw[mt >> 1].z : vw[mt >> 1].x, w1 = (mt & 1) ? vw[mt >> 1].w : vw[mt >> 1].y;
+        uint32_t a[4] = {fp8x2_to_f16x2(w0 & 0xffffu), fp8x2_to_f16x2(w0 >> 16), fp8x2_to_f16x2(w1 & 0xffffu),
+                         fp8x2_to_f16x2(w1 >> 16)};
+        if (kMask) {
+          a[0] &= m01;
+          a[1] &= m01;
+          a[2] &= m23;
+          a[3] &= m23;
+        }
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          if (!kMask || only < 0) mma16816(s.o[mt][c], a, b[c][0], b[c][1]);
+          else add_only(s.o[mt][c], opos[c], only, [&](float (&t)[4]) { mma16816(t, a, b[c][0], b[c][1]); });
+        }
+      }
+    };
+    if constexpr (!kMask) {
+      pv(0xffffffffu, 0xffffffffu, -1);
+    } else {
+      // halves of the tokens 2ti, 2ti+1 | 2ti+8, 2ti+9 that a query at one of the
+      // positions [lo, hi] sees
+      auto halves = [&](int lo, int hi, uint32_t& m01, uint32_t& m23) {
+        uint32_t m[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int t = cut.tok0 + 2 * ti + (x & 1) + 8 * (x >> 1);
+          m[x] = t <= hi && (t > lo - cut.window || t < cut.sinks) ? 0xffffu : 0u;
+        }
+        m01 = m[0] | (m[1] << 16);
+        m23 = m[2] | (m[3] << 16);
+      };
+      bool nan = false;   // an e4m3 NaN byte
+      if (cut.first != cut.last) {
+#pragma unroll
+        for (int kp = 0; kp < 4; ++kp) {
+          const uint32_t w[4] = {vw[kp].x, vw[kp].y, vw[kp].z, vw[kp].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) nan = nan || (((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u);
+        }
+      }
+      if (!__any_sync(0xffffffffu, nan)) {
+        uint32_t m01, m23;
+        halves(cut.first, cut.last, m01, m23);
+        pv(m01, m23, -1);
+      } else {
+        for (int q = cut.first; q <= cut.last; ++q) {
+          uint32_t m01, m23;
+          halves(q, q, m01, m23);
+          pv(m01, m23, q);
+        }
+      }
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void mma_in(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (DT == S4KV_BF16) mma16816_bf16(d, a, b0, b1);
+  else mma16816(d, a, b0, b1);
+}
+template <int DT>
+__device__ __forceinline__ uint32_t pack_in(float lo, float hi) {
+  if constexpr (DT == S4KV_BF16) return pack_bf16x2(lo, hi);
+  else return pack_f16x2(lo, hi);
+}
+template <int DT>
+__device__ __forceinline__ float2 unpack_in(uint32_t w) {
+  if constexpr (DT == S4KV_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  else return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+// Whether a packed 16-bit pair holds an infinity or a NaN.
+template <int DT>
+__device__ __forceinline__ bool wild(uint32_t w) {
+  constexpr uint32_t e = DT == S4KV_BF16 ? 0x7f80u : 0x7c00u;
+  return (w & e) == e || (w & (e << 16)) == (e << 16);
+}
+
+// The unfinished block of INT8 pages: n tokens from tok0 on, 16-bit rows of the
+// rings, read from global memory straight into operands (exact products with the
+// query in its own type, P split into two 16-bit terms).
+template <int DT, int NC>
+__device__ __forceinline__ void ring_block(const uint16_t* kring, const uint16_t* vring, int n, ByteState<NC>& s,
+                                           const uint16_t* (&qrow)[NC / 8], float scale, const Cut& cut,
+                                           const int (&pos)[NC / 8], const int (&opos)[NC / 8][2]) {
+  constexpr int CT = NC / 8;
+  const int lane = threadIdx.x & 31, gi = lane >> 2, ti = lane & 3;
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  uint4 v[4][2];
+  bool part = false;   // a row some columns see and others do not, that is not finite
+#pragma unroll
+  for (int x = 0; x < 4; ++x) {
+    const int t = 2 * ti + (x & 1) + 8 * (x >> 1), at = cut.tok0 + t;
+    const bool any = t < n && at <= cut.last && (at > cut.first - cut.window || at < cut.sinks);
+    const uint4* row = reinterpret_cast<const uint4*>(vring + t * kD);
+    v[x][0] = any ? row[gi] : none;
+    v[x][1] = any ? row[gi + 8] : none;
+  }
+  float z[CT][4];
+  {
+    float s0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {   // channels 32 ti + 8 j .. + 7
+      const uint4 k0 = gi < n ? reinterpret_cast<const uint4*>(kring + gi * kD)[4 * ti + j] : none;
+      const uint4 k1 = gi + 8 < n ? reinterpret_cast<const uint4*>(kring + (gi + 8) * kD)[4 * ti + j] : none;
+      uint4 q[2] = {none, none};
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+        if (qrow[c]) q[c] = reinterpret_cast<const uint4*>(qrow[c])[4 * ti + j];
+      const uint32_t a0[4] = {q[0].x, q[1].x, q[0].y, q[1].y}, a1[4] = {q[0].z, q[1].z, q[0].w, q[1].w};
+      mma_in<DT>(s0, a0, k0.x, k0.y);
+      mma_in<DT>(s0, a1, k0.z, k0.w);
+      mma_in<DT>(s1, a0, k1.x, k1.y);
+      mma_in<DT>(s1, a1, k1.z, k1.w);
+    }
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      z[c][0] = s0[2 * c] * scale;
+      z[c][1] = s0[2 * c + 1] * scale;
+      z[c][2] = s1[2 * c] * scale;
+      z[c][3] = s1[2 * c + 1] * scale;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int t = cut.tok0 + 2 * ti + (x & 1) + 8 * (x >> 1);
+        z[c][x] = visible(t, pos[c], cut.window, cut.sinks) ? z[c][x] : -INFINITY;
+      }
+    }
+  }
+  byte_softmax<NC, true>(s, z);
+  uint32_t hi[CT][2], lo[CT][2];
+#pragma unroll
+  for (int c = 0; c < CT; ++c)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      hi[c][e] = pack_in<DT>(z[c][2 * e], z[c][2 * e + 1]);
+      const float2 r = unpack_in<DT>(hi[c][e]);
+      lo[c][e] = pack_in<DT>(z[c][2 * e] - r.x, z[c][2 * e + 1] - r.y);
+    }
+  if (cut.first != cut.last) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        part = part || wild<DT>(v[x][e].x) || wild<DT>(v[x][e].y) || wild<DT>(v[x][e].z) || wild<DT>(v[x][e].w);
+  }
+  auto pv = [&](const bool (&keep)[4], int only) {   // only: as in byte_block
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      const uint32_t sel = (mt & 1) ? 0x7632u : 0x5410u;
+      uint32_t w[4][2];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint4& y = v[x][e];
+          const uint32_t u = (mt >> 1) == 0 ? y.x : (mt >> 1) == 1 ? y.y : (mt >> 1) == 2 ? y.z : y.w;
+          w[x][e] = keep[x] ? u : 0u;
+        }
+      const uint32_t a[4] = {__byte_perm(w[0][0], w[1][0], sel), __byte_perm(w[0][1], w[1][1], sel),
+                             __byte_perm(w[2][0], w[3][0], sel), __byte_perm(w[2][1], w[3][1], sel)};
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        auto product = [&](float (&t)[4]) {
+          mma_in<DT>(t, a, hi[c][0], hi[c][1]);
+          mma_in<DT>(t, a, lo[c][0], lo[c][1]);
+        };
+        if (only < 0) product(s.o[mt][c]);
+        else add_only(s.o[mt][c], opos[c], only, product);
+      }
+    }
+  };
+  if (!__any_sync(0xffffffffu, part)) {
+    const bool all[4] = {true, true, true, true};
+    pv(all, -1);
+  } else {
+    for (int q = cut.first; q <= cut.last; ++q) {
+      bool keep[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        keep[x] = visible(cut.tok0 + 2 * ti + (x & 1) + 8 * (x >> 1), q, cut.window, cut.sinks);
+      pv(keep, q);
+    }
+  }
+}
+
+// ---- KIVI pages: a block that is cut, or that the residual reaches into ------------------
+// As the decode kernel's tail: keys from the staged records (whole groups) or the
+// key-ring rows at `kring`, values below Tv from the records, later ones from the
+// value-ring rows staged token-major at vrows. pos0, pos1: positions of columns
+// 2ti and 2ti + 1.
+template <int BITS>
+__device__ void kivi_cut_block(const Seg& sg, MmaState& s, float* ptile, const float (&q)[32], const char* recs,
+                               const uint16_t* kring, const char* vrows, uint32_t zero_s, float scale, const Cut& cut,
+                               int pos0, int pos1) {
+  using F = Rec<BITS>;
+  constexpr int RS = kRecStrideB<BITS>;
+  const int lane = threadIdx.x & 31, gi = lane >> 2, ti = lane & 3;
+  const int t0 = cut.tok0, n = min(kG, sg.T - t0), t1 = t0 + n;
+  float acc0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, acc1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float beta = 0.0f;
+  if (t0 + kG <= sg.Tk) beta = kscores_quant<true, BITS>(recs, q, acc0, acc1, kLoAbove / scale);
+  else kscores_ring(kring, n, q, sg.dtype, acc0, acc1);
+  const float bs0 = __shfl_sync(0xffffffffu, beta, 8 * ti) * scale, bs1 = __shfl_sync(0xffffffffu, beta, 8 * ti + 4) * scale;
+  float z[8];   // tokens gi, gi + 8, 16 + gi, 24 + gi of columns 2ti (even entries) and 2ti + 1
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const float* acc = p ? acc1 : acc0;
+    const int ta = t0 + 16 * p + gi, tb = ta + 8;
+    z[4 * p + 0] = visible(ta, pos0, cut.window, cut.sinks) ? fmaf(acc[0], scale, bs0) : -INFINITY;
+    z[4 * p + 1] = visible(ta, pos1, cut.window, cut.sinks) ? fmaf(acc[1], scale, bs1) : -INFINITY;
+    z[4 * p + 2] = visible(tb, pos0, cut.window, cut.sinks) ? fmaf(acc[2], scale, bs0) : -INFINITY;
+    z[4 * p + 3] = visible(tb, pos1, cut.window, cut.sinks) ? fmaf(acc[3], scale, bs1) : -INFINITY;
+  }
+  float mx0 = fmaxf(fmaxf(z[0], z[2]), fmaxf(z[4], z[6])), mx1 = fmaxf(fmaxf(z[1], z[3]), fmaxf(z[5], z[7]));
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) {
+    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
+  }
+  if (__any_sync(0xffffffffu, mx0 > s.m0 + kLazy || mx1 > s.m1 + kLazy)) {
+    const float mn0 = fmaxf(s.m0, mx0), mn1 = fmaxf(s.m1, mx1);
+    const float al0 = mn0 == -INFINITY ? 1.0f : ex2(s.m0 - mn0), al1 = mn1 == -INFINITY ? 1.0f : ex2(s.m1 - mn1);
+    s.m0 = mn0;
+    s.m1 = mn1;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s.o[i][0] *= al0;
+      s.o[i][1] *= al1;
+      s.o[i][2] *= al0;
+      s.o[i][3] *= al1;
+    }
+    s.l0 *= al0;
+    s.l1 *= al1;
+    // bias belongs to column gi: its factor sits in lanes with ti = gi / 2
+    const float a_even = __shfl_sync(0xffffffffu, al0, gi >> 1), a_odd = __shfl_sync(0xffffffffu, al1, gi >> 1);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s.bias[k] *= (gi & 1) ? a_odd : a_even;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) z[i] = z[i] == -INFINITY ? 0.0f : ex2(z[i] - ((i & 1) ? s.m1 : s.m0));
+  s.l0 += (z[0] + z[2]) + (z[4] + z[6]);
+  s.l1 += (z[1] + z[3]) + (z[5] + z[7]);
+#pragma unroll
+  for (int r = 0; r < 4; ++r) *reinterpret_cast<float2*>(ptile + (8 * r + gi) * kPRow + 2 * ti) = make_float2(z[2 * r], z[2 * r + 1]);
+  __syncwarp();
+  const int vt0 = max(t0, sg.Tv);
+  // a value-ring row that only some columns see and that is not finite (lane = row)
+  bool wildrow = false;
+  if (cut.first != cut.last && lane < n && t0 + lane >= vt0) {
+    const uint4* row = reinterpret_cast<const uint4*>(vrows + lane * kVRow);
+    for (int c = 0; c < 16; ++c) {
+      const uint4 w = row[c];
+      if (sg.dtype == S4KV_BF16)
+        wildrow = wildrow || wild<S4KV_BF16>(w.x) || wild<S4KV_BF16>(w.y) || wild<S4KV_BF16>(w.z) || wild<S4KV_BF16>(w.w);
+      else
+        wildrow = wildrow || wild<S4KV_F16>(w.x) || wild<S4KV_F16>(w.y) || wild<S4KV_F16>(w.z) || wild<S4KV_F16>(w.w);
+    }
+  }
+  const bool apart = __any_sync(0xffffffffu, wildrow);
+#pragma unroll 1
+  for (int p = 0; p < 2; ++p) {
+    const int tb = t0 + 16 * p;
+    if (tb >= t1) break;
+    // p of tokens 2ti, 2ti+1, 2ti+8, 2ti+9 of this page, column gi
+    float pe[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) pe[x] = ptile[(16 * p + 2 * ti + (x & 1) + 8 * (x >> 1)) * kPRow + gi];
+    if (tb < sg.Tv) {   // restored values: tokens tb .. Tv - 1 of this page
+      const char* rec = recs + p * RS;
+      const int nq = sg.Tv - tb;
+      bool on[4];       // masked tokens (p = 0) stay out: their scale may be anything
+#pragma unroll
+      for (int x = 0; x < 4; ++x) on[x] = 2 * ti + (x & 1) + 8 * (x >> 1) < nq && pe[x] > 0.0f;
+      uint32_t b0[4], b1[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 s4 = *reinterpret_cast<const float4*>(rec + F::kVm + ((2 * k) * 4 + ti) * 16);
+        const float4 m4 = *reinterpret_cast<const float4*>(rec + F::kVm + ((2 * k + 1) * 4 + ti) * 16);
+        b0[k] = pack_f16x2(on[0] ? pe[0] * s4.x : 0.0f, on[1] ? pe[1] * s4.y : 0.0f);
+        b1[k] = pack_f16x2(on[2] ? pe[2] * s4.z : 0.0f, on[3] ? pe[3] * s4.w : 0.0f);
+        float bk = s.bias[k];
+        bk = on[0] ? fmaf(pe[0], m4.x, bk) : bk;
+        bk = on[1] ? fmaf(pe[1], m4.y, bk) : bk;
+        bk = on[2] ? fmaf(pe[2], m4.z, bk) : bk;
+        bk = on[3] ? fmaf(pe[3], m4.w, bk) : bk;
+        s.bias[k] = bk;
+      }
+      uint32_t vd[8];
+      {
+        const uint4 v0 = *reinterpret_cast<const uint4*>(rec + F::kVc + lane * 16);
+        vd[0] = v0.x; vd[1] = v0.y; vd[2] = v0.z; vd[3] = v0.w;
+        if constexpr (BITS == 4) {
+          const uint4 v1 = *reinterpret_cast<const uint4*>(rec + F::kVc + 512 + lane * 16);
+          vd[4] = v1.x; vd[5] = v1.y; vd[6] = v1.z; vd[7] = v1.w;
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt) {
+        uint32_t a[4];
+        if constexpr (BITS == 4) unpack8(vd[mt], a);
+        else unpack_crumbs(vd[mt >> 1], mt & 1, a);
+        mma16816(s.o[mt], a, b0[mt >> 1], b1[mt >> 1]);
+      }
+    }
+    if (tb + kP > vt0) {   // value-ring rows of this page
+      // this lane's ldmatrix row: matrix j = lane / 8 (tokens + 8 for j >= 2,
+      // channels + 8 for odd j), row lane % 8
+      const int j = lane >> 3;
+      const int row = 16 * p + (lane & 7) + 8 * (j >> 1), t = t0 + row;
+      const bool there = t >= vt0 && t < t1;
+      const int opos[2] = {pos0, pos1};
+      auto pv = [&](bool present, const float (&y)[4], int only) {   // only: as in byte_block
+        const uint32_t base = present ? smem_u32(vrows + row * kVRow + 16 * (j & 1)) : zero_s;
+        const uint32_t step = present ? 32u : 0u;   // 16 channels further per tile
+        if (sg.dtype == S4KV_BF16) {
+          const uint32_t h0 = pack_bf16x2(y[0], y[1]), h1 = pack_bf16x2(y[2], y[3]);
+          const uint32_t l0 = pack_bf16x2(y[0] - __uint_as_float(h0 << 16), y[1] - __uint_as_float(h0 & 0xffff0000u));
+          const uint32_t l1 = pack_bf16x2(y[2] - __uint_as_float(h1 << 16), y[3] - __uint_as_float(h1 & 0xffff0000u));
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) {
+            uint32_t a[4];
+            ldsm_x4_trans(base + mt * step, a);
+            auto product = [&](float (&t)[4]) {
+              mma16816_bf16(t, a, h0, h1);
+              mma16816_bf16(t, a, l0, l1);
+            };
+            if (only < 0) product(s.o[mt]);
+            else add_only(s.o[mt], opos, only, product);
+          }
+        } else {
+          const uint32_t h0 = pack_f16x2(y[0], y[1]), h1 = pack_f16x2(y[2], y[3]);
+          const float2 f0 = unpack_in<S4KV_F16>(h0), f1 = unpack_in<S4KV_F16>(h1);
+          const uint32_t l0 = pack_f16x2(y[0] - f0.x, y[1] - f0.y), l1 = pack_f16x2(y[2] - f1.x, y[3] - f1.y);
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) {
+            uint32_t a[4];
+            ldsm_x4_trans(base + mt * step, a);
+            auto product = [&](float (&t)[4]) {
+              mma16816(t, a, h0, h1);
+              mma16816(t, a, l0, l1);
+            };
+            if (only < 0) product(s.o[mt]);
+            else add_only(s.o[mt], opos, only, product);
+          }
+        }
+      };
+      // quantized tokens of this page already entered through their records
+      float y[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) y[x] = tb + 2 * ti + (x & 1) + 8 * (x >> 1) >= vt0 ? pe[x] : 0.0f;
+      if (!apart) {
+        pv(there && t <= cut.last && (t > cut.first - cut.window || t < cut.sinks), y, -1);
+      } else {
+        for (int qp = cut.first; qp <= cut.last; ++qp) pv(there && visible(t, qp, cut.window, cut.sinks), y, qp);
+      }
+    }
+  }
+  __syncwarp();
+}
+
+// ---- the kernel ----------------------------------------------------------------------------
+__device__ __forceinline__ long long* win_meta(const WindowArgs& a) {
+  return reinterpret_cast<long long*>(a.ws + 2LL * a.grid_warps * partial_floats(a.pcols));
+}
+
+// Eight consecutive channels from c on of one output row.
+__device__ __forceinline__ void store8(const WindowArgs& a, long long row, int c, const float (&y)[8]) {
+  const long long idx = row * kD + c;
+  if (a.out_dtype == S4KV_F32) {
+    float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + idx);
+    p[0] = make_float4(y[0], y[1], y[2], y[3]);
+    p[1] = make_float4(y[4], y[5], y[6], y[7]);
+  } else {
+    uint4 w;
+    w.x = pack_in_dtype(y[0], y[1], a.out_dtype);
+    w.y = pack_in_dtype(y[2], y[3], a.out_dtype);
+    w.z = pack_in_dtype(y[4], y[5], a.out_dtype);
+    w.w = pack_in_dtype(y[6], y[7], a.out_dtype);
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + idx) = w;
+  }
+}
+__device__ __forceinline__ void store1(const WindowArgs& a, long long row, int c, float y) {
+  const long long idx = row * kD + c;
+  if (a.out_dtype == S4KV_F32) reinterpret_cast<float*>(a.out)[idx] = y;
+  else if (a.out_dtype == S4KV_BF16) reinterpret_cast<__nv_bfloat16*>(a.out)[idx] = __float2bfloat16_rn(y);
+  else reinterpret_cast<__half*>(a.out)[idx] = __float2half_rn(y);
+}
+
+// FMT: page format. NC: columns a warp holds (8, or 16 on 8-bit pages). PACKED
+// (KIVI, at most 4 columns): the query's low f16 part rides in columns 4..7.
+template <int FMT, int NC, bool PACKED>
+__global__ void __launch_bounds__(32 * kWinWarps, 1) window_kernel(WindowArgs a) {
+  constexpr int BT = kBlock<FMT>;
+  constexpr int CT = NC / 8;
+  constexpr int kThreads = 32 * kWinWarps;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  auto& sm = *reinterpret_cast<WSmem<FMT>*>(smem_raw);
+  long long* pre = reinterpret_cast<long long*>(smem_raw + prefix_at<FMT>());   // [B + 1]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, ti = lane & 3;
+  uint8_t* region = sm.region[warp];
+  uint64_t* bar = sm.bar[warp];
+  if (lane == 0)
+    for (int i = 0; i < 4; ++i) mbar_init(&bar[i], 1);
+  asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  __shared__ __align__(16) uint4 zero16;
+  if (tid == 0) zero16 = make_uint4(0u, 0u, 0u, 0u);
+  {   // cost prefix over sequences: sequence b owns H tiles segments of its plan's cost
+    long long carry = 0;
+    __shared__ long long wt[kWinWarps];
+    for (int base = 0; base < a.B; base += kThreads) {
+      const int b = base + tid;
+      const long long cnt = b < a.B ? static_cast<long long>(a.H) * a.tiles * plan_of<FMT>(a.seq_lens[b], a).cost : 0;
+      long long x = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (lane == 31) wt[warp] = x;
+      __syncthreads();
+      long long before = carry, total = 0;
+      for (int q = 0; q < kWinWarps; ++q) {
+        if (q < warp) before += wt[q];
+        total += wt[q];
+      }
+      if (b < a.B) pre[b] = before + x - cnt;
+      __syncthreads();
+      carry += total;
+    }
+    if (tid == 0) pre[a.B] = carry;
+    __syncthreads();
+  }
+  const long long C = pre[a.B];
+  int n_act = static_cast<int>(gridDim.x) * kWinWarps;
+  if (a.max_warps > 0 && a.max_warps < n_act) n_act = a.max_warps;
+  {
+    const long long cap = (C + kMinUnits8<FMT> - 1) / kMinUnits8<FMT>;
+    if (cap < n_act) n_act = static_cast<int>(cap);
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int gw = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+  if (gw >= n_act) return;
+  const long long r0 = gw * C / n_act, r1 = (gw + 1) * C / n_act;
+
+  uint32_t phase = 0, pend = 0;   // per-stage wait parity and copies in flight (bit per stage)
+  const uint64_t once = policy_evict_first();
+  bool aborted = false;
+  auto wait = [&](int s) -> bool {
+    if (!mbar_wait(&bar[s], (phase >> s) & 1u, aborted ? 0 : a.wait_ns)) return false;
+    phase ^= 1u << s;
+    pend &= ~(1u << s);
+    return true;
+  };
+  auto fail = [&](int where) {   // a bounded wait ran out: drain, then go on without compute
+    if (lane == 0) report(a.status, S4KV_ERR_DEVICE_TIMEOUT, S4KV_DEV_TIMEOUT, where);
+    aborted = true;
+    for (int s = 0; s < 4; ++s)
+      if ((pend >> s) & 1u) {
+        mbar_wait(&bar[s], (phase >> s) & 1u, kDrainNs);
+        phase ^= 1u << s;
+        pend &= ~(1u << s);
+      }
+  };
+
+  int b;
+  {   // first sequence touching this slice
+    int lo = 0, hi = a.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= r0) lo = mid; else hi = mid - 1;
+    }
+    b = lo;
+  }
+  int T = a.seq_lens[b];
+  Plan pl = plan_of<FMT>(T, a);
+  int seg = static_cast<int>((r0 - pre[b]) / pl.cost);   // h * tiles + tile, within the sequence
+  long long seg_start = pre[b] + seg * pl.cost;
+  const int ncols = a.nq * a.g;
+
+  while (seg_start < r1) {
+    const long long seg_end = seg_start + pl.cost;
+    const long long lo = max(r0, seg_start) - seg_start, hi = min(r1, seg_end) - seg_start;
+    const bool own = lo == 0 && hi == pl.cost;
+    const int h = seg / a.tiles, col0 = (seg - h * a.tiles) * NC;
+    const int slot = a.slot_ids ? a.slot_ids[b] : b;
+    const bool slot_ok = slot >= 0 && slot < a.max_slots;
+    const int lens_v = slot_ok ? __ldcg(a.lens + slot * a.H + h) : 0;
+    // positions: of a column past the last one, the last query's
+    auto pos_of = [&](int col) { return T - a.nq + min(col, ncols - 1) / a.g; };
+    auto qrow_of = [&](int col) -> const uint16_t* {
+      if (col >= ncols) return nullptr;
+      const int i = col / a.g;
+      return a.q + ((static_cast<long long>(b) * a.nq + i) * a.Hq + h * a.g + (col - i * a.g)) * kD;
+    };
+    auto out_row = [&](int col) -> long long {
+      const int i = col / a.g;
+      return (static_cast<long long>(b) * a.nq + i) * a.Hq + h * a.g + (col - i * a.g);
+    };
+    Cut cut;
+    cut.tok0 = 0;
+    cut.window = a.window;
+    cut.sinks = a.sinks;
+    cut.first = pos_of(col0);
+    cut.last = pos_of(min(col0 + NC, ncols) - 1);
+    bool valid = slot_ok && T > 0;
+    if (!slot_ok) {
+      if (lane == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_SLOT, slot);
+    } else if (lens_v != T || T > a.max_seq_len || (T > 0 && T < a.nq)) {
+      valid = false;
+      if (lane == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_LENGTH, b);
+    } else if (static_cast<long long>(a.bt_stride) * kP < T) {
+      valid = false;
+      if (lane == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_TABLE, b);
+    }
+    valid = valid && !aborted;
+    const int* bt = a.block_table + static_cast<long long>(b) * a.bt_stride;
+    auto page = [&](int lp) -> int {   // pool page of logical page lp, -1 (reported) if outside the pool
+      const int pp = bt[lp];
+      if (pp >= 0 && pp < a.num_pages) return pp;
+      report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, pp);
+      return -1;
+    };
+    const uint16_t* kring = reinterpret_cast<const uint16_t*>(a.kring) + (slot_ok ? slot : 0) * a.kring_slot + h * a.kring_head;
+    const uint16_t* vring = reinterpret_cast<const uint16_t*>(a.vring) + (slot_ok ? slot : 0) * a.vring_slot + h * a.vring_head;
+
+    if constexpr (kByte<FMT>) {
+      ByteState<NC> st;
+      byte_init(st);
+      if (valid) {
+        const int u0 = static_cast<int>(lo), u1 = static_cast<int>(hi);
+        const bool ring = FMT == kI8 && (T % kP) != 0 && u1 == pl.nf + pl.nx;   // the last unit is the unfinished block
+        const int n = u1 - u0 - (ring ? 1 : 0);                                  // records to stream
+        auto pages_of = [&](int k) -> int {   // pool pages of units u0 + 32 k + lane
+          const int x = 32 * k + lane;
+          return x < n ? page(pl.block_of(u0 + x)) : 0;
+        };
+        int curp = pages_of(0), nxtp = n > 32 ? pages_of(1) : 0, cur_k = 0;
+        int pos[CT], opos[CT][2];
+        const uint16_t* qrow[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          pos[c] = pos_of(col0 + 8 * c + gi);
+          opos[c][0] = pos_of(col0 + 8 * c + 2 * ti);
+          opos[c][1] = pos_of(col0 + 8 * c + 2 * ti + 1);
+          qrow[c] = qrow_of(col0 + 8 * c + gi);
+        }
+        uint32_t skip = 0;
+        auto issue = [&](int s, int i) {   // i = 0, 1, 2, ... in order
+          if ((i >> 5) != cur_k) {
+            curp = nxtp;
+            ++cur_k;
+            nxtp = pages_of(cur_k + 1);
+          }
+          const int pp = __shfl_sync(0xffffffffu, curp, i & 31);
+          if (pp < 0) {
+            skip |= 1u << s;
+            return;
+          }
+          skip &= ~(1u << s);
+          constexpr uint32_t kCopy = FMT == kI8 ? Rec<kI8>::kCopy : Rec<8>::kBytes;
+          fence_proxy_async();   // earlier generic reads of the stage come first
+          __syncwarp();
+          if (lane == 0) {
+            const char* src = a.pages + (static_cast<long long>(pp) * a.H + h) * Rec<FMT>::kBytes;
+            mbar_expect_tx(&bar[s], kCopy);
+            bulk_load_hint(region + s * Rec<kI8>::kBytes, src, kCopy, &bar[s], once);
+          }
+          pend |= 1u << s;
+        };
+        for (int i = 0; i < n && i < kStages8; ++i) issue(i, i);
+        // queries: f16 operands, and (INT8) -128 scale sum_c q_c
+        const float ks = FMT == 8 ? a.fp8_scale[h] : 1.0f;
+        const float zscale = a.sm_scale_log2 * ks;
+        uint32_t qa[8][NC / 4];   // [kk][row r | CT + r]: channels c_0 c_1 | c_2 c_3
+        float zoff[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 w4 = qrow[c] ? reinterpret_cast<const uint4*>(qrow[c])[4 * ti + j] : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t x = w[i];
+              if (a.dtype == S4KV_BF16) x = pack_f16x2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+              qa[2 * j + (i >> 1)][(i & 1) * CT + c] = x;
+              if (FMT == kI8) {
+                const float2 f = unpack_in<S4KV_F16>(x);
+                sum += f.x + f.y;
+              }
+            }
+          }
+          sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+          zoff[c] = -128.0f * a.sm_scale_log2 * sum;
+        }
+        bool ok = true;
+        int s = 0;
+        for (int i = 0; i < n; ++i) {
+          if (!((skip >> s) & 1u)) {
+            if (!wait(s)) {
+              ok = false;
+              break;
+            }
+            const char* rec = reinterpret_cast<const char*>(region + s * Rec<kI8>::kBytes);
+            if (u0 + i < pl.nf) {
+              byte_block<FMT, NC, false>(rec, st, qa, zoff, zscale, cut, pos, opos);
+            } else {
+              cut.tok0 = pl.block_of(u0 + i) * BT;
+              byte_block<FMT, NC, true>(rec, st, qa, zoff, zscale, cut, pos, opos);
+            }
+          }
+          if (i + kStages8 < n) issue(s, i + kStages8);
+          s = s + 1 == kStages8 ? 0 : s + 1;
+        }
+        if (FMT == 8) {
+          const float vs = a.fp8_scale[a.H + h];
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) st.o[mt][c][e] *= vs;
+        }
+        if (ok && ring) {
+          cut.tok0 = T / kP * kP;
+          if (a.dtype == S4KV_BF16) ring_block<S4KV_BF16, NC>(kring, vring, T % kP, st, qrow, a.sm_scale_log2, cut, pos, opos);
+          else ring_block<S4KV_F16, NC>(kring, vring, T % kP, st, qrow, a.sm_scale_log2, cut, pos, opos);
+        }
+        if (!ok) {
+          fail(b);
+          byte_init(st);
+        }
+      }
+      // ---- output, or the partial that win_merge_kernel combines ----
+      float f[CT][2];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        st.l[c] += __shfl_xor_sync(0xffffffffu, st.l[c], 1);
+        st.l[c] += __shfl_xor_sync(0xffffffffu, st.l[c], 2);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {   // columns 8c + 2ti + e: their sums sit in lanes 8ti + 4e
+          const float l = __shfl_sync(0xffffffffu, st.l[c], 8 * ti + 4 * e);
+          f[c][e] = own ? (l > 0.0f ? 1.0f / l : l == l ? 0.0f : l) : 1.0f;
+        }
+      }
+      const bool direct = own || !slot_ok;
+      const int k = seg_start <= r0 ? 0 : 1;
+      float* P = a.ws + (2LL * gw + k) * partial_floats(a.pcols);
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int col = 8 * c + 2 * ti + e;
+          if (col0 + col < ncols) {
+            const long long row = out_row(col0 + col);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              float y[8];
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt) y[mt] = st.o[mt][c][2 * half + e] * f[c][e];
+              if constexpr (FMT == kI8) {   // channels 64 half + 8 gi + mt
+                if (direct) store8(a, row, 64 * half + 8 * gi, y);
+                else {
+                  float4* d = reinterpret_cast<float4*>(P + col * kD + 64 * half + 8 * gi);
+                  d[0] = make_float4(y[0], y[1], y[2], y[3]);
+                  d[1] = make_float4(y[4], y[5], y[6], y[7]);
+                }
+              } else {   // channels 16 mt + 8 half + gi
+#pragma unroll
+                for (int mt = 0; mt < 8; ++mt) {
+                  if (direct) store1(a, row, 16 * mt + 8 * half + gi, y[mt]);
+                  else P[col * kD + 16 * mt + 8 * half + gi] = y[mt];
+                }
+              }
+            }
+          }
+        }
+        if (!direct && ti == 0 && col0 + 8 * c + gi < ncols) {
+          P[a.pcols * kD + 2 * (8 * c + gi)] = st.m[c];
+          P[a.pcols * kD + 2 * (8 * c + gi) + 1] = st.l[c];
+        }
+      }
+    } else {
+      using F = Rec<FMT>;
+      constexpr int RS = kRecStrideB<FMT>;
+      float* ptile = sm.ptile[warp];
+      uint8_t* st0 = region;
+      uint8_t* st1 = region + kStageBytesB<FMT>;
+      MmaState ms;
+      mma_init(ms);
+      GenState gs;
+      bool have = false;
+      if (valid) {
+        const int nf = pl.nf, tc = a.tail_cost;
+        const int u0 = static_cast<int>(lo < nf ? lo : nf), u1 = static_cast<int>(hi < nf ? hi : nf), n = u1 - u0;
+        int c0 = 0, c1 = 0;   // cut blocks whose cost position starts inside [lo, hi)
+        if (pl.nx > 0 && hi > nf) {
+          c0 = static_cast<int>(lo > nf ? (lo - nf + tc - 1) / tc : 0);
+          const long long cc = (hi - nf + tc - 1) / tc;
+          c1 = static_cast<int>(cc < pl.nx ? cc : pl.nx);
+        }
+        Seg sg;
+        sg.pages = a.pages;
+        sg.bt = bt;
+        sg.kring = kring;
+        sg.vring = vring;
+        sg.H = a.H;
+        sg.h = h;
+        sg.T = T;
+        sg.Tk = T & ~(kG - 1);
+        sg.Tv = max(0, T - a.R);
+        sg.R = a.R;
+        sg.dtype = a.dtype;
+        auto pages_of = [&](int k, int& x0, int& x1) {   // both pages of units u0 + 32 k + lane
+          const int x = 32 * k + lane;
+          x0 = x1 = 0;
+          if (x < n) {
+            const int blk = pl.block_of(u0 + x);
+            x0 = page(2 * blk);
+            x1 = page(2 * blk + 1);
+            if (x1 < 0) x0 = -1;
+          }
+        };
+        int cur0, cur1, nxt0 = 0, nxt1 = 0, cur_k = 0;
+        pages_of(0, cur0, cur1);
+        if (n > 32) pages_of(1, nxt0, nxt1);
+        uint32_t skip = 0;
+        auto issue = [&](int s, int i) {
+          if ((i >> 5) != cur_k) {
+            cur0 = nxt0;
+            cur1 = nxt1;
+            ++cur_k;
+            pages_of(cur_k + 1, nxt0, nxt1);
+          }
+          const int p0 = __shfl_sync(0xffffffffu, cur0, i & 31), p1 = __shfl_sync(0xffffffffu, cur1, i & 31);
+          if (p0 < 0) {
+            skip |= 1u << s;
+            return;
+          }
+          skip &= ~(1u << s);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            uint8_t* dst = s ? st1 : st0;
+            mbar_expect_tx(&bar[s], 2 * F::kBytes);
+            bulk_load_hint(dst, rec_at<FMT>(sg, p0), F::kBytes, &bar[s], once);
+            bulk_load_hint(dst + RS, rec_at<FMT>(sg, p1), F::kBytes, &bar[s], once);
+          }
+          pend |= 1u << s;
+        };
+        for (int i = 0; i < n && i < kStages; ++i) issue(i, i);
+        // this lane's query: column gi (PACKED: gi % 4), channels 32 ti + x
+        const int qcol = col0 + (PACKED ? gi & 3 : gi);
+        const uint16_t* qrow = qrow_of(qcol);
+        float qv[32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 w4 = qrow ? reinterpret_cast<const uint4*>(qrow)[4 * ti + j] : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            qv[8 * j + 2 * i] = widen16(static_cast<uint16_t>(w[i] & 0xffff), a.dtype);
+            qv[8 * j + 2 * i + 1] = widen16(static_cast<uint16_t>(w[i] >> 16), a.dtype);
+          }
+        }
+        bool ok = true;
+        for (int i = 0; i < n; ++i) {
+          const int s = i & 1;
+          if (!((skip >> s) & 1u)) {
+            if (!wait(s)) {
+              ok = false;
+              break;
+            }
+            mma_group<true, FMT, PACKED>(reinterpret_cast<const char*>(s ? st1 : st0), ms, ptile, qv, a.sm_scale_log2,
+                                         kLoAbove / a.sm_scale_log2);
+          }
+          if (i + kStages < n) issue(s, i + kStages);
+        }
+        mma_unscale<FMT>(ms);
+        const int pos0 = pos_of(col0 + (PACKED ? (2 * ti) & 3 : 2 * ti)), pos1 = pos_of(col0 + (PACKED ? (2 * ti + 1) & 3 : 2 * ti + 1));
+        for (int c = c0; ok && c < c1; ++c) {
+          const int blk = pl.block_of(nf + c);
+          const int t0 = kG * blk, t1 = min(t0 + kG, T);
+          cut.tok0 = t0;
+          const bool kquant = t0 + kG <= sg.Tk, vrec = t0 < sg.Tv;
+          const bool kstaged = !kquant && !vrec && t1 - t0 <= kKringStageMax;
+          const int np = t0 + kP < T ? 2 : 1;
+          const int vt0 = max(t0, sg.Tv), nv = max(0, t1 - vt0);
+          const int voff = kstaged ? (t1 - t0) * kD * 2 : kVoffRecsB<FMT>;
+          int p0 = 0, p1 = 0;
+          if (kquant || vrec) {
+            p0 = page(2 * blk);
+            p1 = np == 2 ? page(2 * blk + 1) : p0;
+            if (p0 < 0 || p1 < 0) continue;
+          }
+          const uint32_t rb = vrec ? F::kBytes : F::kKm + 512;   // whole records, or the keys' part
+          uint32_t bytes = nv * kD * 2;
+          if (kquant || vrec) bytes += np * rb;
+          if (kstaged) bytes += (t1 - t0) * kD * 2;
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_expect_tx(&bar[0], bytes);
+            if (kquant || vrec) {
+              bulk_load_hint(st0, rec_at<FMT>(sg, p0), rb, &bar[0], once);
+              if (np == 2) bulk_load_hint(st0 + RS, rec_at<FMT>(sg, p1), rb, &bar[0], once);
+            }
+            if (kstaged) bulk_load_hint(st0, kring, (t1 - t0) * kD * 2, &bar[0], once);
+          }
+          __syncwarp();
+          if (lane < nv) {
+            const int t = vt0 + lane;
+            bulk_load_hint(st0 + voff + (t - t0) * kVRow, vring + static_cast<long long>(t % a.R) * kD, kD * 2, &bar[0], once);
+          }
+          pend |= 1u;
+          if (!wait(0)) {
+            ok = false;
+            break;
+          }
+          kivi_cut_block<FMT>(sg, ms, ptile, qv, reinterpret_cast<const char*>(st0),
+                              kstaged ? reinterpret_cast<const uint16_t*>(st0) : kring,
+                              reinterpret_cast<const char*>(st0 + voff), smem_u32(&zero16), a.sm_scale_log2, cut, pos0, pos1);
+        }
+        if (ok) {
+          mma_to_gen(ms, gs, reinterpret_cast<float*>(st0));
+          have = true;
+        } else {
+          fail(b);
+        }
+      }
+      if (!have) gen_init(gs);
+      const bool direct = own || !slot_ok;
+      const int k = seg_start <= r0 ? 0 : 1;
+      float* P = a.ws + (2LL * gw + k) * partial_floats(a.pcols);
+#pragma unroll
+      for (int j = 0; j < kNH; ++j) {
+        if (col0 + j < ncols && j < a.pcols) {
+          if (direct) {
+            const float l = gs.l[j], inv = l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
+            store_out(a, out_row(col0 + j), lane, make_float4(gs.o[j][0] * inv, gs.o[j][1] * inv, gs.o[j][2] * inv, gs.o[j][3] * inv));
+          } else {
+            *reinterpret_cast<float4*>(P + j * kD + 4 * lane) = make_float4(gs.o[j][0], gs.o[j][1], gs.o[j][2], gs.o[j][3]);
+            if (lane == 0) {
+              P[a.pcols * kD + 2 * j] = gs.m[j];
+              P[a.pcols * kD + 2 * j + 1] = gs.l[j];
+            }
+          }
+        }
+      }
+      __syncwarp();   // the region is scratch until here
+    }
+    if (seg_start >= r0 && lane == 0) {   // this warp holds the segment's first unit: its merge descriptor
+      int ncon = 0;
+      if (!own && slot_ok) ncon = owner_of(seg_end - 1, C, n_act) - gw + 1;
+      const long long first = 2LL * gw + (seg_start <= r0 ? 0 : 1);
+      win_meta(a)[static_cast<long long>(b) * a.H * a.tiles + seg] =
+          static_cast<long long>(static_cast<unsigned>(first)) | (static_cast<long long>(ncon) << 32);
+    }
+    // next segment
+    seg_start = seg_end;
+    if (++seg == a.H * a.tiles) {
+      seg = 0;
+      if (++b >= a.B) break;
+      T = a.seq_lens[b];
+      pl = plan_of<FMT>(T, a);
+    }
+  }
+  if (pend) fail(-1);   // never expected: every issued copy is waited for
+}
+
+// One warp per output row of a split segment: the contributors' partials combined
+// by the log-sum-exp rule, kMC at a time.
+__global__ void __launch_bounds__(32 * kMergeWarps) win_merge_kernel(DecodeArgs d, int window, int sinks, int tiles, int nc) {
+  (void)window;
+  (void)sinks;
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // window_kernel has completed; its writes are visible
+  const int lane = threadIdx.x & 31;
+  const long long* desc = reinterpret_cast<const long long*>(d.ws + 2LL * d.grid_warps * partial_floats(d.pcols));
+  const int ncols = d.nq * d.g;
+  const long long items = static_cast<long long>(d.B) * d.H * ncols, pf = partial_floats(d.pcols);
+  for (long long it = static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5); it < items;
+       it += static_cast<long long>(gridDim.x) * kMergeWarps) {
+    const int col = static_cast<int>(it % ncols), tile = col / nc, j = col - tile * nc;
+    const long long bh = it / ncols;
+    const long long x = __ldcg(desc + bh * tiles + tile);
+    const int n = static_cast<int>(x >> 32);
+    if (n <= 0) continue;   // written by window_kernel
+    const long long first = static_cast<long long>(static_cast<unsigned>(x & 0xffffffffLL));
+    auto part = [&](int i) -> const float* { return d.ws + (i == 0 ? first : (first & ~1LL) + 2LL * i) * pf; };
+    float M = -INFINITY, L = 0.0f;
+    float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i0 = 0; i0 < n; i0 += kMC) {
+      const int nch = min(kMC, n - i0);
+      const float* W = part(i0 + (lane < nch ? lane : 0)) + d.pcols * kD + 2 * j;
+      const float mi = lane < nch ? __ldcg(W) : -INFINITY;
+      const float li = lane < nch ? __ldcg(W + 1) : 0.0f;
+      float4 r[kMC];
+#pragma unroll
+      for (int u = 0; u < kMC; ++u)
+        r[u] = u < nch ? __ldcg(reinterpret_cast<const float4*>(part(i0 + u) + j * kD + 4 * lane))
+                       : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const float mn = fmaxf(M, warp_max(mi));
+      const bool live = mn != -INFINITY;   // every partial empty so far: nothing to weigh
+      const float ao = live ? ex2(M - mn) : 1.0f, wi = live ? ex2(mi - mn) : 0.0f;
+      L = fmaf(L, ao, warp_sum(wi * li));
+      O = make_float4(O.x * ao, O.y * ao, O.z * ao, O.w * ao);
+#pragma unroll
+      for (int u = 0; u < kMC; ++u) {
+        const float w = __shfl_sync(0xffffffffu, wi, u);
+        if (u < nch) O = make_float4(fmaf(w, r[u].x, O.x), fmaf(w, r[u].y, O.y), fmaf(w, r[u].z, O.z), fmaf(w, r[u].w, O.w));
+      }
+      M = mn;
+    }
+    const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
+    const int q = col / d.g;
+    const long long row = (bh / d.H * d.nq + q) * d.Hq + (bh % d.H) * d.g + (col - q * d.g);
+    store_out(d, row, lane, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
+  }
+}
+
+template <int FMT, int NC, bool PACKED>
+cudaError_t run(const WindowArgs& a, int grid, cudaStream_t st) {
+  static size_t granted = 0;   // largest dynamic shared memory asked for so far
+  const size_t need = prefix_at<FMT>() + static_cast<size_t>(a.B + 1) * sizeof(long long);
+  if (need > granted) {
+    const void* f = reinterpret_cast<const void*>(window_kernel<FMT, NC, PACKED>);
+    cudaError_t e = prefer_max_shared(f);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(need));
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return e;
+    }
+    granted = need;
+  }
+  window_kernel<FMT, NC, PACKED><<<grid, 32 * kWinWarps, need, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int window_warps_per_cta() { return kWinWarps; }
+int window_cols(int bits, int cols) { return (bits == 8 || bits == kI8) && cols > 8 ? 16 : 8; }
+
+cudaError_t launch_window(const WindowArgs& a, int grid, cudaStream_t st) {
+  const int cols = a.nq * a.g, nc = window_cols(a.bits, cols);
+  // No more CTAs than the work can use (slices go to one warp of every CTA first):
+  // a sequence has at most the blocks of max_seq_len, or of window, queries and
+  // sinks, and each end of a range may cut one more.
+  {
+    const bool kivi = a.bits != 8 && a.bits != kI8;
+    const long long bt = kivi ? kG : kP, seen = static_cast<long long>(a.window) + a.nq + a.sinks;
+    long long units = (a.max_seq_len < seen ? a.max_seq_len : seen) / bt + 5;
+    if (kivi) units += static_cast<long long>(a.tail_cost - 1) * ((a.R + 2 * kG) / kG + 5);
+    const long long warps = (units * a.B * a.H * a.tiles + 2) / 3;   // 3: the least work of a warp
+    if (warps < grid) grid = static_cast<int>(warps);
+  }
+  cudaError_t e;
+  if (a.bits == kI8) e = nc == 16 ? run<kI8, 16, false>(a, grid, st) : run<kI8, 8, false>(a, grid, st);
+  else if (a.bits == 8) e = nc == 16 ? run<8, 16, false>(a, grid, st) : run<8, 8, false>(a, grid, st);
+  else if (a.bits == 2) e = cols <= 4 ? run<2, 8, true>(a, grid, st) : run<2, 8, false>(a, grid, st);
+  else e = cols <= 4 ? run<4, 8, true>(a, grid, st) : run<4, 8, false>(a, grid, st);
+  if (e != cudaSuccess) return e;
+  // the combine, launched programmatically right behind
+  long long blocks = (static_cast<long long>(a.B) * a.H * cols + kMergeWarps - 1) / kMergeWarps;
+  if (blocks > 16LL * grid) blocks = 16LL * grid;
+  e = prefer_max_shared(reinterpret_cast<const void*>(win_merge_kernel));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, win_merge_kernel, static_cast<const DecodeArgs&>(a), a.window, a.sinks, a.tiles, nc);
+}
+
+}  // namespace s4kv
