@@ -492,9 +492,13 @@ int s4kv_kv_bytes(const s4kv_config* cfg, double batch, double tokens, s4kv_kv_b
  *                          output within the tolerance when key channels are
  *                          scaled x16 or x32; 0 = f16 q' alone: about 8% faster,
  *                          but its error passes the tolerance on such channels.
- *                          Tail groups and multi-query calls always split. */
+ *                          Tail groups, multi-query and window calls always split.
+ *   S4KV_OPT_WINDOW_FORM   launch form of window calls and of attention on INT8
+ *                          pages: 0 (default) by the call's size, 1 = slices over
+ *                          all SMs and a combine kernel, 2 = one launch, a cluster of
+ *                          CTAs for each (sequence, kv head, tile of columns). */
 enum { S4KV_OPT_DECODE_WARPS = 1, S4KV_OPT_DECODE_IMPL = 2, S4KV_OPT_WAIT_NS = 3, S4KV_OPT_TAIL_COST = 4,
-       S4KV_OPT_KEY_SPLIT = 5, S4KV_OPT_MQ_KERNEL = 6 };
+       S4KV_OPT_KEY_SPLIT = 5, S4KV_OPT_MQ_KERNEL = 6, S4KV_OPT_WINDOW_FORM = 7 };
 int s4kv_set_option(s4kv_cache* cache, int option, long long value);
 
 #ifdef __cplusplus

@@ -11,6 +11,7 @@ importing this package raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -36,6 +37,7 @@ S4KV_BITS_INT8 = 0x108
 S4KV_OPT_DECODE_WARPS, S4KV_OPT_DECODE_IMPL, S4KV_OPT_WAIT_NS, S4KV_OPT_TAIL_COST = 1, 2, 3, 4
 S4KV_OPT_KEY_SPLIT = 5
 S4KV_OPT_MQ_KERNEL = 6
+S4KV_OPT_WINDOW_FORM = 7
 
 
 class S4KVError(RuntimeError):
@@ -112,20 +114,19 @@ _lib = _load()
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return ctypes.c_void_p(x)
-    return ctypes.c_void_p(x.data_ptr())
+    # an int or None goes to a c_void_p argument as it is
+    if x is None or isinstance(x, int):
+        return x
+    return x.data_ptr()
 
 
 def _stream(s):
     if s is None:
         import torch
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
-        return ctypes.c_void_p(s)
-    return ctypes.c_void_p(s.cuda_stream)
+        return s
+    return s.cuda_stream
 
 
 def _check(rc: int, what: str):
@@ -315,6 +316,18 @@ class Rope:
         self.c = s4kv_rope(table.data_ptr(), table.shape[0], table.shape[1], int(self.interleaved))
 
 
+def _on_its_device(f):
+    """A method that runs with the cache's device as the current one."""
+    @functools.wraps(f)
+    def call(self, *args, **kwargs):
+        import torch
+        if torch.cuda.current_device() == self._index:
+            return f(self, *args, **kwargs)
+        with torch.cuda.device(self._index):
+            return f(self, *args, **kwargs)
+    return call
+
+
 class KVCache:
     """A cache bound to a torch-allocated device pool (torch provides memory only).
 
@@ -338,6 +351,8 @@ class KVCache:
         self.H = num_kv_heads
         self.R = residual_v
         self._ws = None
+        self._index = self.pool.get_device()
+        self._sizes = {}
 
     def close(self):
         if getattr(self, "h", None):
@@ -379,7 +394,7 @@ class KVCache:
             dt = torch.float32 if out_dtype == S4KV_F32 else self.torch_dtype
             out = torch.empty((B, Hq, 128), dtype=dt, device=q.device)
         if self.bits == S4KV_BITS_INT8:
-            nbytes = s4kv_decode_workspace_bytes(self.h, B, Hq, max_seq_len)
+            nbytes = self._window_bytes(B, 1, Hq, max_seq_len)
             ws = self._scratch(nbytes, stream)
         else:
             ws, nbytes = self.workspace(B, Hq, max_seq_len)
@@ -395,12 +410,13 @@ class KVCache:
         if out is None:
             dt = torch.float32 if out_dtype == S4KV_F32 else self.torch_dtype
             out = torch.empty((B, nq, Hq, 128), dtype=dt, device=q.device)
-        nbytes = s4kv_multi_query_workspace_bytes(self.h, B, nq, Hq, max_seq_len)
         if self.bits == S4KV_BITS_INT8:
+            nbytes = self._window_bytes(B, nq, Hq, max_seq_len)
             s4kv_multi_query_attention(self.h, layer, q, nq, Hq, block_table, block_table.shape[1], seq_lens, slot_ids, B,
                                        sm_scale, out, out_dtype, self._scratch(nbytes, stream), nbytes, max_seq_len,
                                        stream)
             return out
+        nbytes = s4kv_multi_query_workspace_bytes(self.h, B, nq, Hq, max_seq_len)
         if self._ws is None or self._ws.numel() < nbytes:
             self._ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self.pool.device)
         s4kv_multi_query_attention(self.h, layer, q, nq, Hq, block_table, block_table.shape[1], seq_lens,
@@ -410,98 +426,116 @@ class KVCache:
     # ---- calls that check their tensors and take scratch of their own ----
     def _tensor(self, t, name, dtype, shape):
         """t is a contiguous tensor of this cache's device; shape: sizes, None for any."""
-        if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
-            raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} is wanted, got {t.dtype} {tuple(t.shape)}")
+        got = t.shape
+        if t.dtype is not dtype or len(got) != len(shape) or any(w != g for w, g in zip(shape, got) if w is not None):
+            raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} is wanted, got {t.dtype} {tuple(got)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} is not contiguous")
-        if t.device != self.pool.device:
+        if t.get_device() != self._index:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.pool.device}")
-        return t
+        return got
 
     def _scratch(self, nbytes, stream):
         """Scratch of one call, allocated on its stream: calls on other streams and captured graphs share none of it."""
         import torch
         if stream is None:
-            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self.pool.device)
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.pool.device)
         st = torch.cuda.ExternalStream(stream, device=self.pool.device) if isinstance(stream, int) else stream
         with torch.cuda.stream(st):
-            return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=self.pool.device)
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.pool.device)
+
+    def _window_bytes(self, B, nq, Hq, max_seq_len):
+        """Scratch of a window call (on INT8 pages of any attention call): it goes by these sizes alone."""
+        n = self._sizes.get((B, nq, Hq))
+        if n is None:
+            n = self._sizes[B, nq, Hq] = max(16, s4kv_window_workspace_bytes(self.h, B, nq, Hq, max_seq_len))
+        return n
 
     def _out(self, out, name, shape, out_dtype):
         import torch
-        if out_dtype not in (S4KV_F32, self.cdtype):
+        if out_dtype == self.cdtype:
+            dt = self.torch_dtype
+        elif out_dtype == S4KV_F32:
+            dt = torch.float32
+        else:
             raise ValueError("out_dtype is S4KV_F32 or the cache's dtype")
-        dt = torch.float32 if out_dtype == S4KV_F32 else self.torch_dtype
         if out is None:
             return torch.empty(shape, dtype=dt, device=self.pool.device)
-        return self._tensor(out, name, dt, shape)
+        self._tensor(out, name, dt, shape)
+        return out
 
+    @_on_its_device
     def append_rope(self, layer, k, v, cu_new, seq_lens_before, block_table, rope, slot_ids=None, q=None, q_out=None,
                     stream=None):
         """append() with the new keys rotated by their positions on the way (rope: a Rope). With q
         [tokens, H_q, 128], the new tokens' queries are rotated too, into q_out (a new tensor if
         None; q itself is allowed), which is returned."""
         import torch
-        i32, n = torch.int32, seq_lens_before.numel()
-        self._tensor(k, "k", self.torch_dtype, (None, self.H, 128))
-        self._tensor(v, "v", self.torch_dtype, tuple(k.shape))
+        i32, dt, n = torch.int32, self.torch_dtype, seq_lens_before.shape[0]
+        tokens = self._tensor(k, "k", dt, (None, self.H, 128))[0]
+        self._tensor(v, "v", dt, (tokens, self.H, 128))
         self._tensor(cu_new, "cu_new", i32, (n + 1,))
         self._tensor(seq_lens_before, "seq_lens_before", i32, (n,))
-        self._tensor(block_table, "block_table", i32, (None, None))
-        self._tensor(rope.table, "the rotation table", torch.float32, (None, None))
-        if block_table.shape[0] < n:
+        rows, width = self._tensor(block_table, "block_table", i32, (None, None))
+        if rows < n:
             raise ValueError("block_table has fewer rows than there are sequences")
+        if rope.table.get_device() != self._index:
+            raise ValueError(f"the rotation table is on {rope.table.device}, the cache on {self.pool.device}")
         if slot_ids is not None:
             self._tensor(slot_ids, "slot_ids", i32, (n,))
+        heads = 0
         if q is not None:
-            self._tensor(q, "q", self.torch_dtype, (k.shape[0], None, 128))
-            q_out = torch.empty_like(q) if q_out is None else self._tensor(q_out, "q_out", self.torch_dtype, tuple(q.shape))
+            heads = self._tensor(q, "q", dt, (tokens, None, 128))[1]
+            if q_out is None:
+                q_out = torch.empty_like(q)
+            elif q_out is not q:
+                self._tensor(q_out, "q_out", dt, (tokens, heads, 128))
         elif q_out is not None:
             raise ValueError("q_out without q")
-        with torch.cuda.device(self.pool.device):
-            s4kv_append_rope(self.h, layer, rope.c, k, v, k.shape[0], cu_new, slot_ids, seq_lens_before, block_table,
-                             block_table.shape[1], n, q, 0 if q is None else q.shape[1], q_out, stream)
+        s4kv_append_rope(self.h, layer, rope.c, k, v, tokens, cu_new, slot_ids, seq_lens_before, block_table, width, n,
+                         q, heads, q_out, stream)
         return q_out
 
+    @_on_its_device
     def window(self, layer, q, block_table, seq_lens, max_seq_len, window, num_sinks=0, out=None, out_dtype=S4KV_F32,
                slot_ids=None, sm_scale=0.0, stream=None):
         """Causal attention of the last nq tokens, q [B, nq, H_q, 128], within the newest `window` tokens
         of each query's position and the first `num_sinks` tokens -> out [B, nq, H_q, 128]."""
         import torch
-        B, nq, Hq, _ = self._tensor(q, "q", self.torch_dtype, (None, None, None, 128)).shape
-        self._tensor(block_table, "block_table", torch.int32, (None, None))
+        B, nq, Hq, _ = self._tensor(q, "q", self.torch_dtype, (None, None, None, 128))
+        rows, width = self._tensor(block_table, "block_table", torch.int32, (None, None))
         self._tensor(seq_lens, "seq_lens", torch.int32, (B,))
-        if block_table.shape[0] < B:
+        if rows < B:
             raise ValueError("block_table has fewer rows than there are sequences")
         if slot_ids is not None:
             self._tensor(slot_ids, "slot_ids", torch.int32, (B,))
         out = self._out(out, "out", (B, nq, Hq, 128), out_dtype)
-        with torch.cuda.device(self.pool.device):
-            nbytes = s4kv_window_workspace_bytes(self.h, B, nq, Hq, max_seq_len)
-            ws = self._scratch(nbytes, stream)
-            s4kv_window_attention(self.h, layer, q, nq, Hq, window, num_sinks, block_table, block_table.shape[1],
-                                  seq_lens, slot_ids, B, sm_scale, out, out_dtype, ws, nbytes, max_seq_len, stream)
+        nbytes = self._window_bytes(B, nq, Hq, max_seq_len)
+        s4kv_window_attention(self.h, layer, q, nq, Hq, window, num_sinks, block_table, width, seq_lens, slot_ids, B,
+                              sm_scale, out, out_dtype, self._scratch(nbytes, stream), nbytes, max_seq_len, stream)
         return out
 
+    @_on_its_device
     def gather(self, layer, block_table, seq_lens, cu_rows, num_rows, first=None, slot_ids=None, out_k=None, out_v=None,
                out_dtype=S4KV_F32, stream=None):
         """Restores tokens first[i] .. of sequence i (0 without first) into rows [cu_rows[i], cu_rows[i+1])
         of two dense tensors [num_rows, H_kv, 128], which are returned as (k, v)."""
         import torch
-        i32, n = torch.int32, seq_lens.numel()
-        self._tensor(block_table, "block_table", i32, (None, None))
+        i32, n = torch.int32, seq_lens.shape[0]
+        rows, width = self._tensor(block_table, "block_table", i32, (None, None))
         self._tensor(seq_lens, "seq_lens", i32, (n,))
         self._tensor(cu_rows, "cu_rows", i32, (n + 1,))
-        if block_table.shape[0] < n:
+        if rows < n:
             raise ValueError("block_table has fewer rows than there are sequences")
-        for t, name in ((first, "first"), (slot_ids, "slot_ids")):
-            if t is not None:
-                self._tensor(t, name, i32, (n,))
-        out_k = self._out(out_k, "out_k", (num_rows, self.H, 128), out_dtype)
-        out_v = self._out(out_v, "out_v", (num_rows, self.H, 128), out_dtype)
-        with torch.cuda.device(self.pool.device):
-            s4kv_gather(self.h, layer, block_table, block_table.shape[1], seq_lens, slot_ids, first, cu_rows, num_rows,
-                        n, out_k, out_v, out_dtype, stream)
+        if first is not None:
+            self._tensor(first, "first", i32, (n,))
+        if slot_ids is not None:
+            self._tensor(slot_ids, "slot_ids", i32, (n,))
+        shape = (num_rows, self.H, 128)
+        out_k = self._out(out_k, "out_k", shape, out_dtype)
+        out_v = self._out(out_v, "out_v", shape, out_dtype)
+        s4kv_gather(self.h, layer, block_table, width, seq_lens, slot_ids, first, cu_rows, num_rows, n, out_k, out_v,
+                    out_dtype, stream)
         return out_k, out_v
 
     def dequant(self, layer, slot, block_table_row, seq_len, stream=None):

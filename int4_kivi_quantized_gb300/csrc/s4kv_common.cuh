@@ -79,6 +79,7 @@ struct s4kv_cache {
   int decode_impl;          // 0 tensor-core, 1 FFMA
   int key_split;            // S4KV_OPT_KEY_SPLIT
   int mq_kernel;            // S4KV_OPT_MQ_KERNEL
+  int window_form;          // S4KV_OPT_WINDOW_FORM
   int bits;                 // page format: 4, 2, 8 (FP8 E4M3) or S4KV_BITS_INT8
   long long wait_ns;
   int num_sms;
@@ -191,6 +192,7 @@ struct DecodeArgs {
 struct WindowArgs : DecodeArgs {
   int window, sinks;        // token t is visible at position p: t <= p, t > p - window or t < sinks
   int tiles;                // column tiles of a (sequence, kv head): nq g columns, pcols each
+  int form;                 // S4KV_OPT_WINDOW_FORM
 };
 
 // Asks for the largest shared-memory carve-out for `func`, once per device and
@@ -232,9 +234,9 @@ cudaError_t launch_dequant(const DequantArgs& a, cudaStream_t st);
 cudaError_t launch_append_int8(const AppendArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_dequant_int8(const DequantArgs& a, cudaStream_t st);
 cudaError_t launch_gather(const GatherArgs& a, int num_sms, cudaStream_t st);
-cudaError_t launch_window(const WindowArgs& a, int grid, cudaStream_t st);
+cudaError_t launch_window(const WindowArgs& a, int num_sms, cudaStream_t st);
 int window_cols(int bits, int cols);      // columns of one warp's tile for a call of `cols` columns
-int window_warps_per_cta();
+int window_warps_per_sm();
 cudaError_t launch_decode(const DecodeArgs& a, int impl, int grid, cudaStream_t st);
 // the decode step: a cooperative launch of the decode kernel with the append phase
 cudaError_t launch_decode_step(const DecodeArgs& a, int impl, int grid, cudaStream_t st);

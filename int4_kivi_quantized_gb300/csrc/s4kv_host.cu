@@ -114,7 +114,7 @@ int window_tiles(const s4kv_cache* c, int cols) {
 }
 int window_pcols(const s4kv_cache* c, int cols) { return window_tiles(c, cols) == 1 ? cols : window_cols(c->bits, cols); }
 size_t window_ws_bytes(const s4kv_cache* c, int B, int cols) {
-  const size_t warps = static_cast<size_t>(c->num_sms) * window_warps_per_cta();
+  const size_t warps = static_cast<size_t>(c->num_sms) * window_warps_per_sm();
   return 2 * warps * decode_partial_bytes(window_pcols(c, cols)) +
          decode_meta_bytes(B, c->cfg.num_kv_heads * window_tiles(c, cols));
 }
@@ -313,6 +313,10 @@ int s4kv_set_option(s4kv_cache* cache, int option, long long value) {
       if (value < 0 || value > 3) return S4KV_ERR_INVALID_ARG;
       cache->mq_kernel = static_cast<int>(value);
       return S4KV_OK;
+    case S4KV_OPT_WINDOW_FORM:
+      if (value < 0 || value > 2) return S4KV_ERR_INVALID_ARG;
+      cache->window_form = static_cast<int>(value);
+      return S4KV_OK;
     case S4KV_OPT_KEY_SPLIT:
       if (value != 0 && value != 1) return S4KV_ERR_INVALID_ARG;
       cache->key_split = static_cast<int>(value);
@@ -493,9 +497,10 @@ int window_call(s4kv_cache* cache, DecodeArgs d, int nq, int window, int sinks, 
   a.nq = nq;
   a.window = window;
   a.sinks = sinks;
+  a.form = cache->window_form;
   a.tiles = window_tiles(cache, cols);
   a.pcols = window_pcols(cache, cols);
-  a.grid_warps = cache->num_sms * window_warps_per_cta();
+  a.grid_warps = cache->num_sms * window_warps_per_sm();
   const cudaError_t e = launch_window(a, cache->num_sms, st);
   return e == cudaSuccess ? S4KV_OK : S4KV_ERR_CUDA;
 }

@@ -40,22 +40,40 @@ namespace s4kv {
 namespace {
 
 constexpr int kI8 = S4KV_BITS_INT8;
-constexpr int kWinWarps = 12;
-constexpr int kStages8 = 3;
-constexpr int kRegion8 = (kStages8 * Rec<kI8>::kBytes + 127) / 128 * 128;   // 12416
+#ifndef S4KV_WINDOW_I8_WARPS
+#define S4KV_WINDOW_I8_WARPS 12
+#endif
+#ifndef S4KV_WINDOW_I8_STAGES
+#define S4KV_WINDOW_I8_STAGES 2
+#endif
+// Warps of a CTA, one CTA per SM.
+template <int FMT> constexpr int kWarpsOf = FMT == kI8 ? S4KV_WINDOW_I8_WARPS : 12;
+constexpr int kMaxWarps = 16;
+template <int FMT> constexpr int kStagesOf = FMT == kI8 ? S4KV_WINDOW_I8_STAGES : 3;   // records in flight per warp (8-bit pages)
 template <int FMT> constexpr bool kByte = FMT == 8 || FMT == kI8;
 template <int FMT> constexpr int kBlock = kByte<FMT> ? kP : kG;             // tokens of a block
-template <int FMT> constexpr int kRegionOf = kByte<FMT> ? kRegion8 : kRegion;
-template <int FMT> constexpr int kMinUnits8 = kByte<FMT> ? 4 : 3;           // least work per warp
+// 8-bit pages: the stages, or a warp's 16 columns of output when a segment is combined
+template <int FMT> constexpr int kRegionOf = kByte<FMT> ? (kStagesOf<FMT> * Rec<kI8>::kBytes > 16 * kD * 4 ? (kStagesOf<FMT> * Rec<kI8>::kBytes + 127) / 128 * 128 : 16 * kD * 4) : kRegion;
+template <int FMT> constexpr int kLeastUnits = kByte<FMT> ? 4 : 3;           // least work per warp
 
 template <int FMT>
 struct WSmem {
-  alignas(128) uint8_t region[kWinWarps][kRegionOf<FMT>];
-  alignas(16) float ptile[kByte<FMT> ? 1 : kWinWarps][32 * kPRow];
-  alignas(8) uint64_t bar[kWinWarps][4];
+  alignas(128) uint8_t region[kWarpsOf<FMT>][kRegionOf<FMT>];
+  alignas(16) float ptile[kByte<FMT> ? 1 : kWarpsOf<FMT>][32 * kPRow];
+  alignas(8) uint64_t bar[kWarpsOf<FMT>][4];
+};
+// Behind it: the cost prefix of the line (int64 [B + 1]), or what a one-segment
+// launch combines: each warp's maxima and sums, then the CTA's own state.
+struct OneSmem {
+  float wm[kMaxWarps][16], wl[kMaxWarps][16];
+  alignas(16) float part[16][kD];
+  float pm[16], pl[16];
 };
 template <int FMT>
 __host__ __device__ constexpr size_t prefix_at() { return (sizeof(WSmem<FMT>) + 15) / 16 * 16; }
+static_assert(prefix_at<4>() + 4097 * sizeof(long long) <= 227 * 1024 &&
+                  prefix_at<4>() + sizeof(OneSmem) <= 227 * 1024,
+              "the largest batch fits the shared memory of a CTA");
 
 __device__ __forceinline__ bool visible(int t, int pos, int window, int sinks) {
   return t <= pos && (t > pos - window || t < sinks);
@@ -696,16 +714,95 @@ __device__ __forceinline__ void store1(const WindowArgs& a, long long row, int c
   else reinterpret_cast<__half*>(a.out)[idx] = __float2half_rn(y);
 }
 
+// The combine of a one-segment launch: a cluster's CTAs hold one segment, each warp
+// left its columns' (m, l) in wm, wl and its unscaled output in its region. First the
+// warps of a CTA (a thread per four channels of a column), then, column by column,
+// the CTAs through distributed shared memory. Warps without work left l = 0 and
+// nothing else. Every thread of the cluster comes here once.
+template <int FMT>
+__device__ __forceinline__ void combine_cluster(const WindowArgs& a, const WSmem<FMT>& sm, OneSmem& one, int csize, int rank, int ncols,
+                                                long long row0, int col0, int g) {
+  constexpr int kW = kWarpsOf<FMT>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // output row of the tile's column j
+  auto out_row = [&](int j) -> long long {
+    const int i = (col0 + j) / g;
+    return row0 + static_cast<long long>(i) * a.Hq + (col0 + j - i * g);
+  };
+  auto finish = [&](int col, float L, float4 O) {
+    const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
+    store_out(a, out_row(col), lane, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
+  };
+  __syncthreads();
+  for (int col = warp; col < ncols; col += kW) {
+    float M = -INFINITY, L = 0.0f;
+    float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kW; ++w) M = fmaxf(M, one.wm[w][col]);
+#pragma unroll
+    for (int w = 0; w < kW; ++w) {
+      const float l = one.wl[w][col];
+      if (l == 0.0f) continue;
+      const float x = M == -INFINITY ? 1.0f : ex2(one.wm[w][col] - M);
+      const float4 r = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sm.region[w]) + col * kD + 4 * lane);
+      L = fmaf(x, l, L);
+      O = make_float4(fmaf(x, r.x, O.x), fmaf(x, r.y, O.y), fmaf(x, r.z, O.z), fmaf(x, r.w, O.w));
+    }
+    if (csize == 1) {
+      finish(col, L, O);
+    } else {
+      *reinterpret_cast<float4*>(&one.part[col][4 * lane]) = O;
+      if (lane == 0) {
+        one.pm[col] = M;
+        one.pl[col] = L;
+      }
+    }
+  }
+  if (csize == 1) return;
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  auto remote = [&](const void* p, int r) {
+    uint32_t x;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x) : "r"(smem_u32(p)), "r"(r));
+    return x;
+  };
+  for (int col = warp * csize + rank; col < ncols; col += kW * csize) {
+    float M = -INFINITY, L = 0.0f, m = -INFINITY, l = 0.0f;
+    float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (lane < csize) {
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(m) : "r"(remote(&one.pm[col], lane)));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(l) : "r"(remote(&one.pl[col], lane)));
+    }
+    M = warp_max(m);
+    const float wl = l == 0.0f ? 0.0f : M == -INFINITY ? 1.0f : ex2(m - M);
+    for (int r = 0; r < csize; ++r) {
+      const float x = __shfl_sync(0xffffffffu, wl, r), lr = __shfl_sync(0xffffffffu, l, r);
+      if (lr == 0.0f) continue;
+      float4 y;
+      asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w)
+                   : "r"(remote(&one.part[col][4 * lane], r)));
+      L = fmaf(x, lr, L);
+      O = make_float4(fmaf(x, y.x, O.x), fmaf(x, y.y, O.y), fmaf(x, y.z, O.z), fmaf(x, y.w, O.w));
+    }
+    finish(col, L, O);
+  }
+  // no CTA leaves while another may still read its shared memory
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // FMT: page format. NC: columns a warp holds (8, or 16 on 8-bit pages). PACKED
 // (KIVI, at most 4 columns): the query's low f16 part rides in columns 4..7.
-template <int FMT, int NC, bool PACKED>
-__global__ void __launch_bounds__(32 * kWinWarps, 1) window_kernel(WindowArgs a) {
+// ONE: a cluster of CTAs holds one segment and combines it itself (grid.x = CTAs of
+// a cluster, grid.y = segments); otherwise the slices of the whole line, as above.
+template <int FMT, int NC, bool PACKED, bool ONE>
+__global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArgs a) {
   constexpr int BT = kBlock<FMT>;
   constexpr int CT = NC / 8;
-  constexpr int kThreads = 32 * kWinWarps;
+  constexpr int kW = kWarpsOf<FMT>, kThreads = 32 * kW;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   auto& sm = *reinterpret_cast<WSmem<FMT>*>(smem_raw);
   long long* pre = reinterpret_cast<long long*>(smem_raw + prefix_at<FMT>());   // [B + 1]
+  OneSmem& one = *reinterpret_cast<OneSmem*>(smem_raw + prefix_at<FMT>());        // (ONE)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, ti = lane & 3;
   uint8_t* region = sm.region[warp];
   uint64_t* bar = sm.bar[warp];
@@ -714,43 +811,80 @@ __global__ void __launch_bounds__(32 * kWinWarps, 1) window_kernel(WindowArgs a)
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __shared__ __align__(16) uint4 zero16;
   if (tid == 0) zero16 = make_uint4(0u, 0u, 0u, 0u);
-  {   // cost prefix over sequences: sequence b owns H tiles segments of its plan's cost
-    long long carry = 0;
-    __shared__ long long wt[kWinWarps];
-    for (int base = 0; base < a.B; base += kThreads) {
-      const int b = base + tid;
-      const long long cnt = b < a.B ? static_cast<long long>(a.H) * a.tiles * plan_of<FMT>(a.seq_lens[b], a).cost : 0;
-      long long x = cnt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (lane == 31) wt[warp] = x;
-      __syncthreads();
-      long long before = carry, total = 0;
-      for (int q = 0; q < kWinWarps; ++q) {
-        if (q < warp) before += wt[q];
-        total += wt[q];
-      }
-      if (b < a.B) pre[b] = before + x - cnt;
-      __syncthreads();
-      carry += total;
+  int b, seg, T, gw, n_act;
+  long long r0, r1, seg_start, C = 0;
+  Plan pl;
+  if constexpr (ONE) {
+    const int per = a.H * a.tiles;
+    b = static_cast<int>(blockIdx.y) / per;
+    seg = static_cast<int>(blockIdx.y) - b * per;
+    T = a.seq_lens[b];
+    pl = plan_of<FMT>(T, a);
+    gw = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    n_act = static_cast<int>(gridDim.x) * kW;
+    if (a.max_warps > 0 && a.max_warps < n_act) n_act = a.max_warps;
+    if (pl.cost < n_act) n_act = static_cast<int>(pl.cost);
+    seg_start = 0;
+    r0 = gw * pl.cost / n_act;
+    r1 = (gw + 1) * pl.cost / n_act;
+    if (gw >= n_act) r1 = 0;
+    if (lane < NC) {
+      one.wm[warp][lane] = -INFINITY;
+      one.wl[warp][lane] = 0.0f;
     }
-    if (tid == 0) pre[a.B] = carry;
     __syncthreads();
+  } else {
+    {   // cost prefix over sequences: sequence b owns H tiles segments of its plan's cost
+      long long carry = 0;
+      __shared__ long long wt[kW];
+      for (int base = 0; base < a.B; base += kThreads) {
+        const int b = base + tid;
+        const long long cnt = b < a.B ? static_cast<long long>(a.H) * a.tiles * plan_of<FMT>(a.seq_lens[b], a).cost : 0;
+        long long x = cnt;
+  #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (lane == 31) wt[warp] = x;
+        __syncthreads();
+        long long before = carry, total = 0;
+        for (int q = 0; q < kW; ++q) {
+          if (q < warp) before += wt[q];
+          total += wt[q];
+        }
+        if (b < a.B) pre[b] = before + x - cnt;
+        __syncthreads();
+        carry += total;
+      }
+      if (tid == 0) pre[a.B] = carry;
+      __syncthreads();
+    }
+    C = pre[a.B];
+    n_act = static_cast<int>(gridDim.x) * kW;
+    if (a.max_warps > 0 && a.max_warps < n_act) n_act = a.max_warps;
+    {
+      const long long cap = (C + kLeastUnits<FMT> - 1) / kLeastUnits<FMT>;
+      if (cap < n_act) n_act = static_cast<int>(cap);
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    gw = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    if (gw >= n_act) return;
+    r0 = gw * C / n_act;
+    r1 = (gw + 1) * C / n_act;
+    {   // first sequence touching this slice
+      int lo = 0, hi = a.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= r0) lo = mid; else hi = mid - 1;
+      }
+      b = lo;
+    }
+    T = a.seq_lens[b];
+    pl = plan_of<FMT>(T, a);
+    seg = static_cast<int>((r0 - pre[b]) / pl.cost);   // h * tiles + tile, within the sequence
+    seg_start = pre[b] + seg * pl.cost;
   }
-  const long long C = pre[a.B];
-  int n_act = static_cast<int>(gridDim.x) * kWinWarps;
-  if (a.max_warps > 0 && a.max_warps < n_act) n_act = a.max_warps;
-  {
-    const long long cap = (C + kMinUnits8<FMT> - 1) / kMinUnits8<FMT>;
-    if (cap < n_act) n_act = static_cast<int>(cap);
-  }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int gw = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-  if (gw >= n_act) return;
-  const long long r0 = gw * C / n_act, r1 = (gw + 1) * C / n_act;
 
   uint32_t phase = 0, pend = 0;   // per-stage wait parity and copies in flight (bit per stage)
   const uint64_t once = policy_evict_first();
@@ -772,25 +906,12 @@ __global__ void __launch_bounds__(32 * kWinWarps, 1) window_kernel(WindowArgs a)
       }
   };
 
-  int b;
-  {   // first sequence touching this slice
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= r0) lo = mid; else hi = mid - 1;
-    }
-    b = lo;
-  }
-  int T = a.seq_lens[b];
-  Plan pl = plan_of<FMT>(T, a);
-  int seg = static_cast<int>((r0 - pre[b]) / pl.cost);   // h * tiles + tile, within the sequence
-  long long seg_start = pre[b] + seg * pl.cost;
   const int ncols = a.nq * a.g;
 
   while (seg_start < r1) {
     const long long seg_end = seg_start + pl.cost;
     const long long lo = max(r0, seg_start) - seg_start, hi = min(r1, seg_end) - seg_start;
-    const bool own = lo == 0 && hi == pl.cost;
+    const bool own = !ONE && lo == 0 && hi == pl.cost;
     const int h = seg / a.tiles, col0 = (seg - h * a.tiles) * NC;
     const int slot = a.slot_ids ? a.slot_ids[b] : b;
     const bool slot_ok = slot >= 0 && slot < a.max_slots;
@@ -877,7 +998,7 @@ __global__ void __launch_bounds__(32 * kWinWarps, 1) window_kernel(WindowArgs a)
           }
           pend |= 1u << s;
         };
-        for (int i = 0; i < n && i < kStages8; ++i) issue(i, i);
+        for (int i = 0; i < n && i < kStagesOf<FMT>; ++i) issue(i, i);
         // queries: f16 operands, and (INT8) -128 scale sum_c q_c
         const float ks = FMT == 8 ? a.fp8_scale[h] : 1.0f;
         const float zscale = a.sm_scale_log2 * ks;
@@ -921,8 +1042,8 @@ __global__ void __launch_bounds__(32 * kWinWarps, 1) window_kernel(WindowArgs a)
               byte_block<FMT, NC, true>(rec, st, qa, zoff, zscale, cut, pos, opos);
             }
           }
-          if (i + kStages8 < n) issue(s, i + kStages8);
-          s = s + 1 == kStages8 ? 0 : s + 1;
+          if (i + kStagesOf<FMT> < n) issue(s, i + kStagesOf<FMT>);
+          s = s + 1 == kStagesOf<FMT> ? 0 : s + 1;
         }
         if (FMT == 8) {
           const float vs = a.fp8_scale[a.H + h];
@@ -955,9 +1076,10 @@ __global__ void __launch_bounds__(32 * kWinWarps, 1) window_kernel(WindowArgs a)
           f[c][e] = own ? (l > 0.0f ? 1.0f / l : l == l ? 0.0f : l) : 1.0f;
         }
       }
-      const bool direct = own || !slot_ok;
+      const bool direct = !ONE && (own || !slot_ok);
       const int k = seg_start <= r0 ? 0 : 1;
-      float* P = a.ws + (2LL * gw + k) * partial_floats(a.pcols);
+      float* P = ONE ? reinterpret_cast<float*>(region) : a.ws + (2LL * gw + k) * partial_floats(a.pcols);
+      if constexpr (ONE) __syncwarp();   // the region's records are read
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
 #pragma unroll
@@ -987,7 +1109,12 @@ __global__ void __launch_bounds__(32 * kWinWarps, 1) window_kernel(WindowArgs a)
             }
           }
         }
-        if (!direct && ti == 0 && col0 + 8 * c + gi < ncols) {
+        if (ONE) {
+          if (ti == 0) {
+            one.wm[warp][8 * c + gi] = st.m[c];
+            one.wl[warp][8 * c + gi] = st.l[c];
+          }
+        } else if (!direct && ti == 0 && col0 + 8 * c + gi < ncols) {
           P[a.pcols * kD + 2 * (8 * c + gi)] = st.m[c];
           P[a.pcols * kD + 2 * (8 * c + gi) + 1] = st.l[c];
         }
@@ -1141,9 +1268,9 @@ __global__ void __launch_bounds__(32 * kWinWarps, 1) window_kernel(WindowArgs a)
         }
       }
       if (!have) gen_init(gs);
-      const bool direct = own || !slot_ok;
+      const bool direct = !ONE && (own || !slot_ok);
       const int k = seg_start <= r0 ? 0 : 1;
-      float* P = a.ws + (2LL * gw + k) * partial_floats(a.pcols);
+      float* P = ONE ? reinterpret_cast<float*>(region) : a.ws + (2LL * gw + k) * partial_floats(a.pcols);
 #pragma unroll
       for (int j = 0; j < kNH; ++j) {
         if (col0 + j < ncols && j < a.pcols) {
@@ -1153,14 +1280,15 @@ __global__ void __launch_bounds__(32 * kWinWarps, 1) window_kernel(WindowArgs a)
           } else {
             *reinterpret_cast<float4*>(P + j * kD + 4 * lane) = make_float4(gs.o[j][0], gs.o[j][1], gs.o[j][2], gs.o[j][3]);
             if (lane == 0) {
-              P[a.pcols * kD + 2 * j] = gs.m[j];
-              P[a.pcols * kD + 2 * j + 1] = gs.l[j];
+              (ONE ? one.wm[warp][j] : P[a.pcols * kD + 2 * j]) = gs.m[j];
+              (ONE ? one.wl[warp][j] : P[a.pcols * kD + 2 * j + 1]) = gs.l[j];
             }
           }
         }
       }
       __syncwarp();   // the region is scratch until here
     }
+    if (ONE) break;
     if (seg_start >= r0 && lane == 0) {   // this warp holds the segment's first unit: its merge descriptor
       int ncon = 0;
       if (!own && slot_ok) ncon = owner_of(seg_end - 1, C, n_act) - gw + 1;
@@ -1178,30 +1306,42 @@ __global__ void __launch_bounds__(32 * kWinWarps, 1) window_kernel(WindowArgs a)
     }
   }
   if (pend) fail(-1);   // never expected: every issued copy is waited for
+  if constexpr (ONE) {
+    const int h = seg / a.tiles, col0 = (seg - h * a.tiles) * NC;
+    combine_cluster<FMT>(a, sm, one, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x), min(NC, ncols - col0),
+                         static_cast<long long>(b) * a.nq * a.Hq + h * a.g, col0, a.g);
+  }
 }
 
-// One warp per output row of a split segment: the contributors' partials combined
-// by the log-sum-exp rule, kMC at a time.
-__global__ void __launch_bounds__(32 * kMergeWarps) win_merge_kernel(DecodeArgs d, int window, int sinks, int tiles, int nc) {
-  (void)window;
-  (void)sinks;
+// The contributors' partials of a split segment combined by the log-sum-exp rule,
+// one output row an item. A warp takes kMC contributors at a time; with TEAM the
+// four warps of a CTA share one row's contributors (a call of few segments: each
+// has hundreds), otherwise each warp takes rows of its own.
+template <bool TEAM>
+__global__ void __launch_bounds__(32 * kMergeWarps) win_merge_kernel(DecodeArgs d, int tiles, int nc) {
+  __shared__ float4 so[TEAM ? kMergeWarps : 1][32];
+  __shared__ float sml[TEAM ? kMergeWarps : 1][2];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // window_kernel has completed; its writes are visible
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long* desc = reinterpret_cast<const long long*>(d.ws + 2LL * d.grid_warps * partial_floats(d.pcols));
   const int ncols = d.nq * d.g;
   const long long items = static_cast<long long>(d.B) * d.H * ncols, pf = partial_floats(d.pcols);
-  for (long long it = static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5); it < items;
-       it += static_cast<long long>(gridDim.x) * kMergeWarps) {
+  const long long it0 = TEAM ? blockIdx.x : static_cast<long long>(blockIdx.x) * kMergeWarps + warp;
+  const long long step = TEAM ? gridDim.x : static_cast<long long>(gridDim.x) * kMergeWarps;
+  constexpr int kShare = TEAM ? kMergeWarps : 1;   // warps of a row
+  const int mine = TEAM ? warp : 0;
+  for (long long it = it0; it < items; it += step) {
     const int col = static_cast<int>(it % ncols), tile = col / nc, j = col - tile * nc;
     const long long bh = it / ncols;
     const long long x = __ldcg(desc + bh * tiles + tile);
     const int n = static_cast<int>(x >> 32);
     if (n <= 0) continue;   // written by window_kernel
     const long long first = static_cast<long long>(static_cast<unsigned>(x & 0xffffffffLL));
+    // contributor 0 is the descriptor's slot; i >= 1 is the warp i places on, slot 0
     auto part = [&](int i) -> const float* { return d.ws + (i == 0 ? first : (first & ~1LL) + 2LL * i) * pf; };
     float M = -INFINITY, L = 0.0f;
     float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int i0 = 0; i0 < n; i0 += kMC) {
+    for (int i0 = mine * kMC; i0 < n; i0 += kShare * kMC) {
       const int nch = min(kMC, n - i0);
       const float* W = part(i0 + (lane < nch ? lane : 0)) + d.pcols * kD + 2 * j;
       const float mi = lane < nch ? __ldcg(W) : -INFINITY;
@@ -1223,6 +1363,32 @@ __global__ void __launch_bounds__(32 * kMergeWarps) win_merge_kernel(DecodeArgs 
       }
       M = mn;
     }
+    if constexpr (TEAM) {
+      so[warp][lane] = O;
+      if (lane == 0) {
+        sml[warp][0] = M;
+        sml[warp][1] = L;
+      }
+      __syncthreads();
+      if (warp == 0) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) mx = fmaxf(mx, sml[w][0]);
+        L = 0.0f;
+        O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kMergeWarps; ++w) {
+          const float l = sml[w][1];
+          if (l == 0.0f) continue;
+          const float f = mx == -INFINITY ? 1.0f : ex2(sml[w][0] - mx);
+          const float4 y = so[w][lane];
+          L = fmaf(f, l, L);
+          O = make_float4(fmaf(f, y.x, O.x), fmaf(f, y.y, O.y), fmaf(f, y.z, O.z), fmaf(f, y.w, O.w));
+        }
+      }
+      __syncthreads();
+      if (warp != 0) continue;
+    }
     const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
     const int q = col / d.g;
     const long long row = (bh / d.H * d.nq + q) * d.Hq + (bh % d.H) * d.g + (col - q * d.g);
@@ -1230,52 +1396,114 @@ __global__ void __launch_bounds__(32 * kMergeWarps) win_merge_kernel(DecodeArgs 
   }
 }
 
-template <int FMT, int NC, bool PACKED>
-cudaError_t run(const WindowArgs& a, int grid, cudaStream_t st) {
-  static size_t granted = 0;   // largest dynamic shared memory asked for so far
-  const size_t need = prefix_at<FMT>() + static_cast<size_t>(a.B + 1) * sizeof(long long);
-  if (need > granted) {
-    const void* f = reinterpret_cast<const void*>(window_kernel<FMT, NC, PACKED>);
-    cudaError_t e = prefer_max_shared(f);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(need));
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      return e;
-    }
-    granted = need;
+// Grants a kernel its dynamic shared memory (once per size increase).
+template <int FMT, int NC, bool PACKED, bool ONE>
+cudaError_t grant(size_t need) {
+  static size_t granted = 0;
+  if (need <= granted) return cudaSuccess;
+  const void* f = reinterpret_cast<const void*>(window_kernel<FMT, NC, PACKED, ONE>);
+  cudaError_t e = prefer_max_shared(f);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(need));
+  if (e == cudaSuccess && ONE) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) {
+    cudaGetLastError();   // leave no error behind for the caller's next CUDA call
+    return e;
   }
-  window_kernel<FMT, NC, PACKED><<<grid, 32 * kWinWarps, need, st>>>(a);
-  return cudaGetLastError();
+  granted = need;
+  return cudaSuccess;
+}
+template <int FMT> constexpr size_t kOneBytes = prefix_at<FMT>() + sizeof(OneSmem);
+template <int FMT, int NC, bool PACKED>
+cudaError_t one_ready() { return grant<FMT, NC, PACKED, true>(kOneBytes<FMT>); }
+
+// A launch of `segs` clusters of `cluster` CTAs.
+template <int FMT, int NC, bool PACKED>
+void one_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int cluster, int segs, cudaStream_t st) {
+  cfg->gridDim = dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(segs));
+  cfg->blockDim = dim3(32 * kWarpsOf<FMT>);
+  cfg->dynamicSmemBytes = kOneBytes<FMT>;
+  cfg->stream = st;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = cluster > 1 ? 1 : 0;
 }
 
-}  // namespace
+// Shape of a call: how many CTAs each segment takes in a launch that combines
+// itself, 0 for the slices of the line and a combine kernel.
+//
+// A call of few segments is bound by latency, and the second kernel and the pass
+// through the partials are much of it; a long one gains nothing from the fewer
+// launches and loses where sequences differ in length, as a CTA's segment is its
+// own. Measured (INT8, 8 kv heads, us, slices / clusters): 1 sequence of 2000
+// tokens 12.5 / 8.2, of 32000 27.5 / 24.0; 16 of 2000 22.7 / 15.1; 32 of 1024 to
+// 8192 tokens 55.9 / 63.5. So: at most one segment per SM, and at most kOneTokens
+// tokens per warp.
+constexpr int kOneTokens = 384;
+template <int FMT, int NC, bool PACKED>
+int cluster_of(const WindowArgs& a, int num_sms) {
+  const long long segs = static_cast<long long>(a.B) * a.H * a.tiles;
+  if (a.form == 1 || segs > 65535 || (a.form == 0 && segs > num_sms)) return 0;
+  const long long seen = static_cast<long long>(a.window) + a.nq + a.sinks;
+  const long long blocks = (a.max_seq_len < seen ? a.max_seq_len : seen) / kBlock<FMT> + 2;   // of a segment, at most
+  int c = 1;
+  while (c < 8 && 2 * c * segs <= num_sms && blocks > static_cast<long long>(c) * kWarpsOf<FMT>) c *= 2;
+  if (c == 8 && segs <= 6 && blocks > 16LL * kWarpsOf<FMT>) {
+    // clusters of 16 fill a GPC each: only where every one of them is resident at once
+    static int resident = -1;
+    if (resident < 0) {
+      cudaLaunchConfig_t cfg = {};
+      cudaLaunchAttribute attr[1];
+      one_config<FMT, NC, PACKED>(&cfg, attr, 16, 1, nullptr);
+      int n = 0;
+      if (one_ready<FMT, NC, PACKED>() != cudaSuccess ||
+          cudaOccupancyMaxActiveClusters(&n, window_kernel<FMT, NC, PACKED, true>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+      }
+      resident = n;
+    }
+    if (segs <= resident) c = 16;
+  }
+  if (a.form == 0 && blocks * kBlock<FMT> > static_cast<long long>(c) * kWarpsOf<FMT> * kOneTokens) return 0;
+  return c;
+}
 
-int window_warps_per_cta() { return kWinWarps; }
-int window_cols(int bits, int cols) { return (bits == 8 || bits == kI8) && cols > 8 ? 16 : 8; }
-
-cudaError_t launch_window(const WindowArgs& a, int grid, cudaStream_t st) {
-  const int cols = a.nq * a.g, nc = window_cols(a.bits, cols);
+template <int FMT, int NC, bool PACKED>
+cudaError_t run_call(const WindowArgs& a, int num_sms, cudaStream_t st) {
+  if (const int cluster = cluster_of<FMT, NC, PACKED>(a, num_sms)) {
+    const cudaError_t e = one_ready<FMT, NC, PACKED>();
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    one_config<FMT, NC, PACKED>(&cfg, attr, cluster, a.B * a.H * a.tiles, st);
+    return cudaLaunchKernelEx(&cfg, window_kernel<FMT, NC, PACKED, true>, a);
+  }
   // No more CTAs than the work can use (slices go to one warp of every CTA first):
   // a sequence has at most the blocks of max_seq_len, or of window, queries and
   // sinks, and each end of a range may cut one more.
-  {
-    const bool kivi = a.bits != 8 && a.bits != kI8;
-    const long long bt = kivi ? kG : kP, seen = static_cast<long long>(a.window) + a.nq + a.sinks;
-    long long units = (a.max_seq_len < seen ? a.max_seq_len : seen) / bt + 5;
-    if (kivi) units += static_cast<long long>(a.tail_cost - 1) * ((a.R + 2 * kG) / kG + 5);
-    const long long warps = (units * a.B * a.H * a.tiles + 2) / 3;   // 3: the least work of a warp
-    if (warps < grid) grid = static_cast<int>(warps);
-  }
-  cudaError_t e;
-  if (a.bits == kI8) e = nc == 16 ? run<kI8, 16, false>(a, grid, st) : run<kI8, 8, false>(a, grid, st);
-  else if (a.bits == 8) e = nc == 16 ? run<8, 16, false>(a, grid, st) : run<8, 8, false>(a, grid, st);
-  else if (a.bits == 2) e = cols <= 4 ? run<2, 8, true>(a, grid, st) : run<2, 8, false>(a, grid, st);
-  else e = cols <= 4 ? run<4, 8, true>(a, grid, st) : run<4, 8, false>(a, grid, st);
+  int grid = num_sms;
+  const long long seen = static_cast<long long>(a.window) + a.nq + a.sinks;
+  long long units = (a.max_seq_len < seen ? a.max_seq_len : seen) / kBlock<FMT> + 5;
+  if (!kByte<FMT>) units += static_cast<long long>(a.tail_cost - 1) * ((a.R + 2 * kG) / kG + 5);
+  const long long segs = static_cast<long long>(a.B) * a.H * a.tiles;
+  const long long warps = (units * segs + kLeastUnits<FMT> - 1) / kLeastUnits<FMT>;
+  if (warps < grid) grid = static_cast<int>(warps);
+  const size_t smem = prefix_at<FMT>() + static_cast<size_t>(a.B + 1) * sizeof(long long);
+  cudaError_t e = grant<FMT, NC, PACKED, false>(smem);
+  if (e != cudaSuccess) return e;
+  window_kernel<FMT, NC, PACKED, false><<<grid, 32 * kWarpsOf<FMT>, smem, st>>>(a);
+  e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the combine, launched programmatically right behind
-  long long blocks = (static_cast<long long>(a.B) * a.H * cols + kMergeWarps - 1) / kMergeWarps;
-  if (blocks > 16LL * grid) blocks = 16LL * grid;
-  e = prefer_max_shared(reinterpret_cast<const void*>(win_merge_kernel));
+  const long long items = static_cast<long long>(a.B) * a.H * a.nq * a.g;
+  const bool team = static_cast<long long>(grid) * kWarpsOf<FMT> > 16 * segs;   // more than 16 partials a segment
+  void (*f)(DecodeArgs, int, int) = team ? win_merge_kernel<true> : win_merge_kernel<false>;
+  long long blocks = team ? items : (items + kMergeWarps - 1) / kMergeWarps;
+  if (blocks > 16LL * num_sms) blocks = 16LL * num_sms;
+  e = prefer_max_shared(reinterpret_cast<const void*>(f));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
@@ -1286,7 +1514,23 @@ cudaError_t launch_window(const WindowArgs& a, int grid, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, win_merge_kernel, static_cast<const DecodeArgs&>(a), a.window, a.sinks, a.tiles, nc);
+  return cudaLaunchKernelEx(&cfg, f, static_cast<const DecodeArgs&>(a), a.tiles, NC);
+}
+
+}  // namespace
+
+int window_warps_per_sm() { return kMaxWarps; }
+int window_cols(int bits, int cols) { return (bits == 8 || bits == kI8) && cols > 8 ? 16 : 8; }
+
+cudaError_t launch_window(const WindowArgs& a, int num_sms, cudaStream_t st) {
+  const int cols = a.nq * a.g;
+  const bool wide = window_cols(a.bits, cols) == 16;
+  switch (a.bits) {
+    case kI8: return wide ? run_call<kI8, 16, false>(a, num_sms, st) : run_call<kI8, 8, false>(a, num_sms, st);
+    case 8: return wide ? run_call<8, 16, false>(a, num_sms, st) : run_call<8, 8, false>(a, num_sms, st);
+    case 2: return cols <= 4 ? run_call<2, 8, true>(a, num_sms, st) : run_call<2, 8, false>(a, num_sms, st);
+    default: return cols <= 4 ? run_call<4, 8, true>(a, num_sms, st) : run_call<4, 8, false>(a, num_sms, st);
+  }
 }
 
 }  // namespace s4kv

@@ -10,6 +10,17 @@ from plain_cache import INT8, Filled, check, int8_rows, restored
 pytestmark = pytest.mark.gpu
 
 
+@pytest.fixture(params=[1, 2], ids=["slices", "clusters"])
+def form(request, monkeypatch):
+    """A test runs on both launch forms."""
+    make = s4.KVCache.__init__
+
+    def init(self, *a, **kw):
+        make(self, *a, **kw)
+        self.set_option(s4.S4KV_OPT_WINDOW_FORM, request.param)
+    monkeypatch.setattr(s4.KVCache, "__init__", init)
+
+
 def _queries(seed, B, nq, Hq, dtype):
     return torch.randn(B, nq, Hq, 128, generator=inp.gen(seed), dtype=torch.float32).to(dtype).cuda()
 
@@ -89,7 +100,7 @@ def test_a_block_that_is_not_finite_restores_to_such_values_and_no_other_does():
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("H,g", [(1, 1), (2, 4), (3, 5), (4, 7), (1, 8)])
-def test_decode(dtype, H, g):
+def test_decode(dtype, H, g, form):
     lens = [1, 15, 16, 17, 0, 255, 257, 1000, 2049]
     f = Filled(lens, H=H, bits=INT8, dtype=dtype, seed=11 + g, slots=[8, 7, 6, 5, 4, 3, 2, 1, 0])
     q = _queries(3, len(lens), 1, H * g, f.dtype)
@@ -105,7 +116,7 @@ def test_decode(dtype, H, g):
 
 @pytest.mark.parametrize("nq,H,g", [(2, 1, 3), (4, 2, 4), (5, 1, 2), (16, 1, 6), (16, 3, 1), (3, 2, 8)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-def test_multi_query(nq, H, g, dtype):
+def test_multi_query(nq, H, g, dtype, form):
     lens = [nq, nq + 1, 16 + nq, 31, 64, 333, 1500]
     lens = [max(n, nq) for n in lens]
     f = Filled(lens, H=H, bits=INT8, dtype=dtype, seed=30 + nq, chunks=[7, 100])
@@ -116,7 +127,7 @@ def test_multi_query(nq, H, g, dtype):
         check(out[b], q[b], *f.plain(b), range(n - nq, n), INT8, what=f"seq {b} of {n}")
 
 
-def test_decode_splits_agree_with_one_worker():
+def test_decode_splits_agree_with_one_worker(form):
     """The same call on one worker warp and on all: the combine changes roundings only."""
     f = Filled([4000], H=2, bits=INT8, seed=2)
     q = _queries(5, 1, 1, 8, f.dtype)
@@ -130,7 +141,7 @@ def test_decode_splits_agree_with_one_worker():
     assert torch.equal(all_, f.cache.decode(0, q[:, 0], f.bt, f.seq, 4000))   # no order depends on timing
 
 
-def test_decode_step_and_noalloc_equal_append_and_decode():
+def test_decode_step_and_noalloc_equal_append_and_decode(form):
     lens = [0, 14, 15, 16, 200]
     f = Filled(lens, H=2, bits=INT8, seed=21, spare=40)
     g = Filled(lens, H=2, bits=INT8, seed=21, spare=40)
@@ -158,7 +169,7 @@ def test_decode_step_and_noalloc_equal_append_and_decode():
             for a, b in zip(f.cache.dequant(0, i, f.bt[i], n + 20), g.cache.dequant(0, i, g.bt[i], n + 20)))
 
 
-def test_bad_caller_data_is_reported():
+def test_bad_caller_data_is_reported(form):
     f = Filled([100, 50], H=2, bits=INT8, seed=1, spare=20)
     q = _queries(1, 2, 1, 4, f.dtype)[:, 0].contiguous()
 
@@ -198,7 +209,7 @@ def test_bad_caller_data_is_reported():
     f.ok()
 
 
-def test_bounded_wait_gives_up_and_the_next_call_is_clean():
+def test_bounded_wait_gives_up_and_the_next_call_is_clean(form):
     f = Filled([3000, 2500], H=2, bits=INT8, seed=6)
     q = _queries(2, 2, 1, 8, f.dtype)[:, 0].contiguous()
     good = f.cache.decode(0, q, f.bt, f.seq, 3000)

@@ -18,6 +18,18 @@ def _scales(bits, H):
     return ([0.5 + 0.25 * h for h in range(H)], [1.5 - 0.25 * h for h in range(H)]) if bits == 8 else None
 
 
+@pytest.fixture(params=[1, 2], ids=["slices", "clusters"], autouse=True)
+def form(request, monkeypatch):
+    """Every test runs on both launch forms."""
+    make = s4.KVCache.__init__
+
+    def init(self, *a, **kw):
+        make(self, *a, **kw)
+        self.set_option(s4.S4KV_OPT_WINDOW_FORM, request.param)
+    monkeypatch.setattr(s4.KVCache, "__init__", init)
+    return request.param
+
+
 def _all(f, q, window, sinks, what="", **kw):
     B, nq = q.shape[:2]
     out = f.cache.window(0, q, f.bt, f.seq, max(f.lens), window, sinks, slot_ids=f.slots, **kw)
