@@ -1054,29 +1054,19 @@ __device__ __forceinline__ void turn_tile(const RopeArgs& r, uint8_t* Ks, int t0
   }
 }
 
-// Query rows row0, row0 + step, ... of the call turned (s4kv_append_rope), one warp each.
-__device__ __forceinline__ void turn_queries(const AppendArgs& a, int row0, int step) {
-  const int lane = threadIdx.x & 31;
-  for (int row = row0; row < a.num_new; row += step) {
-    int lo = 0, hi = a.n;   // the last i with cu_new[i] <= row, 32 probes a round
-    while (hi - lo > 1) {
-      const int gap = (hi - lo + 31) / 32, at = lo + gap * (lane + 1);
-      const int k = __ffs(__ballot_sync(0xffffffffu, at >= hi || a.cu_new[at] > row)) - 1;
-      lo += gap * k;
-      hi = min(hi, lo + gap);
-    }
-    const int T0 = a.seq_lens_before[lo], c0 = a.cu_new[lo];
-    if (T0 + a.cu_new[lo + 1] - c0 <= a.rope.max_pos) rope::query_row(a.rope, row, T0 + row - c0, a.dtype);
-  }
+// This CTA's share of the queries to turn (s4kv_append_rope), one warp an item.
+template <int DT>
+__device__ __forceinline__ void turn_queries(const AppendArgs& a) {
+  const long long items = rope::query_items(a.rope, a.num_new);
+  for (long long it = static_cast<long long>(threadIdx.x >> 5) * gridDim.x + blockIdx.x; it < items;
+       it += static_cast<long long>(gridDim.x) * (kThreads / 32))
+    rope::query_item<DT>(a, it);
 }
 
-// CTAs of a rotating append that turn queries: the last ones of the grid (KIVI and
-// FP8 pages), a warp for every row up to a resident wave.
-__host__ __device__ inline int query_ctas(const AppendArgs& a) {
-  if (!a.rope.q) return 0;
-  const int want = (a.num_new + kThreads / 32 - 1) / (kThreads / 32);
-  return want < 608 ? want : 608;
-}
+// Whether a CTA turns its share of the queries before its items or after them. Items
+// are bound by instructions and latency, queries by bytes: with one in two of an
+// SM's CTAs at each, they run side by side.
+__device__ __forceinline__ bool queries_first(const AppendArgs& a) { return (blockIdx.x / a.num_sms) & 1; }
 
 template <int BITS, int DT, bool ROPE = false>
 __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArgs a) {
@@ -1091,22 +1081,21 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArg
   float* prm = reinterpret_cast<float*>(staging + kStagingBytes);
 
   if (!build_prefix(a, pre, warp_tot, seq, cpre)) return;
-  int grid = gridDim.x;   // CTAs that share the items
   if constexpr (ROPE) {
-    const int nq = query_ctas(a);
-    grid -= nq;
-    if (static_cast<int>(blockIdx.x) >= grid) {
-      turn_queries(a, (blockIdx.x - grid) * (kThreads / 32) + (threadIdx.x >> 5), nq * (kThreads / 32));
-      return;
-    }
+    if (queries_first(a)) turn_queries<DT>(a);
   }
   // A CTA takes the items that start in its slice of the work line, in order;
   // whole new tiles are loaded kNumStages - 1 items ahead (one cp.async group per
   // item, empty for other items).
   const long long C = cpre[a.n];
-  int item = item_from_cost(a, pre, seq, cpre, C * blockIdx.x / grid);
-  const int total = item_from_cost(a, pre, seq, cpre, C * (blockIdx.x + 1) / grid);   // this CTA's end
-  if (item >= total) return;
+  int item = item_from_cost(a, pre, seq, cpre, C * blockIdx.x / gridDim.x);
+  const int total = item_from_cost(a, pre, seq, cpre, C * (blockIdx.x + 1) / gridDim.x);   // this CTA's end
+  if (item >= total) {
+    if constexpr (ROPE) {
+      if (!queries_first(a)) turn_queries<DT>(a);
+    }
+    return;
+  }
   constexpr int kAhead = kNumStages - 1;
   const int step = 1;
   Item i0 = item_of(a, pre, seq, item), i1;
@@ -1160,6 +1149,9 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArg
     s = s + 1 == kNumStages ? 0 : s + 1;
   }
   cp_async_wait_all();
+  if constexpr (ROPE) {
+    if (!queries_first(a)) turn_queries<DT>(a);
+  }
 }
 
 // ---- FP8 E4M3 pages ("4.4 KV Cache 量化", sections 4.1 and 4.2) ------------------
@@ -1172,23 +1164,17 @@ __device__ __forceinline__ uint32_t e4m3_of(float x, float scale) {
   return static_cast<uint32_t>(__nv_cvt_float_to_fp8(__fdiv_rn(x, scale), __NV_SATFINITE, __NV_E4M3));
 }
 
-template <bool ROPE>
+template <bool ROPE, int DT>
 __global__ void __launch_bounds__(kThreads) append_fp8_kernel(AppendArgs a) {
   extern __shared__ int pre[];   // [n + 1]
   __shared__ int warp_tot[kThreads / 32];
   if (!build_prefix(a, pre, warp_tot)) return;
   const int total = pre[a.n];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  int grid = gridDim.x;   // CTAs that share the items
   if constexpr (ROPE) {
-    const int nq = query_ctas(a);
-    grid -= nq;
-    if (static_cast<int>(blockIdx.x) >= grid) {
-      turn_queries(a, (blockIdx.x - grid) * (kThreads / 32) + warp, nq * (kThreads / 32));
-      return;
-    }
+    if (queries_first(a)) turn_queries<DT>(a);
   }
-  for (int item = blockIdx.x; item < total; item += grid) {
+  for (int item = blockIdx.x; item < total; item += gridDim.x) {
     int lo_i = 0, hi_i = a.n - 1;   // last i with pre[i] <= item
     while (lo_i < hi_i) {
       const int mid = (lo_i + hi_i + 1) >> 1;
@@ -1270,6 +1256,9 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(AppendArgs a) {
         }
       }
     }
+  }
+  if constexpr (ROPE) {
+    if (!queries_first(a)) turn_queries<DT>(a);
   }
 }
 
@@ -1380,15 +1369,25 @@ __global__ void __launch_bounds__(kThreads) dequant_kernel(DequantArgs a) {
 
 int append_ctas_per_sm() { return kAppendCtas; }
 
+// CTAs of an append: those of its items, and enough warps for its queries up to a
+// resident wave.
+static int with_queries(const AppendArgs& a, int grid) {
+  const long long items = rope::query_items(a.rope, a.num_new), want = (items + kThreads / 32 - 1) / (kThreads / 32);
+  const long long wave = static_cast<long long>(a.num_sms) * kAppendCtas;
+  return static_cast<int>(want <= grid ? grid : want < wave ? want : grid < wave ? wave : grid);
+}
+
 cudaError_t launch_append(const AppendArgs& a, int grid, cudaStream_t st) {
   if (a.n <= 0 || grid <= 0) return cudaSuccess;
   if (a.n > kMaxSeqsPerCall) return cudaErrorInvalidValue;
   if (a.bits == 8) {
     const size_t smem = static_cast<size_t>(a.n + 1) * sizeof(int);
-    void (*f)(AppendArgs) = a.rope.table ? append_fp8_kernel<true> : append_fp8_kernel<false>;
+    void (*f)(AppendArgs) = !a.rope.table           ? append_fp8_kernel<false, S4KV_F16>
+                            : a.dtype == S4KV_BF16 ? append_fp8_kernel<true, S4KV_BF16>
+                                                   : append_fp8_kernel<true, S4KV_F16>;
     const cudaError_t c = prefer_max_shared(reinterpret_cast<const void*>(f));
     if (c != cudaSuccess) return c;
-    f<<<grid + query_ctas(a), kThreads, smem, st>>>(a);
+    f<<<with_queries(a, grid), kThreads, smem, st>>>(a);
     return cudaGetLastError();
   }
   const int smem = append_smem_bytes(a.n);
@@ -1416,7 +1415,7 @@ cudaError_t launch_append(const AppendArgs& a, int grid, cudaStream_t st) {
       raised[dev][v] = smem;
     }
   }
-  kern<<<grid + query_ctas(a), kThreads, smem, st>>>(a);
+  kern<<<with_queries(a, grid), kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -114,6 +114,7 @@ struct AppendArgs {
   int bits;                 // code width: 4, 2 or 8 (FP8), or S4KV_BITS_INT8
   const float* fp8_scale;   // FP8: this layer's scales, key [H] then value [H]
   RopeArgs rope;
+  int num_sms;
   int step;                 // INT8 pages, decode step: one row per sequence, seq_lens_before holds the
   int max_len;              // lengths after it, each at most max_len
 };

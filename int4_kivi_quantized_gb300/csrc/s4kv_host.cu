@@ -372,6 +372,7 @@ int append_call(s4kv_cache* cache, int layer, const RopeArgs& rope, const void* 
   a.bits = cache->bits;
   a.fp8_scale = fp8_scales_of(cache, layer);
   a.rope = rope;
+  a.num_sms = cache->num_sms;
   a.step = 0;
   a.max_len = 0;
   if (cache->bits == S4KV_BITS_INT8) {

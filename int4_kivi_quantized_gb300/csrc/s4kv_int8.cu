@@ -12,7 +12,7 @@
 //  * the edge of a (sequence, head): the block that ring rows and new rows
 //    complete together, then the rows left over into the rings (one warp, so ring
 //    rows are read before they are overwritten), and the stored length;
-//  * with a rotation, one query row.
+//  * with a rotation, 16 heads of one query row.
 // This unit is compiled without FMA contraction; every rounding is spelled out.
 
 #include "s4kv_common.cuh"
@@ -27,7 +27,9 @@ constexpr int kThreads = 32 * kWarps;
 #ifndef S4KV_INT8_CTAS
 #define S4KV_INT8_CTAS 4
 #endif
-constexpr int kCtas = S4KV_INT8_CTAS;   // resident CTAs per SM the registers are budgeted for
+// Resident CTAs per SM the registers are budgeted for: a rotation holds 32 angles
+// beside the block's 64 words.
+template <bool ROPE> constexpr int kCtas = ROPE ? 3 : S4KV_INT8_CTAS;
 constexpr float kTiny = 7.8886091e-31f;   // 2^-100
 // 1.5 * 2^23 + 128: t + kMagic has round_half_even(t) + 128 in its low byte
 constexpr float kMagic = 12583040.0f;
@@ -147,18 +149,28 @@ __device__ __forceinline__ void whole_block(const AppendArgs& a, const Seq& s, i
   }
   char* rec = record(a, s, page, h);
   if constexpr (ROPE) {
+    if (a.rope.interleaved || a.rope.dim == kD) {
+      // a lane's chunks c and c + 8 are a unit of the rotation; the next row's angles
+      // load while this one turns
+      rope::Unit u[2];
+      rope::unit_chunks(a.rope, kc, u[0]);
+      u[1] = u[0];
+      rope::unit_angles(a.rope, t0 + kr, u[0]);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int x = 4 * r + kr;
-      if (x >= ring_rows) {
-        const uint4* row = reinterpret_cast<const uint4*>(kin + x * step);
-        uint4 lo = k[2 * r], hi = k[2 * r + 1], plo = hi, phi = lo;
-        if (!a.rope.interleaved && a.rope.dim != kD) {   // the pair's other chunk is another lane's
-          plo = row[rope::partner(a.rope, kc)];
-          phi = row[rope::partner(a.rope, kc + 8)];
+      for (int r = 0; r < 4; ++r) {
+        if (r < 3) rope::unit_angles(a.rope, t0 + 4 * (r + 1) + kr, u[(r + 1) & 1]);
+        if (4 * r + kr >= ring_rows) rope::turn_unit<DT>(a.rope, u[r & 1], k[2 * r], k[2 * r + 1]);
+      }
+    } else {   // a pair's other chunk is another lane's
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int x = 4 * r + kr;
+        if (x >= ring_rows) {
+          const uint4* row = reinterpret_cast<const uint4*>(kin + x * step);
+          const uint4 plo = row[rope::partner(a.rope, kc)], phi = row[rope::partner(a.rope, kc + 8)];
+          k[2 * r] = rope::turn(a.rope, t0 + x, kc, k[2 * r], plo, DT);
+          k[2 * r + 1] = rope::turn(a.rope, t0 + x, kc + 8, k[2 * r + 1], phi, DT);
         }
-        k[2 * r] = rope::turn(a.rope, t0 + x, kc, lo, plo, DT);
-        k[2 * r + 1] = rope::turn(a.rope, t0 + x, kc + 8, hi, phi, DT);
       }
     }
   }
@@ -234,26 +246,8 @@ __device__ __forceinline__ void edge(const AppendArgs& a, int i, int h) {
   if (lane == 0) __stcg(a.lens + s.slot * a.H + h, s.T1);
 }
 
-// Sequence that owns input row r: the last i with cu_new[i] <= r (32 probes a round).
-__device__ __forceinline__ int sequence_of(const AppendArgs& a, int r) {
-  if (a.step) return r;
-  const int lane = threadIdx.x & 31;
-  int lo = 0, hi = a.n;   // cu_new[lo] <= r, and hi is the end or past r
-  while (hi - lo > 1) {
-    const int gap = (hi - lo + 31) / 32;
-    const int at = lo + gap * (lane + 1);
-    const unsigned past = __ballot_sync(0xffffffffu, at >= hi || a.cu_new[at] > r);
-    const int k = past ? __ffs(past) - 1 : 32;
-    const int nlo = lo + gap * k;
-    if (k < 32) hi = min(hi, nlo + gap);
-    lo = nlo;
-  }
-  return lo;
-}
-
 template <int DT, bool ROPE>
-__global__ void __launch_bounds__(kThreads, kCtas) append_int8_kernel(AppendArgs a) {
-  const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kThreads, kCtas<ROPE>) append_int8_kernel(AppendArgs a) {
   if (!a.step) {   // a malformed call (see s4kv_append): nothing is read or written
     int bad = a.cu_new[0] != 0 || a.cu_new[a.n] != a.num_new;
     for (int i = threadIdx.x; i < a.n; i += kThreads) {
@@ -273,13 +267,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_int8_kernel(AppendArgs
   const int slots = a.step ? 0 : (a.num_new + kP - 1) / kP;
   const long long blocks = static_cast<long long>(slots) * a.H;
   const long long edges = blocks + static_cast<long long>(a.n) * a.H;
-  const long long total = edges + (ROPE && a.rope.q ? a.num_new : 0);
+  const long long total = edges + (ROPE ? rope::query_items(a.rope, a.num_new) : 0);
   for (long long it = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5); it < total;
        it += static_cast<long long>(gridDim.x) * kWarps) {
     if (it < blocks) {
       const int slot = static_cast<int>(it / a.H), h = static_cast<int>(it - static_cast<long long>(slot) * a.H);
       const int row = slot * kP;
-      const int i = sequence_of(a, row);
+      const int i = rope::sequence_of_row(a.cu_new, a.n, row);
       const int page = (a.seq_lens_before[i] + row - a.cu_new[i]) / kP;
       const Seq s = sequence<ROPE>(a, i, h, false);
       if (s.ok && page * kP >= s.T0 && page * kP + kP <= s.T1) whole_block<DT, ROPE>(a, s, h, page, 0);
@@ -287,28 +281,24 @@ __global__ void __launch_bounds__(kThreads, kCtas) append_int8_kernel(AppendArgs
       const long long e = it - blocks;
       edge<DT, ROPE>(a, static_cast<int>(e / a.H), static_cast<int>(e % a.H));
     } else if constexpr (ROPE) {
-      const int row = static_cast<int>(it - edges);
-      const int i = sequence_of(a, row);
-      const int T0 = a.seq_lens_before[i], c0 = a.cu_new[i];
-      if (T0 + a.cu_new[i + 1] - c0 <= a.rope.max_pos) rope::query_row(a.rope, row, T0 + row - c0, DT);
+      rope::query_item<DT>(a, it - edges);
     }
     __syncwarp();
   }
-  (void)lane;
 }
 
 }  // namespace
 
 cudaError_t launch_append_int8(const AppendArgs& a, int num_sms, cudaStream_t st) {
-  const bool rope = a.rope.table != nullptr;
+  const bool turn = a.rope.table != nullptr;
   void (*kern)(AppendArgs);
-  if (a.dtype == S4KV_BF16) kern = rope ? append_int8_kernel<S4KV_BF16, true> : append_int8_kernel<S4KV_BF16, false>;
-  else kern = rope ? append_int8_kernel<S4KV_F16, true> : append_int8_kernel<S4KV_F16, false>;
+  if (a.dtype == S4KV_BF16) kern = turn ? append_int8_kernel<S4KV_BF16, true> : append_int8_kernel<S4KV_BF16, false>;
+  else kern = turn ? append_int8_kernel<S4KV_F16, true> : append_int8_kernel<S4KV_F16, false>;
   const cudaError_t c = prefer_max_shared(reinterpret_cast<const void*>(kern));
   if (c != cudaSuccess) return c;
   const long long slots = a.step ? 0 : (a.num_new + kP - 1) / kP;
-  const long long items = (slots + a.n) * a.H + (rope && a.rope.q ? a.num_new : 0);
-  const long long want = (items + kWarps - 1) / kWarps, cap = static_cast<long long>(num_sms) * kCtas;
+  const long long items = (slots + a.n) * a.H + rope::query_items(a.rope, a.num_new);
+  const long long want = (items + kWarps - 1) / kWarps, cap = static_cast<long long>(num_sms) * (turn ? kCtas<true> : kCtas<false>);
   kern<<<static_cast<unsigned>(want < cap ? want : cap), kThreads, 0, st>>>(a);
   return cudaGetLastError();
 }

@@ -90,24 +90,124 @@ __device__ __forceinline__ uint4 turned_chunk(const RopeArgs& r, const uint16_t*
   return turn(r, pos, c, x, p == c ? x : w[p], dtype);
 }
 
-// Query row `row` (Hq heads of one token, at position pos) of q into q_out, by
-// one warp; chunk pairs are read whole before either is written, so q_out may be q.
-__device__ __forceinline__ void query_row(const RopeArgs& r, long long row, int pos, int dtype) {
+// What one lane turns of every head of a row: two chunks A and B and their angles.
+// A head's 16 chunks are eight such units: the pairs of the rotation (u, u + half)
+// and, past the rotated channels, plain neighbours; with interleaved pairs each
+// chunk turns by itself (A by c, s 0..3, B by 4..7).
+struct Unit {
+  int A, B;
+  bool turnA, turnB;
+  float c[8], s[8];
+};
+
+__device__ __forceinline__ void unit_chunks(const RopeArgs& r, int u, Unit& x) {
+  const int half = r.dim >> 4;
+  if (r.interleaved) {
+    x.A = u;
+    x.B = u + 8;
+    x.turnA = x.A < 2 * half;
+    x.turnB = x.B < 2 * half;
+  } else {
+    x.turnA = x.turnB = u < half;
+    x.A = u < half ? u : 2 * u;
+    x.B = u < half ? u + half : 2 * u + 1;
+  }
+}
+
+__device__ __forceinline__ void unit_angles(const RopeArgs& r, int pos, Unit& x) {
+  const float* row = r.table + static_cast<long long>(pos) * r.dim;
+  const int half = r.dim >> 1;
+  if (!x.turnA) return;   // (B turns only where A does)
+  const int a = r.interleaved ? 4 * x.A : 8 * x.A, b = r.interleaved ? (x.turnB ? 4 * x.B : a) : a + 4;
+  const float4 c0 = __ldg(reinterpret_cast<const float4*>(row + a)), c1 = __ldg(reinterpret_cast<const float4*>(row + b));
+  const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + half + a)), s1 = __ldg(reinterpret_cast<const float4*>(row + half + b));
+  x.c[0] = c0.x; x.c[1] = c0.y; x.c[2] = c0.z; x.c[3] = c0.w;
+  x.c[4] = c1.x; x.c[5] = c1.y; x.c[6] = c1.z; x.c[7] = c1.w;
+  x.s[0] = s0.x; x.s[1] = s0.y; x.s[2] = s0.z; x.s[3] = s0.w;
+  x.s[4] = s1.x; x.s[5] = s1.y; x.s[6] = s1.z; x.s[7] = s1.w;
+}
+
+// The unit's chunks, turned in place.
+template <int DT>
+__device__ __forceinline__ void turn_unit(const RopeArgs& r, const Unit& x, uint4& A, uint4& B) {
+  if (!x.turnA) return;
+  float a[8], b[8], p[8], q[8];
+  widen8(A, DT, a);
+  widen8(B, DT, b);
+  if (r.interleaved) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[2 * i] = __fsub_rn(__fmul_rn(a[2 * i], x.c[i]), __fmul_rn(a[2 * i + 1], x.s[i]));
+      p[2 * i + 1] = __fadd_rn(__fmul_rn(a[2 * i + 1], x.c[i]), __fmul_rn(a[2 * i], x.s[i]));
+      q[2 * i] = __fsub_rn(__fmul_rn(b[2 * i], x.c[4 + i]), __fmul_rn(b[2 * i + 1], x.s[4 + i]));
+      q[2 * i + 1] = __fadd_rn(__fmul_rn(b[2 * i + 1], x.c[4 + i]), __fmul_rn(b[2 * i], x.s[4 + i]));
+    }
+    A = round8(p, DT);
+    if (x.turnB) B = round8(q, DT);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      p[i] = __fsub_rn(__fmul_rn(a[i], x.c[i]), __fmul_rn(b[i], x.s[i]));
+      q[i] = __fadd_rn(__fmul_rn(b[i], x.c[i]), __fmul_rn(a[i], x.s[i]));
+    }
+    A = round8(p, DT);
+    B = round8(q, DT);
+  }
+}
+
+// Sequence that owns input row `row`: the last i with cu_new[i] <= row, 32 probes
+// a round, by one warp.
+__device__ __forceinline__ int sequence_of_row(const int* cu_new, int n, int row) {
   const int lane = threadIdx.x & 31;
-  const uint4* src = reinterpret_cast<const uint4*>(r.q + row * r.Hq * kD);
-  uint4* dst = reinterpret_cast<uint4*>(r.q_out + row * r.Hq * kD);
-  const int n = r.Hq * 16;   // chunks of the row; a head's 16 sit in half a warp
-  for (int base = 0; base < n; base += 32) {
-    const int i = base + lane, c = i & 15;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (i < n) x = src[i];
-    const int from = (lane & 16) | partner(r, c);
-    uint4 y;
-    y.x = __shfl_sync(0xffffffffu, x.x, from);
-    y.y = __shfl_sync(0xffffffffu, x.y, from);
-    y.z = __shfl_sync(0xffffffffu, x.z, from);
-    y.w = __shfl_sync(0xffffffffu, x.w, from);
-    if (i < n) dst[i] = turn(r, pos, c, x, y, dtype);
+  int lo = 0, hi = n;   // cu_new[lo] <= row, and hi is the end or past it
+  while (hi - lo > 1) {
+    const int gap = (hi - lo + 31) / 32, at = lo + gap * (lane + 1);
+    const int k = __ffs(__ballot_sync(0xffffffffu, at >= hi || cu_new[at] > row)) - 1;
+    lo += gap * k;
+    hi = min(hi, lo + gap);
+  }
+  return lo;
+}
+
+// Queries of a call: items of one row and kQueryHeads heads, a warp each. All of an
+// item's loads are in flight together (the rotation is nothing but bytes), its
+// angles are read once for the item's heads, and every chunk is read before its
+// pair is written, so q_out may be q.
+constexpr int kQueryHeads = 16;
+__host__ __device__ __forceinline__ long long query_items(const RopeArgs& r, int rows) {
+  return r.q ? static_cast<long long>(rows) * ((r.Hq + kQueryHeads - 1) / kQueryHeads) : 0;
+}
+template <int DT>
+__device__ __forceinline__ void query_item(const AppendArgs& a, long long item) {
+  const RopeArgs& r = a.rope;
+  const int lane = threadIdx.x & 31, blocks = (r.Hq + kQueryHeads - 1) / kQueryHeads;
+  const int row = static_cast<int>(item / blocks), h0 = static_cast<int>(item - static_cast<long long>(row) * blocks) * kQueryHeads;
+  Unit x;
+  unit_chunks(r, lane & 7, x);
+  const uint4* src = reinterpret_cast<const uint4*>(r.q + static_cast<long long>(row) * r.Hq * kD);
+  uint4* dst = reinterpret_cast<uint4*>(r.q_out + static_cast<long long>(row) * r.Hq * kD);
+  uint4 A[kQueryHeads / 4], B[kQueryHeads / 4];
+#pragma unroll
+  for (int i = 0; i < kQueryHeads / 4; ++i) {
+    const int h = h0 + 4 * i + (lane >> 3);
+    A[i] = B[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (h < r.Hq) {
+      A[i] = src[16 * h + x.A];
+      B[i] = src[16 * h + x.B];
+    }
+  }
+  const int seq = sequence_of_row(a.cu_new, a.n, row);
+  const int T0 = a.seq_lens_before[seq], c0 = a.cu_new[seq];
+  if (T0 + a.cu_new[seq + 1] - c0 > r.max_pos) return;   // a token past the table: reported with the keys
+  unit_angles(r, T0 + row - c0, x);
+#pragma unroll
+  for (int i = 0; i < kQueryHeads / 4; ++i) {
+    const int h = h0 + 4 * i + (lane >> 3);
+    turn_unit<DT>(r, x, A[i], B[i]);
+    if (h < r.Hq) {
+      dst[16 * h + x.A] = A[i];
+      dst[16 * h + x.B] = B[i];
+    }
   }
 }
 
