@@ -123,7 +123,7 @@ def _ptr(x):
 def _stream(s):
     if s is None:
         import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -314,6 +314,7 @@ class Rope:
         self.table = table
         self.interleaved = bool(interleaved)
         self.c = s4kv_rope(table.data_ptr(), table.shape[0], table.shape[1], int(self.interleaved))
+        self.ref = ctypes.byref(self.c)
 
 
 def _on_its_device(f):
@@ -326,6 +327,10 @@ def _on_its_device(f):
         with torch.cuda.device(self._index):
             return f(self, *args, **kwargs)
     return call
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 class KVCache:
@@ -352,6 +357,9 @@ class KVCache:
         self.R = residual_v
         self._ws = None
         self._index = self.pool.get_device()
+        # (torch.cuda.current_stream builds a Stream object for every call)
+        self._current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
         self._sizes = {}
 
     def close(self):
@@ -395,7 +403,7 @@ class KVCache:
             out = torch.empty((B, Hq, 128), dtype=dt, device=q.device)
         if self.bits == S4KV_BITS_INT8:
             nbytes = self._window_bytes(B, 1, Hq, max_seq_len)
-            ws = self._scratch(nbytes, stream)
+            ws, stream = self._scratch(nbytes, stream), self._handle(stream)
         else:
             ws, nbytes = self.workspace(B, Hq, max_seq_len)
         s4kv_decode_attention(self.h, layer, q, Hq, block_table, block_table.shape[1], seq_lens,
@@ -414,7 +422,7 @@ class KVCache:
             nbytes = self._window_bytes(B, nq, Hq, max_seq_len)
             s4kv_multi_query_attention(self.h, layer, q, nq, Hq, block_table, block_table.shape[1], seq_lens, slot_ids, B,
                                        sm_scale, out, out_dtype, self._scratch(nbytes, stream), nbytes, max_seq_len,
-                                       stream)
+                                       self._handle(stream))
             return out
         nbytes = s4kv_multi_query_workspace_bytes(self.h, B, nq, Hq, max_seq_len)
         if self._ws is None or self._ws.numel() < nbytes:
@@ -427,13 +435,23 @@ class KVCache:
     def _tensor(self, t, name, dtype, shape):
         """t is a contiguous tensor of this cache's device; shape: sizes, None for any."""
         got = t.shape
-        if t.dtype is not dtype or len(got) != len(shape) or any(w != g for w, g in zip(shape, got) if w is not None):
+        good = t.dtype is dtype and len(got) == len(shape)
+        if good:
+            for w, g in zip(shape, got):
+                good = good and (w is None or w == g)
+        if not good:
             raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} is wanted, got {t.dtype} {tuple(got)}")
         if not t.is_contiguous():
             raise ValueError(f"{name} is not contiguous")
         if t.get_device() != self._index:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.pool.device}")
         return got
+
+    def _handle(self, stream):
+        """The cudaStream_t of `stream`: of the cache's device's current stream for None."""
+        if stream is None:
+            return self._current_stream(self._index)
+        return stream if isinstance(stream, int) else stream.cuda_stream
 
     def _scratch(self, nbytes, stream):
         """Scratch of one call, allocated on its stream: calls on other streams and captured graphs share none of it."""
@@ -492,8 +510,9 @@ class KVCache:
                 self._tensor(q_out, "q_out", dt, (tokens, heads, 128))
         elif q_out is not None:
             raise ValueError("q_out without q")
-        s4kv_append_rope(self.h, layer, rope.c, k, v, tokens, cu_new, slot_ids, seq_lens_before, block_table, width, n,
-                         q, heads, q_out, stream)
+        _check(_lib.s4kv_append_rope(self.h, int(layer), rope.ref, k.data_ptr(), v.data_ptr(), tokens, cu_new.data_ptr(),
+                                     _address(slot_ids), seq_lens_before.data_ptr(), block_table.data_ptr(), width, n,
+                                     _address(q), heads, _address(q_out), self._handle(stream)), "s4kv_append_rope")
         return q_out
 
     @_on_its_device
@@ -510,9 +529,15 @@ class KVCache:
         if slot_ids is not None:
             self._tensor(slot_ids, "slot_ids", torch.int32, (B,))
         out = self._out(out, "out", (B, nq, Hq, 128), out_dtype)
+        max_seq_len = int(max_seq_len)
         nbytes = self._window_bytes(B, nq, Hq, max_seq_len)
-        s4kv_window_attention(self.h, layer, q, nq, Hq, window, num_sinks, block_table, width, seq_lens, slot_ids, B,
-                              sm_scale, out, out_dtype, self._scratch(nbytes, stream), nbytes, max_seq_len, stream)
+        ws = self._scratch(nbytes, stream)
+        wide = 0x7fffffff   # as wide as any sequence
+        _check(_lib.s4kv_window_attention(self.h, int(layer), q.data_ptr(), nq, Hq, min(int(window), wide),
+                                          min(int(num_sinks), wide), block_table.data_ptr(),
+                                          width, seq_lens.data_ptr(), _address(slot_ids), B, float(sm_scale), out.data_ptr(),
+                                          out_dtype, ws.data_ptr(), nbytes, max_seq_len, self._handle(stream)),
+               "s4kv_window_attention")
         return out
 
     @_on_its_device
@@ -531,11 +556,13 @@ class KVCache:
             self._tensor(first, "first", i32, (n,))
         if slot_ids is not None:
             self._tensor(slot_ids, "slot_ids", i32, (n,))
+        num_rows = int(num_rows)
         shape = (num_rows, self.H, 128)
         out_k = self._out(out_k, "out_k", shape, out_dtype)
         out_v = self._out(out_v, "out_v", shape, out_dtype)
-        s4kv_gather(self.h, layer, block_table, width, seq_lens, slot_ids, first, cu_rows, num_rows, n, out_k, out_v,
-                    out_dtype, stream)
+        _check(_lib.s4kv_gather(self.h, int(layer), block_table.data_ptr(), width, seq_lens.data_ptr(), _address(slot_ids),
+                                _address(first), cu_rows.data_ptr(), num_rows, n, out_k.data_ptr(), out_v.data_ptr(),
+                                out_dtype, self._handle(stream)), "s4kv_gather")
         return out_k, out_v
 
     def dequant(self, layer, slot, block_table_row, seq_len, stream=None):

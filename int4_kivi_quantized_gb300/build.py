@@ -22,7 +22,7 @@ SOURCES = {
     "s4kv_decode.cu": [],
     "s4kv_mq.cu": [],
     "s4kv_noalloc.cu": [],
-    "s4kv_int8.cu": EXACT,
+    "s4kv_append8.cu": EXACT,
     "s4kv_window.cu": [],
     "s4kv_gather.cu": EXACT,
 }

@@ -1164,16 +1164,12 @@ __device__ __forceinline__ uint32_t e4m3_of(float x, float scale) {
   return static_cast<uint32_t>(__nv_cvt_float_to_fp8(__fdiv_rn(x, scale), __NV_SATFINITE, __NV_E4M3));
 }
 
-template <bool ROPE, int DT>
 __global__ void __launch_bounds__(kThreads) append_fp8_kernel(AppendArgs a) {
   extern __shared__ int pre[];   // [n + 1]
   __shared__ int warp_tot[kThreads / 32];
   if (!build_prefix(a, pre, warp_tot)) return;
   const int total = pre[a.n];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if constexpr (ROPE) {
-    if (queries_first(a)) turn_queries<DT>(a);
-  }
   for (int item = blockIdx.x; item < total; item += gridDim.x) {
     int lo_i = 0, hi_i = a.n - 1;   // last i with pre[i] <= item
     while (lo_i < hi_i) {
@@ -1197,10 +1193,6 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(AppendArgs a) {
       if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_TABLE, i);
       continue;
     }
-    if (ROPE && T1 > a.rope.max_pos) {
-      if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_POSITION, i);
-      continue;
-    }
     const int* bt_row = a.block_table + static_cast<long long>(i) * a.bt_stride;
     if (j == 0) {
       int* len_word = a.lens + slot * a.H + h;
@@ -1217,11 +1209,7 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(AppendArgs a) {
     for (int idx = 32 * j + warp; idx < n1; idx += kThreads / 32) {
       const int t = T0 + idx;
       const int pp = bt_row[t / kP];
-      uint2 kr = *reinterpret_cast<const uint2*>(row_ptr(a.k, row0 + idx, a.H, h) + 4 * lane);
-      if constexpr (ROPE) {   // lanes 2c and 2c + 1 share chunk c; each keeps its half
-        const uint4 x = rope::turned_chunk(a.rope, row_ptr(a.k, row0 + idx, a.H, h), t, lane >> 1, a.dtype);
-        kr = (lane & 1) ? make_uint2(x.z, x.w) : make_uint2(x.x, x.y);
-      }
+      const uint2 kr = *reinterpret_cast<const uint2*>(row_ptr(a.k, row0 + idx, a.H, h) + 4 * lane);
       const uint2 vr = *reinterpret_cast<const uint2*>(row_ptr(a.v, row0 + idx, a.H, h) + 4 * lane);
       if (pp < 0 || pp >= a.num_pages) {
         if (lane == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, pp);
@@ -1256,9 +1244,6 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(AppendArgs a) {
         }
       }
     }
-  }
-  if constexpr (ROPE) {
-    if (!queries_first(a)) turn_queries<DT>(a);
   }
 }
 
@@ -1382,12 +1367,9 @@ cudaError_t launch_append(const AppendArgs& a, int grid, cudaStream_t st) {
   if (a.n > kMaxSeqsPerCall) return cudaErrorInvalidValue;
   if (a.bits == 8) {
     const size_t smem = static_cast<size_t>(a.n + 1) * sizeof(int);
-    void (*f)(AppendArgs) = !a.rope.table           ? append_fp8_kernel<false, S4KV_F16>
-                            : a.dtype == S4KV_BF16 ? append_fp8_kernel<true, S4KV_BF16>
-                                                   : append_fp8_kernel<true, S4KV_F16>;
-    const cudaError_t c = prefer_max_shared(reinterpret_cast<const void*>(f));
+    const cudaError_t c = prefer_max_shared(reinterpret_cast<const void*>(append_fp8_kernel));
     if (c != cudaSuccess) return c;
-    f<<<with_queries(a, grid), kThreads, smem, st>>>(a);
+    append_fp8_kernel<<<grid, kThreads, smem, st>>>(a);
     return cudaGetLastError();
   }
   const int smem = append_smem_bytes(a.n);

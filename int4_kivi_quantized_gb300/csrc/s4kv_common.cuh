@@ -232,7 +232,7 @@ inline cudaError_t prefer_max_shared(const void* func) {
 cudaError_t launch_append(const AppendArgs& a, int grid, cudaStream_t st);
 int append_ctas_per_sm();   // resident CTAs per SM the append kernel is sized for
 cudaError_t launch_dequant(const DequantArgs& a, cudaStream_t st);
-cudaError_t launch_append_int8(const AppendArgs& a, int num_sms, cudaStream_t st);
+cudaError_t launch_append8(const AppendArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_dequant_int8(const DequantArgs& a, cudaStream_t st);
 cudaError_t launch_gather(const GatherArgs& a, int num_sms, cudaStream_t st);
 cudaError_t launch_window(const WindowArgs& a, int num_sms, cudaStream_t st);

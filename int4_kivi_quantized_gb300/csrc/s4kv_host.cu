@@ -375,8 +375,8 @@ int append_call(s4kv_cache* cache, int layer, const RopeArgs& rope, const void* 
   a.num_sms = cache->num_sms;
   a.step = 0;
   a.max_len = 0;
-  if (cache->bits == S4KV_BITS_INT8) {
-    const cudaError_t e = launch_append_int8(a, cache->num_sms, static_cast<cudaStream_t>(stream));
+  if (cache->bits == S4KV_BITS_INT8 || (cache->bits == 8 && rope.table)) {
+    const cudaError_t e = launch_append8(a, cache->num_sms, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? S4KV_OK : S4KV_ERR_CUDA;
   }
   const long long bound = static_cast<long long>(c.num_kv_heads) * (3LL * n + num_new_tokens / 32 + 1);
@@ -617,7 +617,7 @@ int s4kv_decode_step(s4kv_cache* cache, int layer, const void* k_new, const void
     p.bits = a.bits;
     p.step = 1;
     p.max_len = max_seq_len;
-    if (launch_append_int8(p, cache->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) return S4KV_ERR_CUDA;
+    if (launch_append8(p, cache->num_sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) return S4KV_ERR_CUDA;
     return window_call(cache, a, 1, kNoWindow, 0, static_cast<cudaStream_t>(stream));
   }
   a.grid_warps = grid * decode_warps_per_cta(0);

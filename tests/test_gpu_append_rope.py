@@ -48,6 +48,8 @@ class Pair:
         for _ in range(2):
             c = s4.KVCache(1, sum(pages), H, residual, len(lens), dtype, bits=bits)
             c.pool.zero_()
+            if bits == 8:   # a power of two, and not
+                c.set_fp8_scales(0, [(0.5, 0.37)[h % 2] for h in range(H)], [(1.3, 2.0)[h % 2] for h in range(H)])
             self.caches.append(c)
         self.at = [0] * len(lens)
 
@@ -118,6 +120,8 @@ def test_a_position_past_the_table_is_reported_and_stores_nothing(bits):
     tab = table(100, 128)
     cache = s4.KVCache(1, 40, 2, 16, 2, "bf16", bits=bits)
     cache.pool.zero_()
+    if bits == 8:
+        cache.set_fp8_scales(0, [1.0, 1.0], [1.0, 1.0])
     bt = torch.arange(40, dtype=torch.int32, device="cuda").view(2, 20)
     k, v = inp.kv_rows(1, 101 + 64, 2, 128, torch.bfloat16)
     q = torch.randn(165, 4, 128, generator=inp.gen(1)).bfloat16().cuda()
