@@ -381,7 +381,9 @@ int s4kv_window_attention(s4kv_cache* cache, int layer, const void* q, int num_q
  *                sequence i owns output rows [cu_rows[i], cu_rows[i+1]).
  *   first_token  int32 [n] or NULL (0): row cu_rows[i] + j is token first_token[i] + j.
  *   seq_lens[i]  T_i, equal to the slot's stored length (else S4KV_DEV_BAD_LENGTH);
- *                a range that leaves [0, T_i) is S4KV_DEV_BAD_POSITION. Rows of a
+ *                a range that leaves [0, T_i) is S4KV_DEV_BAD_POSITION, a table row that
+ *                does not cover it (to the end of its last whole 32-token group on KIVI
+ *                pages) S4KV_DEV_BAD_TABLE. Rows of a
  *                sequence that is reported, and of a page that is, are left as they were.
  *   out_k, out_v [num_rows][H_kv][128] in out_dtype (S4KV_F32, or the cache dtype: the
  *                restored fp32 value rounded once), 16-byte aligned.

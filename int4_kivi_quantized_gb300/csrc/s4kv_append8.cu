@@ -49,8 +49,13 @@ __device__ __forceinline__ uint32_t absmax8(uint32_t m, uint4 w) {
 // How a block's elements become bytes: INT8 by its own scale, FP8 by the head's.
 struct Coder {
   float s;     // scale: INT8 A / 127; FP8 the head's
-  float inv;   // INT8 127 / A; FP8 1 / s where s is a power of two (the same quotients), else 0
+  float inv;   // INT8 127 / A; FP8 (MUL) 1 / s
 };
+// FP8 codes are those of x / s; where s is a power of two x (1 / s) is the same number.
+__device__ __forceinline__ bool power_of_two(float s) {
+  const uint32_t b = __float_as_uint(s);
+  return (b & 0x7fffffu) == 0 && b >= 0x01000000u && b < 0x7e000000u;   // 1 / s is normal too
+}
 template <int FMT, int DT>
 __device__ __forceinline__ Coder coder(const uint4 (&x)[8], float head_scale) {
   Coder c;
@@ -64,22 +69,22 @@ __device__ __forceinline__ Coder coder(const uint4 (&x)[8], float head_scale) {
     c.inv = A < kTiny ? 0.0f : __fdiv_rn(127.0f, A);
   } else {
     c.s = head_scale;
-    const uint32_t b = __float_as_uint(head_scale);
-    c.inv = (b & 0x7fffffu) == 0 && b >= 0x01000000u && b < 0x7e000000u ? __frcp_rn(head_scale) : 0.0f;
+    c.inv = __frcp_rn(head_scale);
   }
   return c;
 }
 
-// Codes of a packed pair (low element first) in the low 16 bits.
-template <int FMT, int DT>
+// Codes of a packed pair (low element first) in the low 16 bits. MUL (FP8): by the
+// inverse instead of the quotient.
+template <int FMT, int DT, bool MUL>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w, const Coder& c) {
   const float x = widen16(static_cast<uint16_t>(w & 0xffff), DT), y = widen16(static_cast<uint16_t>(w >> 16), DT);
   if constexpr (FMT == kI8) {
     return __byte_perm(__float_as_uint(__fadd_rn(__fmul_rn(x, c.inv), kMagic)),
                        __float_as_uint(__fadd_rn(__fmul_rn(y, c.inv), kMagic)), 0x0040);
   } else {
-    const float2 q = c.inv != 0.0f ? make_float2(__fmul_rn(x, c.inv), __fmul_rn(y, c.inv))
-                                   : make_float2(__fdiv_rn(x, c.s), __fdiv_rn(y, c.s));
+    const float2 q = MUL ? make_float2(__fmul_rn(x, c.inv), __fmul_rn(y, c.inv))
+                         : make_float2(__fdiv_rn(x, c.s), __fdiv_rn(y, c.s));
     return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3)) & 0xffffu;
   }
 }
@@ -94,8 +99,8 @@ __device__ __forceinline__ uint4 blend(uint4 fresh, uint4 old, uint32_t k0, uint
 // 8 channels) and k[2r + 1] (chunk l % 8 + 8), which make whole 16-byte key words,
 // and with a full rotation both members of every pair. keep: the page's tokens
 // below it stay as they are (FP8).
-template <int FMT, int DT>
-__device__ __forceinline__ void put_keys(char* rec, const uint4 (&k)[8], const Coder& cd, int keep) {
+template <int FMT, int DT, bool MUL>
+__device__ __forceinline__ void put_keys_by(char* rec, const uint4 (&k)[8], const Coder& cd, int keep) {
   const int lane = threadIdx.x & 31, kc = lane & 7, kr = lane >> 3;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {   // tokens ta and ta + 8
@@ -104,10 +109,10 @@ __device__ __forceinline__ void put_keys(char* rec, const uint4 (&k)[8], const C
     for (int half = 0; half < 2; ++half) {
       const uint4 x = k[2 * r + half], y = k[2 * (r + 2) + half];
       uint4 w;
-      w.x = __byte_perm(code_pair<FMT, DT>(x.x, cd), code_pair<FMT, DT>(y.x, cd), 0x5410);
-      w.y = __byte_perm(code_pair<FMT, DT>(x.y, cd), code_pair<FMT, DT>(y.y, cd), 0x5410);
-      w.z = __byte_perm(code_pair<FMT, DT>(x.z, cd), code_pair<FMT, DT>(y.z, cd), 0x5410);
-      w.w = __byte_perm(code_pair<FMT, DT>(x.w, cd), code_pair<FMT, DT>(y.w, cd), 0x5410);
+      w.x = __byte_perm(code_pair<FMT, DT, MUL>(x.x, cd), code_pair<FMT, DT, MUL>(y.x, cd), 0x5410);
+      w.y = __byte_perm(code_pair<FMT, DT, MUL>(x.y, cd), code_pair<FMT, DT, MUL>(y.y, cd), 0x5410);
+      w.z = __byte_perm(code_pair<FMT, DT, MUL>(x.z, cd), code_pair<FMT, DT, MUL>(y.z, cd), 0x5410);
+      w.w = __byte_perm(code_pair<FMT, DT, MUL>(x.w, cd), code_pair<FMT, DT, MUL>(y.w, cd), 0x5410);
       const int c = kc + 8 * half;   // channels 8c .. 8c+7: word c % 4 of lane 4 ta + c / 4
       uint4* dst = reinterpret_cast<uint4*>(rec + R8::kKc + (c & 3) * 512 + (4 * ta + (c >> 2)) * 16);
       if (FMT == 8 && keep > 0) {
@@ -121,8 +126,8 @@ __device__ __forceinline__ void put_keys(char* rec, const uint4 (&k)[8], const C
 
 // Values: lane (a, b) = (l / 4, l % 4) holds tokens 2b, 2b+1, 2b+8, 2b+9 (j = 0..3)
 // in v[2j] (chunk a) and v[2j + 1] (chunk a + 8).
-template <int FMT, int DT>
-__device__ __forceinline__ void put_values(char* rec, const uint4 (&v)[8], const Coder& cd, int keep) {
+template <int FMT, int DT, bool MUL>
+__device__ __forceinline__ void put_values_by(char* rec, const uint4 (&v)[8], const Coder& cd, int keep) {
   const int lane = threadIdx.x & 31;
   // t[half][m]: channel m of chunk a + 8 half as bytes of the four tokens
   uint32_t t[2][8];
@@ -130,8 +135,8 @@ __device__ __forceinline__ void put_values(char* rec, const uint4 (&v)[8], const
   for (int half = 0; half < 2; ++half)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {   // channels 2i, 2i + 1
-      const uint32_t p0 = code_pair<FMT, DT>(word(v[half], i), cd), p1 = code_pair<FMT, DT>(word(v[2 + half], i), cd);
-      const uint32_t p2 = code_pair<FMT, DT>(word(v[4 + half], i), cd), p3 = code_pair<FMT, DT>(word(v[6 + half], i), cd);
+      const uint32_t p0 = code_pair<FMT, DT, MUL>(word(v[half], i), cd), p1 = code_pair<FMT, DT, MUL>(word(v[2 + half], i), cd);
+      const uint32_t p2 = code_pair<FMT, DT, MUL>(word(v[4 + half], i), cd), p3 = code_pair<FMT, DT, MUL>(word(v[6 + half], i), cd);
       const uint32_t lo = __byte_perm(p0, p1, 0x5140), hi = __byte_perm(p2, p3, 0x5140);   // (c0t0, c0t1, c1t0, c1t1)
       t[half][2 * i] = __byte_perm(lo, hi, 0x5410);
       t[half][2 * i + 1] = __byte_perm(lo, hi, 0x7632);
@@ -176,6 +181,17 @@ __device__ __forceinline__ void put_values(char* rec, const uint4 (&v)[8], const
     if (FMT == 8 && keep > 0) z = blend(z, *dst, m01, m23, m01, m23);
     *dst = z;
   }
+}
+
+template <int FMT, int DT>
+__device__ __forceinline__ void put_keys(char* rec, const uint4 (&k)[8], const Coder& cd, int keep) {
+  if (FMT == 8 && !power_of_two(cd.s)) put_keys_by<FMT, DT, false>(rec, k, cd, keep);
+  else put_keys_by<FMT, DT, true>(rec, k, cd, keep);
+}
+template <int FMT, int DT>
+__device__ __forceinline__ void put_values(char* rec, const uint4 (&v)[8], const Coder& cd, int keep) {
+  if (FMT == 8 && !power_of_two(cd.s)) put_values_by<FMT, DT, false>(rec, v, cd, keep);
+  else put_values_by<FMT, DT, true>(rec, v, cd, keep);
 }
 
 // Chunk c's partner chunk in a row spread over eight lanes as put_keys has it (lo:
@@ -320,7 +336,7 @@ __device__ __forceinline__ void fp8_token(const AppendArgs& a, const Seq& s, int
   Coder cd;
   cd.s = a.fp8_scale[values ? a.H + h : h];
   cd.inv = 0.0f;
-  const uint32_t lo = code_pair<8, DT>(x.x, cd), hi = code_pair<8, DT>(x.y, cd);
+  const uint32_t lo = code_pair<8, DT, false>(x.x, cd), hi = code_pair<8, DT, false>(x.y, cd);
   if (!values) {   // slice kk = l % 8, column b = l / 8
     char* dst = rec + R8::kKc + ((lane & 7) >> 1) * 512 + (4 * (tau & 7) + (lane >> 3)) * 16 + 8 * (lane & 1) + 2 * (tau >> 3);
     *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(lo);

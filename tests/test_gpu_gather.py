@@ -100,6 +100,17 @@ def test_bad_caller_data_is_reported_and_its_rows_are_left(bits):
     bad(s4.S4KV_DEV_BAD_CU, first=(-1, 0), kept=False)
 
 
+def test_a_table_that_ends_inside_a_key_group_is_refused():
+    """KIVI pages: tokens 64..79 need the metadata of pages 4 and 5; a table of five columns has not both."""
+    f = Filled([96, 96], H=2, bits=4, residual=16, seed=4)
+    k = torch.full((160, 2, 128), 3.0, device="cuda")
+    f.cache.gather(0, f.bt[:, :5].contiguous(), f.seq, f.i32([0, 80, 160]), 160, out_k=k, out_v=k.clone())
+    assert f.cache.status() == (s4.S4KV_ERR_DEVICE, s4.S4KV_DEV_BAD_TABLE) and bool((k == 3.0).all())
+    f.cache.gather(0, f.bt[:, :4].contiguous(), f.seq, f.i32([0, 64, 128]), 128, out_k=k[:128], out_v=k[:128].clone())
+    f.ok()
+    assert torch.equal(k[:64], f.plain(0)[0][:64]) and torch.equal(k[64:128], f.plain(1)[0][:64])
+
+
 def test_argument_errors_launch_nothing():
     f = Filled([100], H=2, bits=4, seed=4)
     out = torch.full((100, 2, 128), 3.0, device="cuda")
