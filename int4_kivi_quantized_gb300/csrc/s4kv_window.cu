@@ -167,13 +167,13 @@ __device__ __forceinline__ void byte_softmax(ByteState<NC>& s, float (&z)[NC / 8
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
     mx[c] = fmaxf(fmaxf(z[c][0], z[c][1]), fmaxf(z[c][2], z[c][3]));
-    mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 1));
-    mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 2));
     up = up || mx[c] > s.m[c] + kLazy;
   }
-  if (__any_sync(0xffffffffu, up)) {
+  if (__any_sync(0xffffffffu, up)) {   // rare: only now the lanes of a column agree on its maximum
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
+      mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 1));
+      mx[c] = fmaxf(mx[c], __shfl_xor_sync(0xffffffffu, mx[c], 2));
       const float mn = fmaxf(s.m[c], mx[c]);
       const float al = mn == -INFINITY ? 1.0f : ex2(s.m[c] - mn);
       s.m[c] = mn;
@@ -227,7 +227,9 @@ __device__ __forceinline__ void byte_block(const char* rec, ByteState<NC>& s, co
   float z[CT][4];
   float vscale = 1.0f;
   {
+    // two chains of four MMAs for each eight tokens instead of one of eight
     float s0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float u0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int kp = 0; kp < 4; ++kp) {
       const uint4 w = *reinterpret_cast<const uint4*>(rec + kp * 512 + lane * 16);
@@ -237,13 +239,18 @@ __device__ __forceinline__ void byte_block(const char* rec, ByteState<NC>& s, co
         const int kk = 2 * kp + u;
         const uint32_t a[4] = {qa[kk][0], NC == 16 ? qa[kk][NC / 8 - 1] : 0u, qa[kk][NC / 8], NC == 16 ? qa[kk][NC / 4 - 1] : 0u};
         if constexpr (FMT == kI8) {
-          mma16816(s0, a, __byte_perm(w0, 0u, 0x4140), __byte_perm(w1, 0u, 0x4140));
-          mma16816(s1, a, __byte_perm(w0, 0u, 0x4342), __byte_perm(w1, 0u, 0x4342));
+          mma16816(u ? u0 : s0, a, __byte_perm(w0, 0u, 0x4140), __byte_perm(w1, 0u, 0x4140));
+          mma16816(u ? u1 : s1, a, __byte_perm(w0, 0u, 0x4342), __byte_perm(w1, 0u, 0x4342));
         } else {
-          mma16816(s0, a, fp8x2_to_f16x2(w0 & 0xffffu), fp8x2_to_f16x2(w1 & 0xffffu));
-          mma16816(s1, a, fp8x2_to_f16x2(w0 >> 16), fp8x2_to_f16x2(w1 >> 16));
+          mma16816(u ? u0 : s0, a, fp8x2_to_f16x2(w0 & 0xffffu), fp8x2_to_f16x2(w1 & 0xffffu));
+          mma16816(u ? u1 : s1, a, fp8x2_to_f16x2(w0 >> 16), fp8x2_to_f16x2(w1 >> 16));
         }
       }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s0[i] += u0[i];
+      s1[i] += u1[i];
     }
     if constexpr (FMT == kI8) {
       const float2 sc = *reinterpret_cast<const float2*>(rec + Rec<kI8>::kKs);
