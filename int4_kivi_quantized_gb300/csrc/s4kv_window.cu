@@ -25,8 +25,10 @@
 //    128 times the query's sum comes off the scores, and the P V accumulators
 //    start at -128 2^-24 times the sum of the rounded P (one MMA against a
 //    constant tile), so what a block adds is exact codes times its own fp32 scale.
-//  * KIVI pages: whole blocks run through the decode kernel's group arithmetic,
-//    8 columns a warp; cut blocks and the residual through a masked form of it.
+//  * KIVI pages: the key scales are folded into the query and the minima into a
+//    bias per column, the value scales into P and the minima into a bias per column
+//    and channel group, 8 columns a warp; cut blocks and the residual go through a
+//    masked form of the decode kernel's tail.
 //
 // A masked token's key and value never meet arithmetic that could carry an
 // infinity or a NaN of theirs into the result: scores are selected, probabilities
@@ -518,6 +520,129 @@ __device__ __forceinline__ void ring_block(const uint16_t* kring, const uint16_t
   }
 }
 
+// ---- KIVI pages: a whole block (32 tokens, both page records in `stage`) -----------------
+// As on 8-bit pages the query columns are the MMA's rows: a lane's code words are the
+// B operand of tokens gi and gi + 8 as they stand (f16 subnormals), and A holds
+// q' = q * scale of column gi in rows 0..7 and what its rounding to f16 left in rows
+// 8..15, so one MMA carries both terms for eight columns and a lane adds its own two
+// rows. The scores are then the operand of P V already: no pass through shared
+// memory. (m, l): state of column gi; s.o and s.bias as the decode kernel has them
+// (o at the powers of two that mma_unscale removes).
+template <int BITS>
+__device__ __forceinline__ void kivi_block(const char* stage, MmaState& s, float& m, float& l, const float (&q)[32],
+                                           float scale) {
+  using F = Rec<BITS>;
+  constexpr int RS = kRecStrideB<BITS>;
+  const int lane = threadIdx.x & 31, ti = lane & 3;
+  uint32_t w[2][8];
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const uint4 x = *reinterpret_cast<const uint4*>(stage + p * RS + F::kKc + lane * 16);
+    w[p][0] = x.x; w[p][1] = x.y; w[p][2] = x.z; w[p][3] = x.w;
+    if constexpr (BITS == 4) {
+      const uint4 y = *reinterpret_cast<const uint4*>(stage + p * RS + F::kKc + 512 + lane * 16);
+      w[p][4] = y.x; w[p][5] = y.y; w[p][6] = y.z; w[p][7] = y.w;
+    }
+  }
+  float c[4][4];   // page p, tokens 0..7 | 8..15: c[2p + half]
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[i][e] = 0.0f;
+  float2 beta2 = make_float2(0.0f, 0.0f);
+  const char* mrec = stage + (ti >> 1) * RS + F::kKm + (ti & 1) * 16;
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk) {
+    const float4 s4 = *reinterpret_cast<const float4*>(mrec + kk * 32), m4 = *reinterpret_cast<const float4*>(mrec + kk * 32 + 256);
+    const float2 q01 = make_float2(q[4 * kk], q[4 * kk + 1]), q23 = make_float2(q[4 * kk + 2], q[4 * kk + 3]);
+    beta2 = __ffma2_rn(q01, make_float2(m4.x, m4.y), beta2);
+    beta2 = __ffma2_rn(q23, make_float2(m4.z, m4.w), beta2);
+    // 2-bit: the odd slice of a word comes out 16 times larger
+    const float f = BITS == 2 && (kk & 1) ? 0.0625f : 1.0f;
+    const float2 x01 = __fmul2_rn(q01, make_float2(s4.x * f, s4.y * f)), x23 = __fmul2_rn(q23, make_float2(s4.z * f, s4.w * f));
+    const __half2 h01 = __floats2half2_rn(x01.x, x01.y), h23 = __floats2half2_rn(x23.x, x23.y);
+    const float2 r01 = __half22float2(h01), r23 = __half22float2(h23);
+    const uint32_t a[4] = {*reinterpret_cast<const uint32_t*>(&h01), pack_f16x2(x01.x - r01.x, x01.y - r01.y),
+                           *reinterpret_cast<const uint32_t*>(&h23), pack_f16x2(x23.x - r23.x, x23.y - r23.y)};
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      uint32_t k[4];
+      if constexpr (BITS == 4) unpack8_sub(w[p][kk], k);
+      else unpack_crumbs_sub(w[p][kk >> 1], kk & 1, k);
+      mma16816(c[2 * p], a, k[0], k[2]);
+      mma16816(c[2 * p + 1], a, k[1], k[3]);
+    }
+  }
+  float beta = beta2.x + beta2.y;
+  beta += __shfl_xor_sync(0xffffffffu, beta, 1);
+  beta += __shfl_xor_sync(0xffffffffu, beta, 2);
+  beta *= scale;
+  const float lo = scale * kLowRows, hi = scale * (BITS == 4 ? kHighRows : 4194304.0f);
+  float z[2][4];   // page p: tokens 2ti, 2ti+1, 2ti+8, 2ti+9 of column gi
+#pragma unroll
+  for (int p = 0; p < 2; ++p)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      z[p][e] = fmaf(c[2 * p][e] + c[2 * p][2 + e], lo, beta);
+      z[p][2 + e] = fmaf(c[2 * p + 1][e] + c[2 * p + 1][2 + e], hi, beta);
+    }
+  float mx = fmaxf(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[0][2], z[0][3])), fmaxf(fmaxf(z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3])));
+  if (__any_sync(0xffffffffu, mx > m + kLazy)) {
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const float mn = fmaxf(m, mx), al = mn == -INFINITY ? 1.0f : ex2(m - mn);
+    m = mn;
+    l *= al;
+    const float a0 = __shfl_sync(0xffffffffu, al, 8 * ti), a1 = __shfl_sync(0xffffffffu, al, 8 * ti + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      s.o[i][0] *= a0;
+      s.o[i][1] *= a1;
+      s.o[i][2] *= a0;
+      s.o[i][3] *= a1;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s.bias[k] *= al;
+  }
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const char* rec = stage + p * RS;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) z[p][x] = ex2(z[p][x] - m);
+    l += (z[p][0] + z[p][1]) + (z[p][2] + z[p][3]);
+    const float2 p01 = make_float2(z[p][0], z[p][1]), p23 = make_float2(z[p][2], z[p][3]);
+    uint32_t b0[4], b1[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 s4 = *reinterpret_cast<const float4*>(rec + F::kVm + ((2 * k) * 4 + ti) * 16);
+      const float4 m4 = *reinterpret_cast<const float4*>(rec + F::kVm + ((2 * k + 1) * 4 + ti) * 16);
+      const float2 y01 = __fmul2_rn(p01, make_float2(s4.x, s4.y)), y23 = __fmul2_rn(p23, make_float2(s4.z, s4.w));
+      b0[k] = pack_f16x2(y01.x, y01.y);
+      b1[k] = pack_f16x2(y23.x, y23.y);
+      float2 u = __ffma2_rn(p01, make_float2(m4.x, m4.y), make_float2(s.bias[k], 0.0f));
+      u = __ffma2_rn(p23, make_float2(m4.z, m4.w), u);
+      s.bias[k] = u.x + u.y;
+    }
+    uint32_t v[8];
+    {
+      const uint4 x = *reinterpret_cast<const uint4*>(rec + F::kVc + lane * 16);
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      if constexpr (BITS == 4) {
+        const uint4 y = *reinterpret_cast<const uint4*>(rec + F::kVc + 512 + lane * 16);
+        v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < 8; ++mt) {
+      uint32_t a[4];
+      if constexpr (BITS == 4) unpack8_sub(v[mt], a);
+      else unpack_crumbs_sub(v[mt >> 1], mt & 1, a);
+      mma16816(s.o[mt], a, b0[mt >> 1], b1[mt >> 1]);
+    }
+  }
+  __syncwarp();   // the stage is read
+}
+
 // ---- KIVI pages: a block that is cut, or that the residual reaches into ------------------
 // As the decode kernel's tail: keys from the staged records (whole groups) or the
 // key-ring rows at `kring`, values below Tv from the records, later ones from the
@@ -797,11 +922,10 @@ __device__ __forceinline__ void combine_cluster(const WindowArgs& a, const WSmem
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// FMT: page format. NC: columns a warp holds (8, or 16 on 8-bit pages). PACKED
-// (KIVI, at most 4 columns): the query's low f16 part rides in columns 4..7.
+// FMT: page format. NC: columns a warp holds (8, or 16 on 8-bit pages).
 // ONE: a cluster of CTAs holds one segment and combines it itself (grid.x = CTAs of
 // a cluster, grid.y = segments); otherwise the slices of the whole line, as above.
-template <int FMT, int NC, bool PACKED, bool ONE>
+template <int FMT, int NC, bool ONE>
 __global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArgs a) {
   constexpr int BT = kBlock<FMT>;
   constexpr int CT = NC / 8;
@@ -1195,9 +1319,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArg
           pend |= 1u << s;
         };
         for (int i = 0; i < n && i < kStages; ++i) issue(i, i);
-        // this lane's query: column gi (PACKED: gi % 4), channels 32 ti + x
-        const int qcol = col0 + (PACKED ? gi & 3 : gi);
-        const uint16_t* qrow = qrow_of(qcol);
+        // this lane's query: column gi, channels 32 ti + x
+        const uint16_t* qrow = qrow_of(col0 + gi);
         float qv[32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -1210,6 +1333,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArg
           }
         }
         bool ok = true;
+        float m = -INFINITY, l = 0.0f;
         for (int i = 0; i < n; ++i) {
           const int s = i & 1;
           if (!((skip >> s) & 1u)) {
@@ -1217,13 +1341,21 @@ __global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArg
               ok = false;
               break;
             }
-            mma_group<true, FMT, PACKED>(reinterpret_cast<const char*>(s ? st1 : st0), ms, ptile, qv, a.sm_scale_log2,
-                                         kLoAbove / a.sm_scale_log2);
+            kivi_block<FMT>(reinterpret_cast<const char*>(s ? st1 : st0), ms, m, l, qv, a.sm_scale_log2);
           }
           if (i + kStages < n) issue(s, i + kStages);
         }
         mma_unscale<FMT>(ms);
-        const int pos0 = pos_of(col0 + (PACKED ? (2 * ti) & 3 : 2 * ti)), pos1 = pos_of(col0 + (PACKED ? (2 * ti + 1) & 3 : 2 * ti + 1));
+        // into the cut blocks' form: maxima of columns 2ti, 2ti + 1 (the same in every
+        // lane of a column), sums in lanes gi = 0
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        ms.m0 = __shfl_sync(0xffffffffu, m, 8 * ti);
+        ms.m1 = __shfl_sync(0xffffffffu, m, 8 * ti + 4);
+        const float l0 = __shfl_sync(0xffffffffu, l, 8 * ti), l1 = __shfl_sync(0xffffffffu, l, 8 * ti + 4);
+        ms.l0 = lane < 4 ? l0 : 0.0f;
+        ms.l1 = lane < 4 ? l1 : 0.0f;
+        const int pos0 = pos_of(col0 + 2 * ti), pos1 = pos_of(col0 + 2 * ti + 1);
         for (int c = c0; ok && c < c1; ++c) {
           const int blk = pl.block_of(nf + c);
           const int t0 = kG * blk, t1 = min(t0 + kG, T);
@@ -1404,11 +1536,11 @@ __global__ void __launch_bounds__(32 * kMergeWarps) win_merge_kernel(DecodeArgs 
 }
 
 // Grants a kernel its dynamic shared memory (once per size increase).
-template <int FMT, int NC, bool PACKED, bool ONE>
+template <int FMT, int NC, bool ONE>
 cudaError_t grant(size_t need) {
   static size_t granted = 0;
   if (need <= granted) return cudaSuccess;
-  const void* f = reinterpret_cast<const void*>(window_kernel<FMT, NC, PACKED, ONE>);
+  const void* f = reinterpret_cast<const void*>(window_kernel<FMT, NC, ONE>);
   cudaError_t e = prefer_max_shared(f);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(need));
   if (e == cudaSuccess && ONE) e = cudaFuncSetAttribute(f, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -1420,11 +1552,11 @@ cudaError_t grant(size_t need) {
   return cudaSuccess;
 }
 template <int FMT> constexpr size_t kOneBytes = prefix_at<FMT>() + sizeof(OneSmem);
-template <int FMT, int NC, bool PACKED>
-cudaError_t one_ready() { return grant<FMT, NC, PACKED, true>(kOneBytes<FMT>); }
+template <int FMT, int NC>
+cudaError_t one_ready() { return grant<FMT, NC, true>(kOneBytes<FMT>); }
 
 // A launch of `segs` clusters of `cluster` CTAs.
-template <int FMT, int NC, bool PACKED>
+template <int FMT, int NC>
 void one_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int cluster, int segs, cudaStream_t st) {
   cfg->gridDim = dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(segs));
   cfg->blockDim = dim3(32 * kWarpsOf<FMT>);
@@ -1449,7 +1581,7 @@ void one_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int cluster,
 // 8192 tokens 55.9 / 63.5. So: at most one segment per SM, and at most kOneTokens
 // tokens per warp.
 constexpr int kOneTokens = 384;
-template <int FMT, int NC, bool PACKED>
+template <int FMT, int NC>
 int cluster_of(const WindowArgs& a, int num_sms) {
   const long long segs = static_cast<long long>(a.B) * a.H * a.tiles;
   if (a.form == 1 || segs > 65535 || (a.form == 0 && segs > num_sms)) return 0;
@@ -1463,10 +1595,10 @@ int cluster_of(const WindowArgs& a, int num_sms) {
     if (resident < 0) {
       cudaLaunchConfig_t cfg = {};
       cudaLaunchAttribute attr[1];
-      one_config<FMT, NC, PACKED>(&cfg, attr, 16, 1, nullptr);
+      one_config<FMT, NC>(&cfg, attr, 16, 1, nullptr);
       int n = 0;
-      if (one_ready<FMT, NC, PACKED>() != cudaSuccess ||
-          cudaOccupancyMaxActiveClusters(&n, window_kernel<FMT, NC, PACKED, true>, &cfg) != cudaSuccess) {
+      if (one_ready<FMT, NC>() != cudaSuccess ||
+          cudaOccupancyMaxActiveClusters(&n, window_kernel<FMT, NC, true>, &cfg) != cudaSuccess) {
         cudaGetLastError();
         n = 0;
       }
@@ -1478,15 +1610,15 @@ int cluster_of(const WindowArgs& a, int num_sms) {
   return c;
 }
 
-template <int FMT, int NC, bool PACKED>
+template <int FMT, int NC>
 cudaError_t run_call(const WindowArgs& a, int num_sms, cudaStream_t st) {
-  if (const int cluster = cluster_of<FMT, NC, PACKED>(a, num_sms)) {
-    const cudaError_t e = one_ready<FMT, NC, PACKED>();
+  if (const int cluster = cluster_of<FMT, NC>(a, num_sms)) {
+    const cudaError_t e = one_ready<FMT, NC>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    one_config<FMT, NC, PACKED>(&cfg, attr, cluster, a.B * a.H * a.tiles, st);
-    return cudaLaunchKernelEx(&cfg, window_kernel<FMT, NC, PACKED, true>, a);
+    one_config<FMT, NC>(&cfg, attr, cluster, a.B * a.H * a.tiles, st);
+    return cudaLaunchKernelEx(&cfg, window_kernel<FMT, NC, true>, a);
   }
   // No more CTAs than the work can use (slices go to one warp of every CTA first):
   // a sequence has at most the blocks of max_seq_len, or of window, queries and
@@ -1499,9 +1631,9 @@ cudaError_t run_call(const WindowArgs& a, int num_sms, cudaStream_t st) {
   const long long warps = (units * segs + kLeastUnits<FMT> - 1) / kLeastUnits<FMT>;
   if (warps < grid) grid = static_cast<int>(warps);
   const size_t smem = prefix_at<FMT>() + static_cast<size_t>(a.B + 1) * sizeof(long long);
-  cudaError_t e = grant<FMT, NC, PACKED, false>(smem);
+  cudaError_t e = grant<FMT, NC, false>(smem);
   if (e != cudaSuccess) return e;
-  window_kernel<FMT, NC, PACKED, false><<<grid, 32 * kWarpsOf<FMT>, smem, st>>>(a);
+  window_kernel<FMT, NC, false><<<grid, 32 * kWarpsOf<FMT>, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the combine, launched programmatically right behind
@@ -1533,10 +1665,10 @@ cudaError_t launch_window(const WindowArgs& a, int num_sms, cudaStream_t st) {
   const int cols = a.nq * a.g;
   const bool wide = window_cols(a.bits, cols) == 16;
   switch (a.bits) {
-    case kI8: return wide ? run_call<kI8, 16, false>(a, num_sms, st) : run_call<kI8, 8, false>(a, num_sms, st);
-    case 8: return wide ? run_call<8, 16, false>(a, num_sms, st) : run_call<8, 8, false>(a, num_sms, st);
-    case 2: return cols <= 4 ? run_call<2, 8, true>(a, num_sms, st) : run_call<2, 8, false>(a, num_sms, st);
-    default: return cols <= 4 ? run_call<4, 8, true>(a, num_sms, st) : run_call<4, 8, false>(a, num_sms, st);
+    case kI8: return wide ? run_call<kI8, 16>(a, num_sms, st) : run_call<kI8, 8>(a, num_sms, st);
+    case 8: return wide ? run_call<8, 16>(a, num_sms, st) : run_call<8, 8>(a, num_sms, st);
+    case 2: return run_call<2, 8>(a, num_sms, st);
+    default: return run_call<4, 8>(a, num_sms, st);
   }
 }
 
