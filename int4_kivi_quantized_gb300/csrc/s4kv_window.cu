@@ -42,39 +42,38 @@ namespace s4kv {
 namespace {
 
 constexpr int kI8 = S4KV_BITS_INT8;
-#ifndef S4KV_WINDOW_I8_WARPS
-#define S4KV_WINDOW_I8_WARPS 12
-#endif
-#ifndef S4KV_WINDOW_I8_STAGES
-#define S4KV_WINDOW_I8_STAGES 2
-#endif
-// Warps of a CTA, one CTA per SM.
-template <int FMT> constexpr int kWarpsOf = FMT == kI8 ? S4KV_WINDOW_I8_WARPS : 12;
-constexpr int kMaxWarps = 16;
-template <int FMT> constexpr int kStagesOf = FMT == kI8 ? S4KV_WINDOW_I8_STAGES : 3;   // records in flight per warp (8-bit pages)
+// Warps of a CTA (one CTA per SM), and the records that a warp of 8-bit pages has in
+// flight or at hand. More warps would hide more of a page's latency, but 16 columns
+// then spill (16 warps of 128 registers: 54 us against 44 at 12 on the case below);
+// more records do not help INT8 pages, whose loads outrun the arithmetic: three for
+// each of 12 warps, 22 MB in flight over the GPU, read 16 sequences of 32000 tokens,
+// 8 kv heads, in 175 us, two in 166 us, and 8 to 16 warps with two to four lie between.
+constexpr int kWarps = 12;
+template <int FMT> constexpr int kStagesOf = FMT == kI8 ? 2 : 3;
 template <int FMT> constexpr bool kByte = FMT == 8 || FMT == kI8;
 template <int FMT> constexpr int kBlock = kByte<FMT> ? kP : kG;             // tokens of a block
 // 8-bit pages: the stages, or a warp's 16 columns of output when a segment is combined
-template <int FMT> constexpr int kRegionOf = kByte<FMT> ? (kStagesOf<FMT> * Rec<kI8>::kBytes > 16 * kD * 4 ? (kStagesOf<FMT> * Rec<kI8>::kBytes + 127) / 128 * 128 : 16 * kD * 4) : kRegion;
+template <int FMT, int NC> constexpr int kRegionOf = kByte<FMT> ? (kStagesOf<FMT> * Rec<kI8>::kBytes > 16 * kD * 4 ? (kStagesOf<FMT> * Rec<kI8>::kBytes + 127) / 128 * 128 : 16 * kD * 4) : kRegion;
 template <int FMT> constexpr int kLeastUnits = kByte<FMT> ? 4 : 3;           // least work per warp
 
-template <int FMT>
+template <int FMT, int NC>
 struct WSmem {
-  alignas(128) uint8_t region[kWarpsOf<FMT>][kRegionOf<FMT>];
-  alignas(16) float ptile[kByte<FMT> ? 1 : kWarpsOf<FMT>][32 * kPRow];
-  alignas(8) uint64_t bar[kWarpsOf<FMT>][4];
+  alignas(128) uint8_t region[kWarps][kRegionOf<FMT, NC>];
+  alignas(16) float ptile[kByte<FMT> ? 1 : kWarps][32 * kPRow];
+  alignas(16) uint4 q[NC == 16 ? kWarps : 1][NC == 16 ? 8 : 1][32];   // 16 columns: the queries as A operands, by slice and lane
+  alignas(8) uint64_t bar[kWarps][4];
 };
 // Behind it: the cost prefix of the line (int64 [B + 1]), or what a one-segment
 // launch combines: each warp's maxima and sums, then the CTA's own state.
 struct OneSmem {
-  float wm[kMaxWarps][16], wl[kMaxWarps][16];
+  float wm[kWarps][16], wl[kWarps][16];
   alignas(16) float part[16][kD];
   float pm[16], pl[16];
 };
-template <int FMT>
-__host__ __device__ constexpr size_t prefix_at() { return (sizeof(WSmem<FMT>) + 15) / 16 * 16; }
-static_assert(prefix_at<4>() + 4097 * sizeof(long long) <= 227 * 1024 &&
-                  prefix_at<4>() + sizeof(OneSmem) <= 227 * 1024,
+template <int FMT, int NC>
+__host__ __device__ constexpr size_t prefix_at() { return (sizeof(WSmem<FMT, NC>) + 15) / 16 * 16; }
+static_assert(prefix_at<4, 8>() + 4097 * sizeof(long long) <= 227 * 1024 &&
+                  prefix_at<4, 8>() + sizeof(OneSmem) <= 227 * 1024,
               "the largest batch fits the shared memory of a CTA");
 
 __device__ __forceinline__ bool visible(int t, int pos, int window, int sinks) {
@@ -219,9 +218,10 @@ __device__ __forceinline__ void add_only(float (&o)[4], const int (&opos)[2], in
 // One staged record of 16 tokens. Keys: lane (gi, ti) reads its words as the B
 // operand of tokens gi and gi + 8; q as A. qa: f16 queries, rows gi (and gi + 8);
 // zoff[ct] = -128 scale sum_c q_c (INT8). scale = sm_scale log2(e) (times the
-// key scale on FP8). kMask: tokens are masked by `cut` and the columns' positions.
+// key scale on FP8). Sixteen columns leave no registers for the queries: qs holds
+// them. kMask: tokens are masked by `cut` and the columns' positions.
 template <int FMT, int NC, bool kMask>
-__device__ __forceinline__ void byte_block(const char* rec, ByteState<NC>& s, const uint32_t (&qa)[8][NC / 4],
+__device__ __forceinline__ void byte_block(const char* rec, ByteState<NC>& s, const uint32_t (&qa)[8][2], const uint4 (*qs)[32],
                                            const float (&zoff)[NC / 8], float scale, const Cut& cut,
                                            const int (&pos)[NC / 8], const int (&opos)[NC / 8][2]) {
   constexpr int CT = NC / 8;
@@ -239,7 +239,14 @@ __device__ __forceinline__ void byte_block(const char* rec, ByteState<NC>& s, co
       for (int u = 0; u < 2; ++u) {
         const uint32_t w0 = u ? w.z : w.x, w1 = u ? w.w : w.y;
         const int kk = 2 * kp + u;
-        const uint32_t a[4] = {qa[kk][0], NC == 16 ? qa[kk][NC / 8 - 1] : 0u, qa[kk][NC / 8], NC == 16 ? qa[kk][NC / 4 - 1] : 0u};
+        uint32_t a[4] = {qa[kk][0], 0u, qa[kk][1], 0u};
+        if constexpr (NC == 16) {
+          const uint4 x = qs[kk][lane];
+          a[0] = x.x;
+          a[1] = x.y;
+          a[2] = x.z;
+          a[3] = x.w;
+        }
         if constexpr (FMT == kI8) {
           mma16816(u ? u0 : s0, a, __byte_perm(w0, 0u, 0x4140), __byte_perm(w1, 0u, 0x4140));
           mma16816(u ? u1 : s1, a, __byte_perm(w0, 0u, 0x4342), __byte_perm(w1, 0u, 0x4342));
@@ -851,10 +858,9 @@ __device__ __forceinline__ void store1(const WindowArgs& a, long long row, int c
 // warps of a CTA (a thread per four channels of a column), then, column by column,
 // the CTAs through distributed shared memory. Warps without work left l = 0 and
 // nothing else. Every thread of the cluster comes here once.
-template <int FMT>
-__device__ __forceinline__ void combine_cluster(const WindowArgs& a, const WSmem<FMT>& sm, OneSmem& one, int csize, int rank, int ncols,
+template <int FMT, int NC>
+__device__ __forceinline__ void combine_cluster(const WindowArgs& a, const WSmem<FMT, NC>& sm, OneSmem& one, int csize, int rank, int ncols,
                                                 long long row0, int col0, int g) {
-  constexpr int kW = kWarpsOf<FMT>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // output row of the tile's column j
   auto out_row = [&](int j) -> long long {
@@ -866,13 +872,13 @@ __device__ __forceinline__ void combine_cluster(const WindowArgs& a, const WSmem
     store_out(a, out_row(col), lane, make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv));
   };
   __syncthreads();
-  for (int col = warp; col < ncols; col += kW) {
+  for (int col = warp; col < ncols; col += kWarps) {
     float M = -INFINITY, L = 0.0f;
     float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-    for (int w = 0; w < kW; ++w) M = fmaxf(M, one.wm[w][col]);
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, one.wm[w][col]);
 #pragma unroll
-    for (int w = 0; w < kW; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
       const float l = one.wl[w][col];
       if (l == 0.0f) continue;
       const float x = M == -INFINITY ? 1.0f : ex2(one.wm[w][col] - M);
@@ -897,7 +903,7 @@ __device__ __forceinline__ void combine_cluster(const WindowArgs& a, const WSmem
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(x) : "r"(smem_u32(p)), "r"(r));
     return x;
   };
-  for (int col = warp * csize + rank; col < ncols; col += kW * csize) {
+  for (int col = warp * csize + rank; col < ncols; col += kWarps * csize) {
     float M = -INFINITY, L = 0.0f, m = -INFINITY, l = 0.0f;
     float4 O = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (lane < csize) {
@@ -926,14 +932,14 @@ __device__ __forceinline__ void combine_cluster(const WindowArgs& a, const WSmem
 // ONE: a cluster of CTAs holds one segment and combines it itself (grid.x = CTAs of
 // a cluster, grid.y = segments); otherwise the slices of the whole line, as above.
 template <int FMT, int NC, bool ONE>
-__global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(WindowArgs a) {
   constexpr int BT = kBlock<FMT>;
   constexpr int CT = NC / 8;
-  constexpr int kW = kWarpsOf<FMT>, kThreads = 32 * kW;
+  constexpr int kThreads = 32 * kWarps;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  auto& sm = *reinterpret_cast<WSmem<FMT>*>(smem_raw);
-  long long* pre = reinterpret_cast<long long*>(smem_raw + prefix_at<FMT>());   // [B + 1]
-  OneSmem& one = *reinterpret_cast<OneSmem*>(smem_raw + prefix_at<FMT>());        // (ONE)
+  auto& sm = *reinterpret_cast<WSmem<FMT, NC>*>(smem_raw);
+  long long* pre = reinterpret_cast<long long*>(smem_raw + prefix_at<FMT, NC>());   // [B + 1]
+  OneSmem& one = *reinterpret_cast<OneSmem*>(smem_raw + prefix_at<FMT, NC>());        // (ONE)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gi = lane >> 2, ti = lane & 3;
   uint8_t* region = sm.region[warp];
   uint64_t* bar = sm.bar[warp];
@@ -952,7 +958,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArg
     T = a.seq_lens[b];
     pl = plan_of<FMT>(T, a);
     gw = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-    n_act = static_cast<int>(gridDim.x) * kW;
+    n_act = static_cast<int>(gridDim.x) * kWarps;
     if (a.max_warps > 0 && a.max_warps < n_act) n_act = a.max_warps;
     if (pl.cost < n_act) n_act = static_cast<int>(pl.cost);
     seg_start = 0;
@@ -967,7 +973,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArg
   } else {
     {   // cost prefix over sequences: sequence b owns H tiles segments of its plan's cost
       long long carry = 0;
-      __shared__ long long wt[kW];
+      __shared__ long long wt[kWarps];
       for (int base = 0; base < a.B; base += kThreads) {
         const int b = base + tid;
         const long long cnt = b < a.B ? static_cast<long long>(a.H) * a.tiles * plan_of<FMT>(a.seq_lens[b], a).cost : 0;
@@ -980,7 +986,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArg
         if (lane == 31) wt[warp] = x;
         __syncthreads();
         long long before = carry, total = 0;
-        for (int q = 0; q < kW; ++q) {
+        for (int q = 0; q < kWarps; ++q) {
           if (q < warp) before += wt[q];
           total += wt[q];
         }
@@ -992,7 +998,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArg
       __syncthreads();
     }
     C = pre[a.B];
-    n_act = static_cast<int>(gridDim.x) * kW;
+    n_act = static_cast<int>(gridDim.x) * kWarps;
     if (a.max_warps > 0 && a.max_warps < n_act) n_act = a.max_warps;
     {
       const long long cap = (C + kLeastUnits<FMT> - 1) / kLeastUnits<FMT>;
@@ -1133,7 +1139,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArg
         // queries: f16 operands, and (INT8) -128 scale sum_c q_c
         const float ks = FMT == 8 ? a.fp8_scale[h] : 1.0f;
         const float zscale = a.sm_scale_log2 * ks;
-        uint32_t qa[8][NC / 4];   // [kk][row r | CT + r]: channels c_0 c_1 | c_2 c_3
+        uint32_t qa[8][2];        // 8 columns: row gi, channels c_0 c_1 | c_2 c_3 of slice kk
         float zoff[CT];
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
@@ -1146,7 +1152,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArg
             for (int i = 0; i < 4; ++i) {
               uint32_t x = w[i];
               if (a.dtype == S4KV_BF16) x = pack_f16x2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
-              qa[2 * j + (i >> 1)][(i & 1) * CT + c] = x;
+              if constexpr (NC == 8) qa[2 * j + (i >> 1)][i & 1] = x;
+              else reinterpret_cast<uint32_t*>(&sm.q[warp][2 * j + (i >> 1)][lane])[2 * (i & 1) + c] = x;
               if (FMT == kI8) {
                 const float2 f = unpack_in<S4KV_F16>(x);
                 sum += f.x + f.y;
@@ -1167,10 +1174,10 @@ __global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArg
             }
             const char* rec = reinterpret_cast<const char*>(region + s * Rec<kI8>::kBytes);
             if (u0 + i < pl.nf) {
-              byte_block<FMT, NC, false>(rec, st, qa, zoff, zscale, cut, pos, opos);
+              byte_block<FMT, NC, false>(rec, st, qa, sm.q[NC == 16 ? warp : 0], zoff, zscale, cut, pos, opos);
             } else {
               cut.tok0 = pl.block_of(u0 + i) * BT;
-              byte_block<FMT, NC, true>(rec, st, qa, zoff, zscale, cut, pos, opos);
+              byte_block<FMT, NC, true>(rec, st, qa, sm.q[NC == 16 ? warp : 0], zoff, zscale, cut, pos, opos);
             }
           }
           if (i + kStagesOf<FMT> < n) issue(s, i + kStagesOf<FMT>);
@@ -1447,7 +1454,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<FMT>, 1) window_kernel(WindowArg
   if (pend) fail(-1);   // never expected: every issued copy is waited for
   if constexpr (ONE) {
     const int h = seg / a.tiles, col0 = (seg - h * a.tiles) * NC;
-    combine_cluster<FMT>(a, sm, one, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x), min(NC, ncols - col0),
+    combine_cluster<FMT, NC>(a, sm, one, static_cast<int>(gridDim.x), static_cast<int>(blockIdx.x), min(NC, ncols - col0),
                          static_cast<long long>(b) * a.nq * a.Hq + h * a.g, col0, a.g);
   }
 }
@@ -1551,16 +1558,16 @@ cudaError_t grant(size_t need) {
   granted = need;
   return cudaSuccess;
 }
-template <int FMT> constexpr size_t kOneBytes = prefix_at<FMT>() + sizeof(OneSmem);
+template <int FMT, int NC> constexpr size_t kOneBytes = prefix_at<FMT, NC>() + sizeof(OneSmem);
 template <int FMT, int NC>
-cudaError_t one_ready() { return grant<FMT, NC, true>(kOneBytes<FMT>); }
+cudaError_t one_ready() { return grant<FMT, NC, true>(kOneBytes<FMT, NC>); }
 
 // A launch of `segs` clusters of `cluster` CTAs.
 template <int FMT, int NC>
 void one_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int cluster, int segs, cudaStream_t st) {
   cfg->gridDim = dim3(static_cast<unsigned>(cluster), static_cast<unsigned>(segs));
-  cfg->blockDim = dim3(32 * kWarpsOf<FMT>);
-  cfg->dynamicSmemBytes = kOneBytes<FMT>;
+  cfg->blockDim = dim3(32 * kWarps);
+  cfg->dynamicSmemBytes = kOneBytes<FMT, NC>;
   cfg->stream = st;
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
@@ -1588,8 +1595,8 @@ int cluster_of(const WindowArgs& a, int num_sms) {
   const long long seen = static_cast<long long>(a.window) + a.nq + a.sinks;
   const long long blocks = (a.max_seq_len < seen ? a.max_seq_len : seen) / kBlock<FMT> + 2;   // of a segment, at most
   int c = 1;
-  while (c < 8 && 2 * c * segs <= num_sms && blocks > static_cast<long long>(c) * kWarpsOf<FMT>) c *= 2;
-  if (c == 8 && segs <= 6 && blocks > 16LL * kWarpsOf<FMT>) {
+  while (c < 8 && 2 * c * segs <= num_sms && blocks > static_cast<long long>(c) * kWarps) c *= 2;
+  if (c == 8 && segs <= 6 && blocks > 16LL * kWarps) {
     // clusters of 16 fill a GPC each: only where every one of them is resident at once
     static int resident = -1;
     if (resident < 0) {
@@ -1606,7 +1613,7 @@ int cluster_of(const WindowArgs& a, int num_sms) {
     }
     if (segs <= resident) c = 16;
   }
-  if (a.form == 0 && blocks * kBlock<FMT> > static_cast<long long>(c) * kWarpsOf<FMT> * kOneTokens) return 0;
+  if (a.form == 0 && blocks * kBlock<FMT> > static_cast<long long>(c) * kWarps * kOneTokens) return 0;
   return c;
 }
 
@@ -1630,15 +1637,15 @@ cudaError_t run_call(const WindowArgs& a, int num_sms, cudaStream_t st) {
   const long long segs = static_cast<long long>(a.B) * a.H * a.tiles;
   const long long warps = (units * segs + kLeastUnits<FMT> - 1) / kLeastUnits<FMT>;
   if (warps < grid) grid = static_cast<int>(warps);
-  const size_t smem = prefix_at<FMT>() + static_cast<size_t>(a.B + 1) * sizeof(long long);
+  const size_t smem = prefix_at<FMT, NC>() + static_cast<size_t>(a.B + 1) * sizeof(long long);
   cudaError_t e = grant<FMT, NC, false>(smem);
   if (e != cudaSuccess) return e;
-  window_kernel<FMT, NC, false><<<grid, 32 * kWarpsOf<FMT>, smem, st>>>(a);
+  window_kernel<FMT, NC, false><<<grid, 32 * kWarps, smem, st>>>(a);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   // the combine, launched programmatically right behind
   const long long items = static_cast<long long>(a.B) * a.H * a.nq * a.g;
-  const bool team = static_cast<long long>(grid) * kWarpsOf<FMT> > 16 * segs;   // more than 16 partials a segment
+  const bool team = static_cast<long long>(grid) * kWarps > 16 * segs;   // more than 16 partials a segment
   void (*f)(DecodeArgs, int, int) = team ? win_merge_kernel<true> : win_merge_kernel<false>;
   long long blocks = team ? items : (items + kMergeWarps - 1) / kMergeWarps;
   if (blocks > 16LL * num_sms) blocks = 16LL * num_sms;
@@ -1658,7 +1665,7 @@ cudaError_t run_call(const WindowArgs& a, int num_sms, cudaStream_t st) {
 
 }  // namespace
 
-int window_warps_per_sm() { return kMaxWarps; }
+int window_warps_per_sm() { return kWarps; }
 int window_cols(int bits, int cols) { return (bits == 8 || bits == kI8) && cols > 8 ? 16 : 8; }
 
 cudaError_t launch_window(const WindowArgs& a, int num_sms, cudaStream_t st) {
