@@ -414,6 +414,7 @@ struct Page {
 
 template <int FMT, int DT, bool ROPE>
 __global__ void __launch_bounds__(kThreads, kCtas) append8_kernel(AppendArgs a) {
+  stream_wait();
   extern __shared__ __align__(128) uint8_t smem_raw[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint4* mine = reinterpret_cast<uint4*>(smem_raw + warp * kStage) + lane;   // piece i of this lane at mine[32 i]
@@ -531,8 +532,7 @@ cudaError_t run(const AppendArgs& a, int num_sms, cudaStream_t st) {
   int unit = a.H;
   while (unit % 2 == 0 && unit * kWarps / 2 % a.H == 0) unit /= 2;
   if (grid > unit) grid -= grid % unit;
-  f<<<static_cast<unsigned>(grid), kThreads, kWarps * kStage, st>>>(a);
-  return cudaGetLastError();
+  return launch_behind(f, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kWarps * kStage, st, a);
 }
 
 }  // namespace

@@ -228,6 +228,24 @@ inline cudaError_t prefer_max_shared(const void* func) {
   return cudaSuccess;
 }
 
+// Launches `f` so that its start-up overlaps the end of the work before it in the
+// stream: the kernel waits on the device (stream_wait) before it touches memory.
+template <typename... P, typename... A>
+inline cudaError_t launch_behind(void (*f)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, f, static_cast<P>(args)...);
+}
+__device__ __forceinline__ void stream_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Host-side launchers (one per translation unit).
 cudaError_t launch_append(const AppendArgs& a, int grid, cudaStream_t st);
 int append_ctas_per_sm();   // resident CTAs per SM the append kernel is sized for

@@ -350,6 +350,7 @@ __device__ __forceinline__ int sequence_of(const GatherArgs& a, int s) {
 // range that a slot lies in changes with the sequence.
 template <int FMT, typename OUT>
 __global__ void __launch_bounds__(kThreads, kCtas) gather_kernel(GatherArgs a, int combos, int slots) {
+  stream_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   {   // a malformed call: nothing is read or written
     int bad = a.cu_rows[0] != 0 || a.cu_rows[a.n] != a.num_rows;
@@ -494,8 +495,9 @@ cudaError_t run_out(const GatherArgs& a, int num_sms, cudaStream_t st) {
   const int parts = (pairs + combos - 1) / combos;
   const int slots = a.num_rows / kP + 2 * a.n;
   const int want = (slots + side - 1) / side, cap = (num_sms * kCtas + parts - 1) / parts;
-  f<<<dim3(static_cast<unsigned>(want < cap ? want : cap), static_cast<unsigned>(parts)), kThreads, 0, st>>>(a, combos, slots);
-  return cudaGetLastError();
+  const int grid = want < cap ? want : cap;   // one wave: a CTA's checks cost more than a longer run
+  return launch_behind(f, dim3(static_cast<unsigned>(grid), static_cast<unsigned>(parts)), dim3(kThreads), 0, st,
+                       a, combos, slots);
 }
 template <int FMT>
 cudaError_t run(const GatherArgs& a, int num_sms, cudaStream_t st) {

@@ -38,6 +38,8 @@
 
 #include "s4kv_kernels.cuh"
 
+#include <mutex>
+
 namespace s4kv {
 namespace {
 
@@ -948,6 +950,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(WindowArgs a) {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   __shared__ __align__(16) uint4 zero16;
   if (tid == 0) zero16 = make_uint4(0u, 0u, 0u, 0u);
+  stream_wait();
   int b, seg, T, gw, n_act;
   long long r0, r1, seg_start, C = 0;
   Plan pl;
@@ -1542,11 +1545,17 @@ __global__ void __launch_bounds__(32 * kMergeWarps) win_merge_kernel(DecodeArgs 
   }
 }
 
-// Grants a kernel its dynamic shared memory (once per size increase).
+// Grants a kernel its dynamic shared memory on the current device (once per device
+// and size increase).
+constexpr int kMaxDevices = 64;
+std::mutex g_lock;
 template <int FMT, int NC, bool ONE>
 cudaError_t grant(size_t need) {
-  static size_t granted = 0;
-  if (need <= granted) return cudaSuccess;
+  static size_t granted[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> guard(g_lock);
+  if (need <= granted[dev]) return cudaSuccess;
   const void* f = reinterpret_cast<const void*>(window_kernel<FMT, NC, ONE>);
   cudaError_t e = prefer_max_shared(f);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(need));
@@ -1555,7 +1564,7 @@ cudaError_t grant(size_t need) {
     cudaGetLastError();   // leave no error behind for the caller's next CUDA call
     return e;
   }
-  granted = need;
+  granted[dev] = need;
   return cudaSuccess;
 }
 template <int FMT, int NC> constexpr size_t kOneBytes = prefix_at<FMT, NC>() + sizeof(OneSmem);
@@ -1569,12 +1578,35 @@ void one_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int cluster,
   cfg->blockDim = dim3(32 * kWarps);
   cfg->dynamicSmemBytes = kOneBytes<FMT, NC>;
   cfg->stream = st;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // as launch_behind
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg->attrs = attr;
-  cfg->numAttrs = cluster > 1 ? 1 : 0;
+  cfg->numAttrs = cluster > 1 ? 2 : 1;
+}
+
+// Clusters of 16 CTAs that the current device holds at once.
+template <int FMT, int NC>
+int clusters_of_16() {
+  static int known[kMaxDevices] = {};   // 1 + the answer
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || one_ready<FMT, NC>() != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> guard(g_lock);
+  if (known[dev] == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    one_config<FMT, NC>(&cfg, attr, 16, 1, nullptr);
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, window_kernel<FMT, NC, true>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    known[dev] = 1 + n;
+  }
+  return known[dev] - 1;
 }
 
 // Shape of a call: how many CTAs each segment takes in a launch that combines
@@ -1598,19 +1630,7 @@ int cluster_of(const WindowArgs& a, int num_sms) {
   while (c < 8 && 2 * c * segs <= num_sms && blocks > static_cast<long long>(c) * kWarps) c *= 2;
   if (c == 8 && segs <= 6 && blocks > 16LL * kWarps) {
     // clusters of 16 fill a GPC each: only where every one of them is resident at once
-    static int resident = -1;
-    if (resident < 0) {
-      cudaLaunchConfig_t cfg = {};
-      cudaLaunchAttribute attr[1];
-      one_config<FMT, NC>(&cfg, attr, 16, 1, nullptr);
-      int n = 0;
-      if (one_ready<FMT, NC>() != cudaSuccess ||
-          cudaOccupancyMaxActiveClusters(&n, window_kernel<FMT, NC, true>, &cfg) != cudaSuccess) {
-        cudaGetLastError();
-        n = 0;
-      }
-      resident = n;
-    }
+    const int resident = clusters_of_16<FMT, NC>();
     if (segs <= resident) c = 16;
   }
   if (a.form == 0 && blocks * kBlock<FMT> > static_cast<long long>(c) * kWarps * kOneTokens) return 0;
@@ -1623,7 +1643,7 @@ cudaError_t run_call(const WindowArgs& a, int num_sms, cudaStream_t st) {
     const cudaError_t e = one_ready<FMT, NC>();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     one_config<FMT, NC>(&cfg, attr, cluster, a.B * a.H * a.tiles, st);
     return cudaLaunchKernelEx(&cfg, window_kernel<FMT, NC, true>, a);
   }
@@ -1640,8 +1660,7 @@ cudaError_t run_call(const WindowArgs& a, int num_sms, cudaStream_t st) {
   const size_t smem = prefix_at<FMT, NC>() + static_cast<size_t>(a.B + 1) * sizeof(long long);
   cudaError_t e = grant<FMT, NC, false>(smem);
   if (e != cudaSuccess) return e;
-  window_kernel<FMT, NC, false><<<grid, 32 * kWarps, smem, st>>>(a);
-  e = cudaGetLastError();
+  e = launch_behind(window_kernel<FMT, NC, false>, dim3(static_cast<unsigned>(grid)), dim3(32 * kWarps), smem, st, a);
   if (e != cudaSuccess) return e;
   // the combine, launched programmatically right behind
   const long long items = static_cast<long long>(a.B) * a.H * a.nq * a.g;
@@ -1651,16 +1670,8 @@ cudaError_t run_call(const WindowArgs& a, int num_sms, cudaStream_t st) {
   if (blocks > 16LL * num_sms) blocks = 16LL * num_sms;
   e = prefer_max_shared(reinterpret_cast<const void*>(f));
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, f, static_cast<const DecodeArgs&>(a), a.tiles, NC);
+  return launch_behind(f, dim3(static_cast<unsigned>(blocks)), dim3(32 * kMergeWarps), 0, st, static_cast<const DecodeArgs&>(a),
+                       a.tiles, NC);
 }
 
 }  // namespace

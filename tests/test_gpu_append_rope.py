@@ -116,6 +116,18 @@ def test_long_prompts_and_many_sequences(bits):
 
 
 @pytest.mark.parametrize("bits", FORMATS)
+@pytest.mark.parametrize("H,Hq", [(1, 1), (5, 3), (64, 64), (8, 1024), (2, 17)])
+def test_head_counts(bits, H, Hq):
+    lens = [3, 40, 0, 17]
+    tab = table(40, 128)
+    p = Pair(lens, bits, "fp16", 24, H, seed=H)
+    p.grow([2, 21, 0, 16], s4.Rope(tab), tab, False, Hq=Hq, round_=0)
+    p.grow(lens, s4.Rope(tab), tab, False, Hq=Hq, round_=1, in_place=True)
+    p.grow(lens, s4.Rope(tab), tab, False, Hq=Hq, round_=2)   # nothing new
+    p.same()
+
+
+@pytest.mark.parametrize("bits", FORMATS)
 def test_a_position_past_the_table_is_reported_and_stores_nothing(bits):
     tab = table(100, 128)
     cache = s4.KVCache(1, 40, 2, 16, 2, "bf16", bits=bits)

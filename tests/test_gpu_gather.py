@@ -100,6 +100,31 @@ def test_bad_caller_data_is_reported_and_its_rows_are_left(bits):
     bad(s4.S4KV_DEV_BAD_CU, first=(-1, 0), kept=False)
 
 
+@pytest.mark.parametrize("bits", FORMATS)
+def test_a_slot_asked_for_twice_and_another_layer(bits):
+    f = Filled([150], H=2, bits=bits, residual=32, seed=5)
+    two = s4.KVCache(2, f.cache.cfg.num_pages, 2, 32, 1, "bf16", bits=bits)
+    two.append(1, f.k[0], f.v[0], f.i32([0, 150]), f.i32([0]), f.bt)
+    K, V, _, _ = f.plain(0)
+    k, v = two.gather(1, torch.cat([f.bt, f.bt, f.bt]), f.i32([150] * 3), f.i32([0, 100, 100, 150]), 150,
+                      first=f.i32([50, 3, 17]), slot_ids=f.i32([0, 0, 0]))
+    assert two.status() == (0, 0)
+    assert torch.equal(k, torch.cat([K[50:], K[17:67]])) and torch.equal(v, torch.cat([V[50:], V[17:67]]))
+    two.gather(0, f.bt, f.i32([150]), f.i32([0, 10]), 10)
+    assert two.status() == (s4.S4KV_ERR_DEVICE, s4.S4KV_DEV_BAD_LENGTH)
+
+
+@pytest.mark.parametrize("H", [1, 3, 5, 8, 64])
+def test_head_counts(H):
+    for bits in FORMATS:
+        f = Filled([70, 33], H=H, bits=bits, residual=20, seed=H)
+        k, v = f.cache.gather(0, f.bt, f.seq, f.i32([0, 70, 103]), 103, out_dtype=f.cache.cdtype)
+        f.ok()
+        for b, rows in ((0, slice(0, 70)), (1, slice(70, 103))):
+            K, V, _, _ = f.plain(b)
+            assert torch.equal(k[rows], K.to(k.dtype)) and torch.equal(v[rows], V.to(v.dtype))
+
+
 def test_a_table_that_ends_inside_a_key_group_is_refused():
     """KIVI pages: tokens 64..79 need the metadata of pages 4 and 5; a table of five columns has not both."""
     f = Filled([96, 96], H=2, bits=4, residual=16, seed=4)

@@ -150,6 +150,38 @@ def test_masked_tokens_may_hold_anything(bits, dtype, bad, Hq):
         assert not torch.isfinite(out[0, nq - 1]).all()
 
 
+@pytest.mark.parametrize("bits", FORMATS)
+@pytest.mark.parametrize("nq,H,g", [(1, 1, 96), (1, 2, 17), (8, 1, 12), (3, 2, 32), (16, 1, 5)])
+def test_many_heads_per_kv_head(bits, nq, H, g):
+    f = Filled([nq, 200, 333], H=H, bits=bits, residual=64, seed=g)
+    q = _queries(7, 3, nq, H * g, f.dtype)
+    _all(f, q, 90, 7)
+    _all(f, q, 4000, 0)
+
+
+@pytest.mark.parametrize("bits", FORMATS)
+def test_scale_layers_and_a_slot_asked_for_twice(bits):
+    f = Filled([150, 90], H=2, bits=bits, residual=32, seed=5)
+    two = s4.KVCache(3, f.cache.cfg.num_pages, 2, 32, 2, "bf16", bits=bits)
+    k, v = torch.cat(f.k), torch.cat(f.v)
+    two.append(2, k, v, f.i32([0, 150, 240]), f.i32([0, 0]), f.bt)
+    q = _queries(8, 2, 2, 8, f.dtype)
+    want = f.cache.window(0, q, f.bt, f.seq, 150, 70, 3)
+    assert torch.equal(two.window(2, q, f.bt, f.seq, 150, 70, 3), want)
+    assert two.status() == (0, 0)
+    two.window(1, q, f.bt, f.seq, 150, 70, 3)            # nothing was appended to layer 1
+    assert two.status() == (s4.S4KV_ERR_DEVICE, s4.S4KV_DEV_BAD_LENGTH)
+    bt2, q2 = torch.cat([f.bt[:1], f.bt[:1]]), torch.cat([q[:1], q[:1]])
+    twice = f.cache.window(0, q2, bt2, f.i32([150, 150]), 150, 70, 3, slot_ids=f.i32([0, 0]))
+    f.ok()
+    for i in range(2):   # (another batch is cut into other slices: not the same bits)
+        check(twice[i], q[0], *f.plain(0), range(148, 150), bits, 70, 3)
+    # a softmax scale of its own: that of queries scaled by it
+    out = f.cache.window(0, q, f.bt, f.seq, 150, 70, 3, sm_scale=2.0 / 128 ** 0.5)
+    for b, n in enumerate(f.lens):
+        check(out[b], q[b] * 2, *f.plain(b), range(n - 2, n), bits, 70, 3)
+
+
 def test_lengths_slots_and_tables_are_checked():
     f = Filled([100, 50, 0], H=2, bits=4, residual=32, seed=1)
     q = _queries(1, 3, 3, 4, f.dtype)
