@@ -1039,18 +1039,28 @@ __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint
   }
 }
 
-// The staged key rows of a fast tile (t0: its first token) turned in place: a
-// thread holds a chunk and its partner, reads both, then writes both.
+// The staged key rows of a fast tile (first token t0) turned in place, each thread
+// two units (8 of a row): their angles are loaded before the rows are waited for.
+constexpr int kTileUnits = kG * 8 / kThreads;
+__device__ __forceinline__ void tile_angles(const RopeArgs& r, int t0, rope::Unit (&u)[kTileUnits]) {
+#pragma unroll
+  for (int i = 0; i < kTileUnits; ++i) {
+    const int q = threadIdx.x + i * kThreads;
+    rope::unit_chunks(r, q & 7, u[i]);
+    rope::unit_angles(r, t0 + (q >> 3), u[i]);
+  }
+}
 template <int DT>
-__device__ __forceinline__ void turn_tile(const RopeArgs& r, uint8_t* Ks, int t0) {
-  const int half = r.dim >> 4, units = r.interleaved ? 2 * half : half;   // chunks, or chunk pairs, of a row
-  for (int q = threadIdx.x; q < kG * units; q += kThreads) {
-    const int t = q / units, c = q - t * units, p = rope::partner(r, c);
-    uint4* pc = reinterpret_cast<uint4*>(Ks + sw_off(t, c));
-    uint4* pp = reinterpret_cast<uint4*>(Ks + sw_off(t, p));
-    const uint4 x = *pc, y = *pp;
-    *pc = rope::turn(r, t0 + t, c, x, y, DT);
-    if (p != c) *pp = rope::turn(r, t0 + t, p, y, x, DT);
+__device__ __forceinline__ void turn_tile(const RopeArgs& r, uint8_t* Ks, const rope::Unit (&u)[kTileUnits]) {
+#pragma unroll
+  for (int i = 0; i < kTileUnits; ++i) {
+    const int t = (threadIdx.x + i * kThreads) >> 3;
+    uint4* pa = reinterpret_cast<uint4*>(Ks + sw_off(t, u[i].A));
+    uint4* pb = reinterpret_cast<uint4*>(Ks + sw_off(t, u[i].B));
+    uint4 A = *pa, B = *pb;
+    rope::turn_unit<DT>(r, u[i], A, B);
+    *pa = A;
+    *pb = B;
   }
 }
 
@@ -1125,13 +1135,19 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArg
     // tile's stage is refilled only kNumStages - 1 items later, past that
     // barrier).
     if (i0.fast) {
-      cp_async_wait_prev();
-      __syncthreads();
+      const bool turns = !ROPE || i0.T1 <= a.rope.max_pos;   // (else the ring item reports it)
       if constexpr (ROPE) {
-        if (i0.T1 <= a.rope.max_pos) turn_tile<DT>(a.rope, stages + s * kStageBytes, kG * i0.tile);
+        rope::Unit u[kTileUnits];
+        if (turns) tile_angles(a.rope, kG * i0.tile, u);
+        cp_async_wait_prev();
+        __syncthreads();
+        if (turns) turn_tile<DT>(a.rope, stages + s * kStageBytes, u);
+        __syncthreads();
+      } else {
+        cp_async_wait_prev();
         __syncthreads();
       }
-      if (!ROPE || i0.T1 <= a.rope.max_pos) fast_tile<BITS, DT>(a, i0, stages + s * kStageBytes, tile_refs[s], staging, prm);
+      if (turns) fast_tile<BITS, DT>(a, i0, stages + s * kStageBytes, tile_refs[s], staging, prm);
     } else if (ring_item_is_few(a, i0)) {
       __syncthreads();
       ring_item_few<BITS, ROPE>(a, i0);
