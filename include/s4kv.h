@@ -100,6 +100,8 @@
  *   A byte holds c + 128. Tokens of the unfinished block (the newest T mod 16)
  *   wait in 16-bit rings of 16 rows and are quantized as the block fills; a
  *   block with an element that is not finite restores to values that are not.
+ *   Attention takes values of any size; keys beyond 2^100 in magnitude, where
+ *   a query sees them, may make its row NaN.
  *   Lane L = 4a + b (a in 0..7, b in 0..3); word (kp, L), kp in 0..3, is the 16
  *   bytes at kp*512 + L*16 of a half.
  *   Keys: word (kp, L) holds channels 32b + 8kp + 0..7 of tokens a and a + 8;

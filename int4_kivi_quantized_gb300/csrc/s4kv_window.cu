@@ -25,6 +25,9 @@
 //    128 times the query's sum comes off the scores, and the P V accumulators
 //    start at -128 2^-24 times the sum of the rounded P (one MMA against a
 //    constant tile), so what a block adds is exact codes times its own fp32 scale.
+//    In a cut block a token that no query sees may have set the scale (the type's
+//    largest value, say), and a rest of those subtractions times it would be felt:
+//    there the codes enter as the signed numbers that they are.
 //  * KIVI pages: the key scales are folded into the query and the minima into a
 //    bias per column, the value scales into P and the minima into a bias per column
 //    and channel group, 8 columns a warp; cut blocks and the residual go through a
@@ -102,7 +105,7 @@ template <int FMT>
 __device__ __forceinline__ Plan plan_of(int T, const WindowArgs& a) {
   constexpr int BT = kBlock<FMT>;
   Plan p;
-  if (T < a.nq || T <= 0) {   // nothing to attend to (T = 0), or a bad length
+  if (T < a.nq || T <= 0 || T > a.max_seq_len) {   // nothing to attend to (T = 0), or a bad length
     p.A0 = p.A1 = p.W0 = p.F0 = p.F1 = p.E = p.nf = p.nx = 0;
     p.cost = 1;
     return p;
@@ -217,6 +220,18 @@ __device__ __forceinline__ void add_only(float (&o)[4], const int (&opos)[2], in
   for (int e = 0; e < 4; ++e) o[e] = opos[e & 1] == only ? o[e] + t[e] : o[e];
 }
 
+// What INT8 accumulators lack of the true output, until the records are done.
+constexpr float kI8Rest = 262144.0f;
+
+// INT8 codes as exact f16 numbers: byte | 0x6400 is 1024 + byte, less 1152.
+__device__ __forceinline__ uint32_t less1152(uint32_t w) {
+  const uint32_t k = 0x64806480u;
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&w), *reinterpret_cast<const __half2*>(&k));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+__device__ __forceinline__ uint32_t codes01(uint32_t w) { return less1152(__byte_perm(w, 0x64646464u, 0x4140)); }
+__device__ __forceinline__ uint32_t codes23(uint32_t w) { return less1152(__byte_perm(w, 0x64646464u, 0x4342)); }
+
 // One staged record of 16 tokens. Keys: lane (gi, ti) reads its words as the B
 // operand of tokens gi and gi + 8; q as A. qa: f16 queries, rows gi (and gi + 8);
 // zoff[ct] = -128 scale sum_c q_c (INT8). scale = sm_scale log2(e) (times the
@@ -249,7 +264,10 @@ __device__ __forceinline__ void byte_block(const char* rec, ByteState<NC>& s, co
           a[2] = x.z;
           a[3] = x.w;
         }
-        if constexpr (FMT == kI8) {
+        if constexpr (FMT == kI8 && kMask) {
+          mma16816(u ? u0 : s0, a, codes01(w0), codes01(w1));
+          mma16816(u ? u1 : s1, a, codes23(w0), codes23(w1));
+        } else if constexpr (FMT == kI8) {
           mma16816(u ? u0 : s0, a, __byte_perm(w0, 0u, 0x4140), __byte_perm(w1, 0u, 0x4140));
           mma16816(u ? u1 : s1, a, __byte_perm(w0, 0u, 0x4342), __byte_perm(w1, 0u, 0x4342));
         } else {
@@ -266,10 +284,10 @@ __device__ __forceinline__ void byte_block(const char* rec, ByteState<NC>& s, co
     if constexpr (FMT == kI8) {
       const float2 sc = *reinterpret_cast<const float2*>(rec + Rec<kI8>::kKs);
       vscale = sc.y;
-      const float c1 = sc.x * (scale * 16777216.0f);
+      const float c1 = sc.x * (kMask ? scale : scale * 16777216.0f);
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
-        const float c2 = sc.x * zoff[c];
+        const float c2 = kMask ? 0.0f : sc.x * zoff[c];
         z[c][0] = fmaf(s0[2 * c], c1, c2);
         z[c][1] = fmaf(s0[2 * c + 1], c1, c2);
         z[c][2] = fmaf(s1[2 * c], c1, c2);
@@ -308,8 +326,14 @@ __device__ __forceinline__ void byte_block(const char* rec, ByteState<NC>& s, co
       // -2^-17 = -128 2^-24 in every element (f16 subnormal 0x8080)
       const uint32_t k[4] = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};
       const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      mma16816_c(bias[c], k, b[c][0], b[c][1], zero);
-      const float vs = vscale * 16777216.0f;
+      if constexpr (kMask) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) bias[c][e] = 0.0f;
+      } else {
+        mma16816_c(bias[c], k, b[c][0], b[c][1], zero);
+      }
+      // 2^24 of the codes' subnormals: 2^6 here, so that no scale overflows, and kI8Rest at the end
+      const float vs = vscale * (kMask ? 1.0f / kI8Rest : 16777216.0f / kI8Rest);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         bool any = true;
@@ -323,8 +347,18 @@ __device__ __forceinline__ void byte_block(const char* rec, ByteState<NC>& s, co
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const uint32_t w0 = u ? w.z : w.x, w1 = u ? w.w : w.y;
-        const uint32_t a[4] = {__byte_perm(w0, 0u, 0x4140), __byte_perm(w0, 0u, 0x4342), __byte_perm(w1, 0u, 0x4140),
-                               __byte_perm(w1, 0u, 0x4342)};
+        uint32_t a[4];
+        if constexpr (kMask) {
+          a[0] = codes01(w0);
+          a[1] = codes23(w0);
+          a[2] = codes01(w1);
+          a[3] = codes23(w1);
+        } else {
+          a[0] = __byte_perm(w0, 0u, 0x4140);
+          a[1] = __byte_perm(w0, 0u, 0x4342);
+          a[2] = __byte_perm(w1, 0u, 0x4140);
+          a[3] = __byte_perm(w1, 0u, 0x4342);
+        }
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
           float t[4];
@@ -1186,8 +1220,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(WindowArgs a) {
           if (i + kStagesOf<FMT> < n) issue(s, i + kStagesOf<FMT>);
           s = s + 1 == kStagesOf<FMT> ? 0 : s + 1;
         }
-        if (FMT == 8) {
-          const float vs = a.fp8_scale[a.H + h];
+        {
+          const float vs = FMT == 8 ? a.fp8_scale[a.H + h] : kI8Rest;
 #pragma unroll
           for (int mt = 0; mt < 8; ++mt)
 #pragma unroll

@@ -150,6 +150,47 @@ def test_masked_tokens_may_hold_anything(bits, dtype, bad, Hq):
         assert not torch.isfinite(out[0, nq - 1]).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("nq,Hq", [(1, 2), (3, 8)])
+def test_int8_extremes_beside_the_window(dtype, nq, Hq):
+    """A token that no query sees holds the type's lowest and largest value and sets the scale of a block that
+    is seen in part: the block's other tokens are restored as zeros, and count as exact zeros."""
+    n, window, sinks = 300 + nq, 100, 5
+    t = torch.bfloat16 if dtype == "bf16" else torch.float16
+
+    def edit(b, k, v):
+        for x in (195, 9):    # in the blocks that the window's start and the last sink cut
+            k[x], v[x] = torch.finfo(t).min, torch.finfo(t).min
+            k[x, :, ::2], v[x, :, 1::2] = torch.finfo(t).max, torch.finfo(t).max
+    f = Filled([n], H=2, bits="int8", dtype=dtype, seed=4, edit=edit)
+    q = _queries(9, 1, nq, Hq, f.dtype)
+    out = f.cache.window(0, q, f.bt, f.seq, n, window, sinks)
+    f.ok()
+    K, V, mk, mv = f.plain(0)
+    for x in (195, 9):
+        K[x] = V[x] = 0
+    assert not K[192:208].any() and not V[:16].any()
+    check(out[0], q[0], K, V, mk, mv, range(n - nq, n), "int8", window, sinks)
+
+
+def test_int8_values_of_any_size():
+    """Values near the type's largest and smallest scales, all seen."""
+    big = 2.0 ** 120
+
+    def edit(b, k, v):
+        v *= big if b == 0 else 2.0 ** -98
+    f = Filled([70, 70], H=2, bits="int8", dtype="bf16", seed=4, edit=edit)
+    assert f.v[0].float().abs().max() > 2.0 ** 121 and torch.isfinite(f.v[0].float()).all()
+    q = _queries(9, 2, 1, 4, f.dtype)
+    for window in (1000, 50):
+        out = f.cache.window(0, q, f.bt, f.seq, 70, window, 0)
+        f.ok()
+        for b in range(2):
+            up = 2.0 ** -120 if b == 0 else 2.0 ** 98    # (the bound's smallest terms are made for values near 1)
+            K, V, mk, mv = f.plain(b)
+            check(out[b] * up, q[b], K, V * up, mk, mv, [69], "int8", window, 0, f"seq {b}")
+
+
 @pytest.mark.parametrize("bits", FORMATS)
 @pytest.mark.parametrize("nq,H,g", [(1, 1, 96), (1, 2, 17), (8, 1, 12), (3, 2, 32), (16, 1, 5)])
 def test_many_heads_per_kv_head(bits, nq, H, g):
@@ -197,6 +238,9 @@ def test_lengths_slots_and_tables_are_checked():
     assert not out[1].any() and torch.equal(out[0], good[0])
     bad(s4.S4KV_DEV_BAD_LENGTH, top=99)
     bad(s4.S4KV_DEV_BAD_LENGTH, seq=f.i32([-5, 50, 0]))
+    for top in (2 ** 31 - 1, 2 ** 31 - 20, -2 ** 31):     # beside a good sequence, which keeps its rows
+        out = bad(s4.S4KV_DEV_BAD_LENGTH, seq=f.i32([100, top, 0]))
+        assert not out[1].any() and torch.equal(out[0], good[0])
     bad(s4.S4KV_DEV_BAD_SLOT, slots=f.i32([0, 3, 2]))
     bad(s4.S4KV_DEV_BAD_TABLE, bt=f.bt[:, :5].contiguous())
     # shorter than the chunk of queries
