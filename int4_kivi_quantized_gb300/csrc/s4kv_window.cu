@@ -60,6 +60,13 @@ template <int FMT> constexpr int kBlock = kByte<FMT> ? kP : kG;             // t
 // 8-bit pages: the stages, or a warp's 16 columns of output when a segment is combined
 template <int FMT, int NC> constexpr int kRegionOf = kByte<FMT> ? (kStagesOf<FMT> * Rec<kI8>::kBytes > 16 * kD * 4 ? (kStagesOf<FMT> * Rec<kI8>::kBytes + 127) / 128 * 128 : 16 * kD * 4) : kRegion;
 template <int FMT> constexpr int kLeastUnits = kByte<FMT> ? 4 : 3;           // least work per warp
+// Behind the blocks of a segment the line has kSegCost positions without work: a warp
+// that goes on to another segment writes a partial and starts again at the lengths and
+// the table, which takes it some blocks' time. 8-bit pages: 0 / 4 / 6 / 12 blocks: 32
+// sequences of 1024 to 8192 tokens 57.6 / 55.7 / 55.9 / 56.2 us, 16 of 777 to 8191 with
+// 16 columns 44.4 / 40.7 / 39.1 / 38.9. KIVI pages, where the cut blocks' cost says it
+// already: 0 / 1 / 3: 64 sequences behind a window of 4096 83.8 / 84.1 / 85.4.
+template <int FMT> constexpr int kSegCost = kByte<FMT> ? 6 : 0;
 
 template <int FMT, int NC>
 struct WSmem {
@@ -87,9 +94,11 @@ __device__ __forceinline__ bool visible(int t, int pos, int window, int sinks) {
 
 // Visible blocks of a sequence of T tokens: whole ones [0, A0) and [F0, F1), cut
 // ones [A0, A1), [W0, F0) and [F1, E). One plan serves every tile of the sequence.
+template <int FMT>
 struct Plan {
   int A0, A1, W0, F0, F1, E, nf, nx;
-  long long cost;
+  long long work;   // cost of the blocks; kSegCost positions without any follow
+  __device__ __forceinline__ long long cost() const { return work + kSegCost<FMT>; }
   __device__ __forceinline__ int block_of(int u) const {   // unit u: whole blocks first
     if (u < A0) return u;
     if (u < nf) return F0 + u - A0;
@@ -102,12 +111,12 @@ struct Plan {
 };
 
 template <int FMT>
-__device__ __forceinline__ Plan plan_of(int T, const WindowArgs& a) {
+__device__ __forceinline__ Plan<FMT> plan_of(int T, const WindowArgs& a) {
   constexpr int BT = kBlock<FMT>;
-  Plan p;
+  Plan<FMT> p;
   if (T < a.nq || T <= 0 || T > a.max_seq_len) {   // nothing to attend to (T = 0), or a bad length
     p.A0 = p.A1 = p.W0 = p.F0 = p.F1 = p.E = p.nf = p.nx = 0;
-    p.cost = 1;
+    p.work = 1;
     return p;
   }
   // blocks that are quantized whole
@@ -123,7 +132,7 @@ __device__ __forceinline__ Plan plan_of(int T, const WindowArgs& a) {
   if (p.F0 >= p.F1) p.F0 = p.F1 = p.W0;
   p.nf = p.A0 + p.F1 - p.F0;
   p.nx = (p.A1 - p.A0) + (p.F0 - p.W0) + (p.E - p.F1);
-  p.cost = p.nf + static_cast<long long>(kByte<FMT> ? 1 : a.tail_cost) * p.nx;
+  p.work = p.nf + static_cast<long long>(kByte<FMT> ? 1 : a.tail_cost) * p.nx;
   return p;
 }
 
@@ -987,7 +996,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(WindowArgs a) {
   stream_wait();
   int b, seg, T, gw, n_act;
   long long r0, r1, seg_start, C = 0;
-  Plan pl;
+  Plan<FMT> pl;
   if constexpr (ONE) {
     const int per = a.H * a.tiles;
     b = static_cast<int>(blockIdx.y) / per;
@@ -997,10 +1006,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(WindowArgs a) {
     gw = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
     n_act = static_cast<int>(gridDim.x) * kWarps;
     if (a.max_warps > 0 && a.max_warps < n_act) n_act = a.max_warps;
-    if (pl.cost < n_act) n_act = static_cast<int>(pl.cost);
+    if (pl.work < n_act) n_act = static_cast<int>(pl.work);
     seg_start = 0;
-    r0 = gw * pl.cost / n_act;
-    r1 = (gw + 1) * pl.cost / n_act;
+    r0 = gw * pl.work / n_act;
+    r1 = (gw + 1) * pl.work / n_act;
     if (gw >= n_act) r1 = 0;
     if (lane < NC) {
       one.wm[warp][lane] = -INFINITY;
@@ -1013,7 +1022,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(WindowArgs a) {
       __shared__ long long wt[kWarps];
       for (int base = 0; base < a.B; base += kThreads) {
         const int b = base + tid;
-        const long long cnt = b < a.B ? static_cast<long long>(a.H) * a.tiles * plan_of<FMT>(a.seq_lens[b], a).cost : 0;
+        const long long cnt = b < a.B ? static_cast<long long>(a.H) * a.tiles * plan_of<FMT>(a.seq_lens[b], a).cost() : 0;
         long long x = cnt;
   #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -1056,8 +1065,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(WindowArgs a) {
     }
     T = a.seq_lens[b];
     pl = plan_of<FMT>(T, a);
-    seg = static_cast<int>((r0 - pre[b]) / pl.cost);   // h * tiles + tile, within the sequence
-    seg_start = pre[b] + seg * pl.cost;
+    seg = static_cast<int>((r0 - pre[b]) / pl.cost());   // h * tiles + tile, within the sequence
+    seg_start = pre[b] + seg * pl.cost();
+    if (kSegCost<FMT> > 0 && r0 - seg_start >= pl.work) {   // nothing of this segment is left
+      seg_start += pl.cost();
+      if (++seg == a.H * a.tiles) {
+        seg = 0;
+        if (++b >= a.B) return;
+        T = a.seq_lens[b];
+        pl = plan_of<FMT>(T, a);
+      }
+    }
   }
 
   uint32_t phase = 0, pend = 0;   // per-stage wait parity and copies in flight (bit per stage)
@@ -1083,9 +1101,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(WindowArgs a) {
   const int ncols = a.nq * a.g;
 
   while (seg_start < r1) {
-    const long long seg_end = seg_start + pl.cost;
+    const long long seg_end = seg_start + pl.work;   // of its blocks
     const long long lo = max(r0, seg_start) - seg_start, hi = min(r1, seg_end) - seg_start;
-    const bool own = !ONE && lo == 0 && hi == pl.cost;
+    const bool own = !ONE && lo == 0 && hi == pl.work;
     const int h = seg / a.tiles, col0 = (seg - h * a.tiles) * NC;
     const int slot = a.slot_ids ? a.slot_ids[b] : b;
     const bool slot_ok = slot >= 0 && slot < a.max_slots;
@@ -1480,7 +1498,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(WindowArgs a) {
           static_cast<long long>(static_cast<unsigned>(first)) | (static_cast<long long>(ncon) << 32);
     }
     // next segment
-    seg_start = seg_end;
+    seg_start = seg_end + kSegCost<FMT>;
     if (++seg == a.H * a.tiles) {
       seg = 0;
       if (++b >= a.B) break;
