@@ -115,6 +115,7 @@ struct AppendArgs {
   const float* fp8_scale;   // FP8: this layer's scales, key [H] then value [H]
   RopeArgs rope;
   int num_sms;
+  int query_ctas;           // 8-bit pages: the grid's last CTAs, which turn queries and nothing else
   int step;                 // INT8 pages, decode step: one row per sequence, seq_lens_before holds the
   int max_len;              // lengths after it, each at most max_len
 };
