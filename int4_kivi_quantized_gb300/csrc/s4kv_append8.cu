@@ -16,6 +16,9 @@
 //  * with a rotation, 16 heads of one query row, in CTAs of their own.
 // 512 bytes of rows in and 258 (256) of record out per token and kv head: bound by
 // those bytes, with the arithmetic of a rotation and a code per element close behind.
+// Measured (16000 tokens, 8 kv heads, bf16; bytes at a plain copy's 6783 GB/s): INT8
+// 17.3 us (bytes 14.3), rotated 25, with 32 query heads 66 (52.5); FP8 rotated 26 and 70.
+// One token of each of 128 sequences with its rotation and query: 5.
 // This unit is compiled without FMA contraction; every rounding is spelled out.
 
 #include "s4kv_common.cuh"
@@ -31,6 +34,8 @@ using R8 = Rec<kI8>;
 static_assert(R8::kKc == Rec<8>::kKc && R8::kVc == Rec<8>::kVc, "both formats keep keys, then values");
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
+// (plain appends of 16000 tokens at 3 / 4 / 5: 18.4 / 17.3 / 16.2 us; rotated with 32 query
+// heads 86 / 66 / 77)
 #ifndef S4KV_APPEND8_CTAS
 #define S4KV_APPEND8_CTAS 4
 #endif

@@ -12,6 +12,11 @@
 // hold channel a of every chunk, and an 8 x 8 transpose over the lanes of one b
 // brings them there.
 //
+// Measured (8 prompts of 1900 to 2048 tokens, 8 kv heads, into 16-bit rows; bytes at a
+// plain copy's 6783 GB/s): INT8 and FP8 16.5 us (bytes 14.3), 4-bit 19 (13.1), 2-bit 16
+// (11.9); histories of 336 MB of rows 96 (74.3; a fill of those rows alone 84: writes go
+// slower than copies).
+//
 // Page slots: sequence i starts at slot cu_rows[i] / 16 + 2 i; a range of x rows
 // touches at most x / 16 + 2 pages, so sequences do not overlap, and a slot finds
 // its sequence by a search over cu_rows alone.

@@ -2,7 +2,9 @@
 // 8-channel chunk of a row turned by the angles of its position. Every product
 // and sum is one binary32 rounding (no fused multiply-add) and the result is
 // rounded once to the cache dtype, so the rows are those of a rotation done in
-// 32-bit arithmetic before an ordinary append, bit for bit.
+// 32-bit arithmetic before an ordinary append, bit for bit. Rotating apart from the
+// append would read and write every key row once more (512 bytes beside the 770 that an
+// INT8 append moves for a token and kv head); here it costs the angles, from L2.
 #pragma once
 
 #include "s4kv_common.cuh"

@@ -33,6 +33,15 @@
 //    and channel group, 8 columns a warp; cut blocks and the residual go through a
 //    masked form of the decode kernel's tail.
 //
+// Measured (GB300, a captured graph's time a call; bytes: the visible records, rings,
+// queries and outputs at the rate of a plain copy, 6783 GB/s): INT8 pages, one sequence
+// of 256 tokens, one kv head 6.3 us (latency); 8 kv heads of 4 queries, 32 sequences of
+// 1024 to 8192 tokens 55 (bytes 44.8); 16 of 777 to 8191 with four query positions 39
+// (21.9: 16 columns leave three warps a scheduler, and each waits on its own chain of
+// score, exponential and value MMAs); 32 of 32768, 4 kv heads of 7 queries, 167 (158.7).
+// 4-bit pages, 64 sequences behind a window of 4096, 8 kv heads: 82 (61.3: arithmetic,
+// and the two cut blocks of each segment).
+//
 // A masked token's key and value never meet arithmetic that could carry an
 // infinity or a NaN of theirs into the result: scores are selected, probabilities
 // scaled only where they are positive, 16-bit and FP8 value rows that no column
@@ -49,8 +58,8 @@ namespace {
 constexpr int kI8 = S4KV_BITS_INT8;
 // Warps of a CTA (one CTA per SM), and the records that a warp of 8-bit pages has in
 // flight or at hand. More warps would hide more of a page's latency, but 16 columns
-// then spill (16 warps of 128 registers: 54 us against 44 at 12 on the case below);
-// more records do not help INT8 pages, whose loads outrun the arithmetic: three for
+// then spill (16 sequences of 777 to 8191 tokens, 8 kv heads: 16 warps of 128 registers
+// 54 us, 12 warps 44); more records do not help INT8 pages, whose loads outrun the arithmetic: three for
 // each of 12 warps, 22 MB in flight over the GPU, read 16 sequences of 32000 tokens,
 // 8 kv heads, in 175 us, two in 166 us, and 8 to 16 warps with two to four lie between.
 constexpr int kWarps = 12;
@@ -1668,9 +1677,10 @@ int clusters_of_16() {
 // through the partials are much of it; a long one gains nothing from the fewer
 // launches and loses where sequences differ in length, as a CTA's segment is its
 // own. Measured (INT8, 8 kv heads, us, slices / clusters): 1 sequence of 2000
-// tokens 12.5 / 8.2, of 32000 27.5 / 24.0; 16 of 2000 22.7 / 15.1; 32 of 1024 to
-// 8192 tokens 55.9 / 63.5. So: at most one segment per SM, and at most kOneTokens
-// tokens per warp.
+// tokens 10.6 / 8.2, of 32000 26.7 / 24.3; 16 of 2000 20.2 / 14.8; 32 of 1024 to
+// 8192 tokens 54.5 / 63.6; 16 of 32000, all alike, 167.6 / 158.7, but the host knows
+// only the longest. So: at most one segment per SM, and at most kOneTokens tokens per
+// warp.
 constexpr int kOneTokens = 384;
 template <int FMT, int NC>
 int cluster_of(const WindowArgs& a, int num_sms) {
