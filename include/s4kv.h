@@ -368,8 +368,8 @@ int s4kv_multi_query_attention(s4kv_cache* cache, int layer, const void* q, int 
  * the window may hold anything: their pages can have been given away. (An append
  * on KIVI pages still writes the page of token T - R - 1 and the newest key group.)
  * A masked token contributes nothing, whatever its stored key and value hold.
- * Every page format. Two kernel launches, as for s4kv_decode_attention; the
- * workspace rule and the other arguments and errors are its too. */
+ * Every page format. One or two kernel launches (S4KV_OPT_WINDOW_FORM); the
+ * workspace rule and the other arguments and errors of s4kv_decode_attention. */
 int s4kv_window_workspace_bytes(const s4kv_cache* cache, int B, int num_q_tokens, int num_q_heads,
                                 int max_seq_len, size_t* bytes);
 int s4kv_window_attention(s4kv_cache* cache, int layer, const void* q, int num_q_tokens, int num_q_heads,

@@ -13,7 +13,7 @@
 // brings them there.
 //
 // Measured (8 prompts of 1900 to 2048 tokens, 8 kv heads, into 16-bit rows; bytes at a
-// plain copy's 6783 GB/s): INT8 and FP8 16.5 us (bytes 14.3), 4-bit 19 (13.1), 2-bit 16
+// plain copy's 6783 GB/s): INT8 and FP8 16.5 us (bytes 14.3), 4-bit 17 (13.1), 2-bit 16
 // (11.9); histories of 336 MB of rows 96 (74.3; a fill of those rows alone 84: writes go
 // slower than copies).
 //
@@ -83,18 +83,21 @@ __device__ __forceinline__ float2 e4m3x2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// Records are read by plain loads: the work before this kernel may still be writing them
+// when it starts, so they are not constant over its lifetime.
+
 // The key words of chunk c of tokens ta and ta + 8: 8-bit pages 16 bytes, 4-bit 8
 // bytes (slices 2 (c % 4) and + 1), 2-bit 4 bytes.
 template <int FMT>
 __device__ __forceinline__ uint4 key_words(const char* rec, int ta, int c) {
   const int L = 4 * ta + (c >> 2), j = c & 3;
   if constexpr (kByte<FMT>) {
-    return __ldg(reinterpret_cast<const uint4*>(rec + j * 512 + L * 16));
+    return *reinterpret_cast<const uint4*>(rec + j * 512 + L * 16);
   } else if constexpr (FMT == 4) {
-    const uint2 w = __ldg(reinterpret_cast<const uint2*>(rec + Rec<4>::kKc + (j >> 1) * 512 + L * 16 + (j & 1) * 8));
+    const uint2 w = *reinterpret_cast<const uint2*>(rec + Rec<4>::kKc + (j >> 1) * 512 + L * 16 + (j & 1) * 8);
     return make_uint4(w.x, w.y, 0u, 0u);
   } else {
-    return make_uint4(__ldg(reinterpret_cast<const uint32_t*>(rec + Rec<2>::kKc + L * 16 + j * 4)), 0u, 0u, 0u);
+    return make_uint4(*reinterpret_cast<const uint32_t*>(rec + Rec<2>::kKc + L * 16 + j * 4), 0u, 0u, 0u);
   }
 }
 
@@ -136,7 +139,7 @@ __device__ __forceinline__ void key_meta(const char* meta, int c, float (&s)[8],
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     const float4* p = reinterpret_cast<const float4*>(meta + F::kKm + (2 * (i + half) + u) * 16);
-    const float4 a = __ldg(p), b = __ldg(p + 16);
+    const float4 a = *p, b = *(p + 16);
     s[4 * half] = a.x; s[4 * half + 1] = a.y; s[4 * half + 2] = a.z; s[4 * half + 3] = a.w;
     m[4 * half] = b.x; m[4 * half + 1] = b.y; m[4 * half + 2] = b.z; m[4 * half + 3] = b.w;
   }
@@ -148,7 +151,7 @@ template <int FMT>
 __device__ __forceinline__ void value_words(const char* rec, uint4 (&v)[kValueWords<FMT>]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int i = 0; i < kValueWords<FMT>; ++i) v[i] = __ldg(reinterpret_cast<const uint4*>(rec + Rec<FMT>::kVc + i * 512 + lane * 16));
+  for (int i = 0; i < kValueWords<FMT>; ++i) v[i] = *reinterpret_cast<const uint4*>(rec + Rec<FMT>::kVc + i * 512 + lane * 16);
 }
 
 // Their codes: t[half][m] holds channel m of chunk a + 8 half, a byte a token (8-bit
@@ -242,7 +245,7 @@ __device__ __forceinline__ void put_keys(const GatherArgs& a, const char* rec, i
 #pragma unroll
   for (int i = 0; i < 4; ++i) w[i] = key_words<FMT>(rec, 4 * (i >> 1) + kr, kc + 8 * (i & 1));
   float ks;
-  if constexpr (FMT == kI8) ks = __ldg(reinterpret_cast<const float*>(rec + Rec<kI8>::kKs));
+  if constexpr (FMT == kI8) ks = *reinterpret_cast<const float*>(rec + Rec<kI8>::kKs);
   else ks = a.fp8_scale[h];
   const float s8[8] = {ks}, none[8] = {};
 #pragma unroll
@@ -291,14 +294,14 @@ __device__ __forceinline__ void put_values(const GatherArgs& a, const char* rec,
   value_words<FMT>(rec, v);
   float vs = 0.0f;
   float4 s4[2], m4[2];   // KIVI, by half: of tokens 2b, 2b+1, 2b+8, 2b+9
-  if constexpr (FMT == kI8) vs = __ldg(reinterpret_cast<const float*>(rec + Rec<kI8>::kVs));
+  if constexpr (FMT == kI8) vs = *reinterpret_cast<const float*>(rec + Rec<kI8>::kVs);
   else if constexpr (FMT == 8) vs = a.fp8_scale[a.H + h];
   else {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int k = (ca + 8 * half) >> 2;
-      s4[half] = __ldg(reinterpret_cast<const float4*>(rec + Rec<FMT>::kVm + ((2 * k) * 4 + b) * 16));
-      m4[half] = __ldg(reinterpret_cast<const float4*>(rec + Rec<FMT>::kVm + ((2 * k + 1) * 4 + b) * 16));
+      s4[half] = *(reinterpret_cast<const float4*>(rec + Rec<FMT>::kVm + ((2 * k) * 4 + b) * 16));
+      m4[half] = *(reinterpret_cast<const float4*>(rec + Rec<FMT>::kVm + ((2 * k + 1) * 4 + b) * 16));
     }
   }
   uint32_t tc[2][8];

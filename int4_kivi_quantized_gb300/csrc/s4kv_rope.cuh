@@ -38,7 +38,7 @@ __device__ __forceinline__ uint4 round8(const float (&x)[8], int dtype) {
 
 // The 8 chunk-aligned floats of a table row from index i on.
 __device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
   x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
   x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
@@ -60,8 +60,8 @@ __device__ __forceinline__ uint4 turn(const RopeArgs& r, int pos, int c, uint4 x
   float a[8], o[8];
   widen8(x, dtype, a);
   if (r.interleaved) {
-    const float4 cs = __ldg(reinterpret_cast<const float4*>(row + 4 * c));
-    const float4 sn = __ldg(reinterpret_cast<const float4*>(row + half + 4 * c));
+    const float4 cs = *reinterpret_cast<const float4*>(row + 4 * c);
+    const float4 sn = *reinterpret_cast<const float4*>(row + half + 4 * c);
     const float cc[4] = {cs.x, cs.y, cs.z, cs.w}, ss[4] = {sn.x, sn.y, sn.z, sn.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -121,8 +121,8 @@ __device__ __forceinline__ void unit_angles(const RopeArgs& r, int pos, Unit& x)
   const int half = r.dim >> 1;
   if (!x.turnA) return;   // (B turns only where A does)
   const int a = r.interleaved ? 4 * x.A : 8 * x.A, b = r.interleaved ? (x.turnB ? 4 * x.B : a) : a + 4;
-  const float4 c0 = __ldg(reinterpret_cast<const float4*>(row + a)), c1 = __ldg(reinterpret_cast<const float4*>(row + b));
-  const float4 s0 = __ldg(reinterpret_cast<const float4*>(row + half + a)), s1 = __ldg(reinterpret_cast<const float4*>(row + half + b));
+  const float4 c0 = *reinterpret_cast<const float4*>(row + a), c1 = *reinterpret_cast<const float4*>(row + b);
+  const float4 s0 = *reinterpret_cast<const float4*>(row + half + a), s1 = *reinterpret_cast<const float4*>(row + half + b);
   x.c[0] = c0.x; x.c[1] = c0.y; x.c[2] = c0.z; x.c[3] = c0.w;
   x.c[4] = c1.x; x.c[5] = c1.y; x.c[6] = c1.z; x.c[7] = c1.w;
   x.s[0] = s0.x; x.s[1] = s0.y; x.s[2] = s0.z; x.s[3] = s0.w;
