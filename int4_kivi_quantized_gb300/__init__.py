@@ -322,7 +322,7 @@ def _on_its_device(f):
     @functools.wraps(f)
     def call(self, *args, **kwargs):
         import torch
-        if torch.cuda.current_device() == self._index:
+        if self._current_device() == self._index:
             return f(self, *args, **kwargs)
         with torch.cuda.device(self._index):
             return f(self, *args, **kwargs)
@@ -358,6 +358,7 @@ class KVCache:
         self._ws = None
         self._index = self.pool.get_device()
         # (torch.cuda.current_stream builds a Stream object for every call)
+        self._current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         self._current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda device: torch.cuda.current_stream(device).cuda_stream)
         self._sizes = {}
@@ -435,6 +436,8 @@ class KVCache:
     def _tensor(self, t, name, dtype, shape):
         """t is a contiguous tensor of this cache's device; shape: sizes, None for any."""
         got = t.shape
+        if got == shape and t.dtype is dtype and t.is_contiguous() and t.get_device() == self._index:
+            return got
         good = t.dtype is dtype and len(got) == len(shape)
         if good:
             for w, g in zip(shape, got):
@@ -469,7 +472,8 @@ class KVCache:
             n = self._sizes[B, nq, Hq] = max(16, s4kv_window_workspace_bytes(self.h, B, nq, Hq, max_seq_len))
         return n
 
-    def _out(self, out, name, shape, out_dtype):
+    def _out(self, out, name, shape, out_dtype, like=None):
+        """`out`, checked, or a new tensor (like: a checked tensor of this shape, which torch is quicker to copy)."""
         import torch
         if out_dtype == self.cdtype:
             dt = self.torch_dtype
@@ -478,7 +482,9 @@ class KVCache:
         else:
             raise ValueError("out_dtype is S4KV_F32 or the cache's dtype")
         if out is None:
-            return torch.empty(shape, dtype=dt, device=self.pool.device)
+            if like is None:
+                return torch.empty(shape, dtype=dt, device=self.pool.device)
+            return torch.empty_like(like) if like.dtype is dt else torch.empty_like(like, dtype=dt)
         self._tensor(out, name, dt, shape)
         return out
 
@@ -528,7 +534,7 @@ class KVCache:
             raise ValueError("block_table has fewer rows than there are sequences")
         if slot_ids is not None:
             self._tensor(slot_ids, "slot_ids", torch.int32, (B,))
-        out = self._out(out, "out", (B, nq, Hq, 128), out_dtype)
+        out = self._out(out, "out", (B, nq, Hq, 128), out_dtype, q)
         max_seq_len = int(max_seq_len)
         nbytes = self._window_bytes(B, nq, Hq, max_seq_len)
         ws = self._scratch(nbytes, stream)
@@ -559,7 +565,7 @@ class KVCache:
         num_rows = int(num_rows)
         shape = (num_rows, self.H, 128)
         out_k = self._out(out_k, "out_k", shape, out_dtype)
-        out_v = self._out(out_v, "out_v", shape, out_dtype)
+        out_v = self._out(out_v, "out_v", shape, out_dtype, out_k)
         _check(_lib.s4kv_gather(self.h, int(layer), block_table.data_ptr(), width, seq_lens.data_ptr(), _address(slot_ids),
                                 _address(first), cu_rows.data_ptr(), num_rows, n, out_k.data_ptr(), out_v.data_ptr(),
                                 out_dtype, self._handle(stream)), "s4kv_gather")
