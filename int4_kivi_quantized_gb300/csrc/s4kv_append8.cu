@@ -33,6 +33,7 @@ constexpr int kI8 = S4KV_BITS_INT8;
 using R8 = Rec<kI8>;
 static_assert(R8::kKc == Rec<8>::kKc && R8::kVc == Rec<8>::kVc, "both formats keep keys, then values");
 constexpr int kWarps = 4;
+static_assert(kWarps == 4, "two pairs of warps, a barrier each");
 constexpr int kThreads = 32 * kWarps;
 // (plain appends of 16000 tokens at 3 / 4 / 5: 18.4 / 17.3 / 16.2 us; rotated with 32 query
 // heads 86 / 66 / 77)
@@ -250,12 +251,16 @@ __device__ __forceinline__ void turn_keys(const RopeArgs& r, uint4 (&k)[8], int 
 struct Seq {
   int i, slot, T0, T1, c0;
   bool ok;
+  // whole pages of new tokens, by logical page: [first_page, end_page)
+  __device__ __forceinline__ int first_page() const { return (T0 + kP - 1) / kP; }
+  __device__ __forceinline__ int end_page() const { return T1 / kP; }
+  __device__ __forceinline__ int pages() const { return max(0, end_page() - first_page()); }
 };
 
-// Sequence i's row range, lengths and slot, checked; errors are reported by the
-// edge items (tell), all of a sequence's items agree on them.
+// Sequence i's row range, lengths and slot, checked but for the stored length; errors
+// are reported by the keys' edge items (tell), all of a sequence's items agree on them.
 template <bool ROPE>
-__device__ __forceinline__ Seq sequence(const AppendArgs& a, int i, int h, bool tell) {
+__device__ __forceinline__ Seq sequence(const AppendArgs& a, int i, bool tell) {
   Seq s;
   s.i = i;
   s.slot = a.slot_ids ? a.slot_ids[i] : i;
@@ -279,11 +284,6 @@ __device__ __forceinline__ Seq sequence(const AppendArgs& a, int i, int h, bool 
     bad = S4KV_DEV_BAD_TABLE;
   } else if (ROPE && s.T1 > a.rope.max_pos) {
     bad = S4KV_DEV_BAD_POSITION;
-  } else if (s.T0 != 0) {
-    // the length this append starts from, or the one its edge item may have stored already
-    const int stored = __ldcg(a.lens + s.slot * a.H + h);
-    if (stored != s.T0 && stored != s.T1) bad = S4KV_DEV_BAD_LENGTH;
-    if (tell && stored != s.T0) bad = S4KV_DEV_BAD_LENGTH;   // (the edge item is the only writer)
   }
   s.ok = bad == 0;
   if (bad && tell && (threadIdx.x & 31) == 0) report(a.status, S4KV_ERR_DEVICE, bad, arg);
@@ -376,13 +376,40 @@ __device__ __forceinline__ void fp8_part(const AppendArgs& a, const Seq& s, int 
   for (int t = t0; t < t1; ++t) fp8_token<DT, ROPE>(a, s, h, values, t, rec);
 }
 
-// The edge of (sequence, head, tensor): see the top of the file. The keys' item
-// reports errors and stores the length.
+// Whether x holds for a thread of warps 2 (ID - 1) and 2 (ID - 1) + 1: both come here.
+template <int ID>
+__device__ __forceinline__ bool pair_or(bool x) {
+  int y = x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %0, 0;\n\tbarrier.cta.red.or.pred p, %1, 64, p;\n\t"
+      "selp.s32 %0, 1, 0, p;\n\t}"
+      : "+r"(y)
+      : "n"(ID)
+      : "memory");
+  return y != 0;
+}
+
+// The edge of (sequence, head, tensor): see the top of the file. Keys and values are
+// two neighbouring warps (pair x is warps 2x and 2x + 1); the keys' reports errors, looks
+// at the stored length for both and stores the new one.
 template <int FMT, int DT, bool ROPE>
 __device__ __forceinline__ void edge(const AppendArgs& a, int i, int h, bool values) {
   const int lane = threadIdx.x & 31;
-  const Seq s = sequence<ROPE>(a, i, h, !values);
-  if (!s.ok) return;
+  const Seq s = sequence<ROPE>(a, i, !values);
+  int* len = a.lens + s.slot * a.H + h;
+  // with whole pages too the length is every item's to count (a slot that starts afresh
+  // may have held any length: nothing to look at)
+  const bool shared_len = s.T0 != 0 && s.pages() > 0;
+  bool go = false;
+  if (!values && lane == 0) {
+    go = s.ok;
+    if (go && s.T0 != 0) {
+      go = shared_len ? admit(len, s.T0, s.T1, 1, s.pages() + 1) : __ldcg(len) == s.T0;
+      if (!go) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_LENGTH, i);
+    }
+  }
+  go = threadIdx.x < 64 ? pair_or<1>(go) : pair_or<2>(go);
+  if (!go) return;
   const int head = s.T0 % kP, end = s.T1 - s.T1 % kP;
   if constexpr (FMT == 8) {
     // the page that earlier and new tokens share, then a last page that is not full
@@ -405,7 +432,7 @@ __device__ __forceinline__ void edge(const AppendArgs& a, int i, int h, bool val
       reinterpret_cast<uint4*>(ring + (t % kP) * kD)[c] = x;
     }
   }
-  if (!values && lane == 0) __stcg(a.lens + s.slot * a.H + h, s.T1);
+  if (!values && lane == 0 && !shared_len) __stcg(len, s.T1);
 }
 
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
@@ -457,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) append8_kernel(AppendArgs a) 
   }
   const long long stride = static_cast<long long>(ctas) * kWarps;
   const long long w0 = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  // the edges go to the warps that have the fewest pages, from the last one down
+  // the edges go to the warps that have the fewest pages, from the last one down: warps 2x
+  // and 2x + 1 of a CTA have the values and the keys of the same ones, in step
   const long long edges = 2LL * a.n * a.H;
   for (long long e = stride - 1 - w0; e < edges; e += stride) {
     const long long sh = e >> 1;
@@ -467,18 +495,33 @@ __global__ void __launch_bounds__(kThreads, kCtas) append8_kernel(AppendArgs a) 
     Seq s;   // the sequence of the last page looked at; a warp's heads repeat where stride is a multiple of H
     s.i = -1;
     int sh = -1, c1 = 0;
+    bool ask = false;   // whether the pages of s have still to be admitted
     // the first page of this warp at or after item `it`, which moves past it
     auto next = [&](long long& it, Page& p) -> bool {
       for (; it < pages; it += stride) {
         const int slot = static_cast<int>(it / a.H), h = static_cast<int>(it - static_cast<long long>(slot) * a.H);
         const int row = slot * kP;
         if (s.i < 0 || h != sh || row < s.c0 || row >= c1) {
-          s = sequence<ROPE>(a, rope::sequence_of_row(a.cu_new, a.n, row), h, false);
+          s = sequence<ROPE>(a, rope::sequence_of_row(a.cu_new, a.n, row), false);
           c1 = s.c0 + (s.T1 - s.T0);
           sh = h;
+          ask = s.T0 != 0;
         }
         const int page = (s.T0 + row - s.c0) / kP;
-        if (!s.ok || page * kP < s.T0 || page * kP + kP > s.T1) continue;
+        if (!s.ok || page < s.first_page() || page >= s.end_page()) continue;
+        if (ask) {
+          // for all of this warp's pages of (sequence, head): stride / H slots apart, or
+          // this one where the next has another head
+          bool go = false;
+          if (lane == 0) {
+            const int step = static_cast<int>(stride / a.H);
+            const int part = step * a.H == static_cast<int>(stride) ? (s.end_page() - 1 - page) / step + 1 : 1;
+            go = admit(a.lens + s.slot * a.H + h, s.T0, s.T1, part, s.pages() + 1);
+          }
+          s.ok = __shfl_sync(0xffffffffu, go, 0);
+          ask = false;
+          if (!s.ok) continue;
+        }
         p.t0 = page * kP;
         p.h = h;
         p.at = (static_cast<long long>(s.c0 + p.t0 - s.T0) * a.H + h) * kD;

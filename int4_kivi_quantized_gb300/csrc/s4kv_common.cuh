@@ -277,6 +277,23 @@ __device__ __forceinline__ void report(int* status, int code, int detail, int ar
   }
 }
 
+// Admission of an append of several work items (a (sequence, kv head) that had T0
+// tokens, T0 > 0, and gets T1 - T0 more): one lane of each item, or of each run of
+// items, comes here once with the number of items it answers for (part of total, at
+// least two: an item alone compares and stores).
+// True where the slot held T0 tokens when the launch began; where it is false it is
+// false for every item, and nothing is stored. The stored length changes while other
+// items have still to look at it, so the word itself counts: the first item turns T0
+// into minus its part, the others subtract theirs, the last one leaves T1. A length
+// that is T1 already (the same append again) is told from one that this launch made.
+__device__ __forceinline__ bool admit(int* len, int T0, int T1, int part, int total) {
+  const int seen = atomicCAS(len, T0, -part);
+  if (seen == T0) return true;
+  if (seen >= 0) return false;
+  if (atomicAdd(len, -part) == part - total) atomicExch(len, T1);
+  return true;
+}
+
 __device__ __forceinline__ float widen16(uint16_t bits, int dtype) {
   if (dtype == S4KV_BF16) return __uint_as_float(static_cast<uint32_t>(bits) << 16);
   return __half2float(__ushort_as_half(bits));
