@@ -404,7 +404,7 @@ __device__ __forceinline__ void edge(const AppendArgs& a, int i, int h, bool val
   if (!values && lane == 0) {
     go = s.ok;
     if (go && s.T0 != 0) {
-      go = shared_len ? admit(len, s.T0, s.T1, 1, s.pages() + 1) : __ldcg(len) == s.T0;
+      go = shared_len ? goes_on(len, s.T0) : __ldcg(len) == s.T0;
       if (!go) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_LENGTH, i);
     }
   }
@@ -432,7 +432,10 @@ __device__ __forceinline__ void edge(const AppendArgs& a, int i, int h, bool val
       reinterpret_cast<uint4*>(ring + (t % kP) * kD)[c] = x;
     }
   }
-  if (!values && lane == 0 && !shared_len) __stcg(len, s.T1);
+  if (!values && lane == 0) {
+    if (shared_len) looked(len, s.T0, s.T1, 1, s.pages() + 1);
+    else __stcg(len, s.T1);
+  }
 }
 
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
@@ -472,7 +475,6 @@ __global__ void __launch_bounds__(kThreads, kCtas) append8_kernel(AppendArgs a) 
   // past the last one's 16 rows, so slots are distinct, and row 16 slot lies inside
   // the page: it names the sequence.
   const int slots = a.step ? 0 : (a.num_new + kP - 1) / kP;
-  const long long pages = static_cast<long long>(slots) * a.H;
   const int ctas = static_cast<int>(gridDim.x) - a.query_ctas;
   if constexpr (ROPE) {
     if (static_cast<int>(blockIdx.x) >= ctas) {
@@ -492,41 +494,49 @@ __global__ void __launch_bounds__(kThreads, kCtas) append8_kernel(AppendArgs a) 
     edge<FMT, DT, ROPE>(a, static_cast<int>(sh / a.H), static_cast<int>(sh % a.H), e & 1);
   }
   {
-    Seq s;   // the sequence of the last page looked at; a warp's heads repeat where stride is a multiple of H
+    // Page items (slot, head), head by head within a slot. A warp has one head and
+    // neighbouring slots where the heads divide the warps (so that few sequences' lengths
+    // are looked at), else whatever comes: the next one is dslot and dhead on.
+    int slot = static_cast<int>(w0) / a.H, h = static_cast<int>(w0) - slot * a.H, end = slots, dslot = a.dslot;
+    if (a.dhead == 0) {
+      const int x = slot, more = slots - a.each * a.dslot;   // the first `more` warps of a head have one more
+      slot = x * a.each + min(x, more);
+      end = slot + a.each + (x < more ? 1 : 0);
+      dslot = 1;
+    }
+    Seq s;   // the sequence of the last page looked at
     s.i = -1;
     int sh = -1, c1 = 0;
-    bool ask = false;   // whether the pages of s have still to be admitted
-    // the first page of this warp at or after item `it`, which moves past it
-    auto next = [&](long long& it, Page& p) -> bool {
-      for (; it < pages; it += stride) {
-        const int slot = static_cast<int>(it / a.H), h = static_cast<int>(it - static_cast<long long>(slot) * a.H);
-        const int row = slot * kP;
-        if (s.i < 0 || h != sh || row < s.c0 || row >= c1) {
+    bool ask = false;   // whether s has still to be looked at
+    int owed = 0;       // the pages that it has just been looked at for
+    // the next page of this warp, from item (slot, h) on, which moves past it
+    auto next = [&](Page& p) -> bool {
+      while (slot < end) {
+        const int row = slot * kP, hh = h, left = end - slot;   // (left: of this warp, where it has one head)
+        slot += dslot;
+        h += a.dhead;
+        if (h >= a.H) {
+          h -= a.H;
+          ++slot;
+        }
+        if (s.i < 0 || hh != sh || row < s.c0 || row >= c1) {
           s = sequence<ROPE>(a, rope::sequence_of_row(a.cu_new, a.n, row), false);
           c1 = s.c0 + (s.T1 - s.T0);
-          sh = h;
+          sh = hh;
           ask = s.T0 != 0;
         }
         const int page = (s.T0 + row - s.c0) / kP;
         if (!s.ok || page < s.first_page() || page >= s.end_page()) continue;
-        if (ask) {
-          // for all of this warp's pages of (sequence, head): stride / H slots apart, or
-          // this one where the next has another head
-          bool go = false;
-          if (lane == 0) {
-            const int step = static_cast<int>(stride / a.H);
-            const int part = step * a.H == static_cast<int>(stride) ? (s.end_page() - 1 - page) / step + 1 : 1;
-            go = admit(a.lens + s.slot * a.H + h, s.T0, s.T1, part, s.pages() + 1);
-          }
-          s.ok = __shfl_sync(0xffffffffu, go, 0);
+        if (ask) {   // for all of this warp's pages of (sequence, head)
           ask = false;
+          s.ok = goes_on(a.lens + s.slot * a.H + hh, s.T0);
           if (!s.ok) continue;
+          owed = a.dhead == 0 ? min(s.end_page() - page, left) : 1;
         }
         p.t0 = page * kP;
-        p.h = h;
-        p.at = (static_cast<long long>(s.c0 + p.t0 - s.T0) * a.H + h) * kD;
+        p.h = hh;
+        p.at = (static_cast<long long>(s.c0 + p.t0 - s.T0) * a.H + hh) * kD;
         p.pp = a.block_table[static_cast<long long>(s.i) * a.bt_stride + page];
-        it += stride;
         return true;
       }
       return false;
@@ -540,15 +550,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) append8_kernel(AppendArgs a) 
 #pragma unroll
       for (int i = 0; i < 8; ++i) copy16(mine + 32 * (8 + i), a.v + p.at + value_row(i) * step + 8 * value_chunk(i));
     };
+    auto pay = [&]() {   // (behind the loads of the page that next found)
+      if (owed > 0 && lane == 0) looked(a.lens + s.slot * a.H + sh, s.T0, s.T1, owed, s.pages() + 1);
+      owed = 0;
+    };
     Page cur, nxt;
-    long long it = w0;
-    bool have = next(it, cur);
+    bool have = next(cur);
     if (have) load_keys(cur);
     copies_end();
     if (have) load_values(cur);
     copies_end();
+    pay();
     while (have) {
-      const bool more = next(it, nxt);
+      const bool more = next(nxt);
       char* rec = record<FMT>(a, cur.pp, cur.h);
       uint4 x[8];
       all_but_newest_group();   // the keys are there
@@ -565,6 +579,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) append8_kernel(AppendArgs a) 
       const Coder vc = coder<FMT, DT>(x, FMT == 8 ? a.fp8_scale[a.H + cur.h] : 0.0f);
       if (more) load_values(nxt);
       copies_end();
+      pay();
       put_values<FMT, DT>(rec, x, vc, 0);
       if (FMT == kI8 && rec && lane == 0) *reinterpret_cast<float2*>(rec + R8::kKs) = make_float2(kc.s, vc.s);
       cur = nxt;
@@ -596,6 +611,9 @@ cudaError_t run(const AppendArgs& a, int num_sms, cudaStream_t st) {
   if (grid > unit) grid -= grid % unit;
   AppendArgs b = a;
   b.query_ctas = static_cast<int>(more);
+  b.dslot = static_cast<int>(grid * kWarps / a.H);
+  b.dhead = static_cast<int>(grid * kWarps % a.H);
+  b.each = b.dslot > 0 ? static_cast<int>(slots / b.dslot) : 0;
   return launch_behind(f, dim3(static_cast<unsigned>(grid + more)), dim3(kThreads), kWarps * kStage, st, b);
 }
 

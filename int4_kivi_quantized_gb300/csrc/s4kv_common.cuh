@@ -116,6 +116,7 @@ struct AppendArgs {
   RopeArgs rope;
   int num_sms;
   int query_ctas;           // 8-bit pages: the grid's last CTAs, which turn queries and nothing else
+  int dslot, dhead, each;   // the other CTAs' warps / H and % H, and the page slots over the former
   int step;                 // INT8 pages, decode step: one row per sequence, seq_lens_before holds the
   int max_len;              // lengths after it, each at most max_len
 };
@@ -277,21 +278,20 @@ __device__ __forceinline__ void report(int* status, int code, int detail, int ar
   }
 }
 
-// Admission of an append of several work items (a (sequence, kv head) that had T0
-// tokens, T0 > 0, and gets T1 - T0 more): one lane of each item, or of each run of
-// items, comes here once with the number of items it answers for (part of total, at
-// least two: an item alone compares and stores).
-// True where the slot held T0 tokens when the launch began; where it is false it is
-// false for every item, and nothing is stored. The stored length changes while other
-// items have still to look at it, so the word itself counts: the first item turns T0
-// into minus its part, the others subtract theirs, the last one leaves T1. A length
-// that is T1 already (the same append again) is told from one that this launch made.
-__device__ __forceinline__ bool admit(int* len, int T0, int T1, int part, int total) {
-  const int seen = atomicCAS(len, T0, -part);
-  if (seen == T0) return true;
-  if (seen >= 0) return false;
-  if (atomicAdd(len, -part) == part - total) atomicExch(len, T1);
-  return true;
+// The stored length of a slot under an append of several work items (a (sequence, kv head)
+// that had T0 tokens, T0 > 0, and gets T1 - T0 more). Each item looks whether the slot
+// held T0 tokens when the launch began (goes_on) before it stores anything, and says so
+// when it has looked (looked; once for a run of items, with their number `part` of
+// `total`). The length changes while other items have still to look, so the word itself
+// counts: the first turns T0 into minus its part, the others subtract theirs, the last one
+// leaves T1. So a length that is T1 already (the same append again) is not taken for one
+// that this launch made, and all items of a (sequence, head) decide alike.
+__device__ __forceinline__ bool goes_on(const int* len, int T0) {
+  const int v = __ldcg(len);
+  return v == T0 || v < 0;
+}
+__device__ __forceinline__ void looked(int* len, int T0, int T1, int part, int total) {
+  if (atomicCAS(len, T0, part < total ? -part : T1) != T0 && atomicAdd(len, -part) == part - total) atomicExch(len, T1);
 }
 
 __device__ __forceinline__ float widen16(uint16_t bits, int dtype) {
