@@ -48,7 +48,6 @@ __device__ __forceinline__ int tile_range(int T0, int T1, int R, int* lo) {
   return h > l ? h - l : 0;
 }
 
-
 struct Ctx {
   const AppendArgs* a;
   const int* bt_row;
@@ -458,6 +457,8 @@ __device__ __noinline__ void value_bytes_fix(unsigned flags, const uint8_t* Vs, 
 struct Item {
   int i, h, j, T0, T1, row0, tile;   // tile: index of the 32-token tile (items j >= 1)
   bool fast;                         // a tile whose key group is made only of new rows
+  bool several;                      // the stored length is looked at by the ring item and its tiles (goes_on);
+                                     // else by the ring item alone, or not (a slot that starts afresh held any)
 };
 
 __device__ __forceinline__ Item item_of(const AppendArgs& a, const int* pre, const int* seq, int item) {
@@ -481,9 +482,14 @@ __device__ __forceinline__ Item item_of(const AppendArgs& a, const int* pre, con
   it.h = h;
   it.j = r - h * per;
   it.tile = tlo + it.j - 1;
+  it.several = per > 1 && it.T0 != 0;
   it.fast = it.j >= 1 && kG * it.tile >= it.T0 && kG * it.tile + kG <= it.T1;
   return it;
 }
+
+// A CTA's items of one (sequence, head) are a run: its first item, or the CTA's, opens it.
+// Runs that follow one another differ in this bit.
+__device__ __forceinline__ int run_parity(const AppendArgs& a, const Item& it) { return (it.i * a.H + it.h) & 1; }
 
 // First item whose share of the work line starts at or after x: the work line
 // lays the items end to end in item order, a ring item weighing ring_weight and
@@ -597,7 +603,7 @@ __device__ __noinline__ void value_lane(const uint8_t* Vs, int row, int tok, uin
 
 template <int BITS, int DT>
 __device__ void fast_tile(const AppendArgs& a, const Item& it, const uint8_t* stage, const int* tile_ref,
-                          uint8_t* staging, float* prm) {
+                          uint8_t* staging, float* prm, const int* run_go) {
   using F = Rec<BITS>;
   const int tid = threadIdx.x, w = tid >> 5, l = tid & 31;
   if (static_cast<long long>(a.bt_stride) * kP < it.T1) {
@@ -772,7 +778,7 @@ __device__ void fast_tile(const AppendArgs& a, const Item& it, const uint8_t* st
   char* rec1 = nullptr;
   if (slot < 0 || slot >= a.max_slots) {
     if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_SLOT, slot);
-  } else {
+  } else if (run_go[run_parity(a, it)]) {   // (else the ring item reports the length)
     if (pp0 >= 0 && pp0 < a.num_pages) rec0 = a.pages + (static_cast<long long>(pp0) * a.H + it.h) * F::kBytes;
     else if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, pp0);
     if (pp1 >= 0 && pp1 < a.num_pages) rec1 = a.pages + (static_cast<long long>(pp1) * a.H + it.h) * F::kBytes;
@@ -837,7 +843,7 @@ __device__ __forceinline__ bool ring_item_is_few(const AppendArgs& a, const Item
 }
 
 template <int BITS, bool ROPE = false>
-__device__ __forceinline__ void ring_item_few(const AppendArgs& a, const Item& it) {
+__device__ __forceinline__ void ring_item_few(const AppendArgs& a, const Item& it, bool go) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i = it.i, h = it.h, T0 = it.T0, T1 = it.T1, row0 = it.row0;
   const int slot = a.slot_ids ? a.slot_ids[i] : i;
@@ -878,7 +884,7 @@ __device__ __forceinline__ void ring_item_few(const AppendArgs& a, const Item& i
   }
   if (tid < (T1 - vb) * 16)
     vfirst = reinterpret_cast<const uint4*>(row_ptr(a.v, row0 + (vb + tid / 16 - T0), a.H, h))[tid % 16];
-  if (T0 != 0 && stored != T0) {
+  if (it.several ? !go : T0 != 0 && stored != T0) {
     if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_LENGTH, i);
     __syncthreads();
     return;
@@ -887,14 +893,14 @@ __device__ __forceinline__ void ring_item_few(const AppendArgs& a, const Item& i
   __syncthreads();
   ring_copy<ROPE>(kring, kG, kb, T1, a.k, static_cast<long long>(row0) - T0, a.H, h, kfirst, a.rope, a.dtype);
   ring_copy(vring, a.R, vb, T1, a.v, static_cast<long long>(row0) - T0, a.H, h, vfirst, a.rope, a.dtype);
-  if (tid == 0) *len_word = T1;
+  if (tid == 0 && !it.several) *len_word = T1;
   __syncthreads();
 }
 
 // Ring items and the tiles that are not whole new key groups.
 template <int BITS, bool ROPE = false>
 __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint8_t (*stage)[1536], const uint16_t** src,
-                                       uint8_t* rows) {
+                                       uint8_t* rows, bool go) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i = it.i, h = it.h, j = it.j, T0 = it.T0, T1 = it.T1, row0 = it.row0;
   const int slot = a.slot_ids ? a.slot_ids[i] : i;
@@ -946,7 +952,7 @@ __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint
     }
     if (tid < (T1 - vb) * 16)
       vfirst = reinterpret_cast<const uint4*>(row_ptr(a.v, row0 + (vb + tid / 16 - T0), a.H, h))[tid % 16];
-    if (T0 != 0 && stored != T0) {
+    if (it.several ? !go : T0 != 0 && stored != T0) {
       if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_LENGTH, i);
       __syncthreads();
       return;
@@ -1022,9 +1028,10 @@ __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint
     __syncthreads();
     ring_copy<ROPE>(kring, kG, kb, T1, a.k, static_cast<long long>(row0) - T0, a.H, h, kfirst, a.rope, a.dtype);
     ring_copy(vring, a.R, vb, T1, a.v, static_cast<long long>(row0) - T0, a.H, h, vfirst, a.rope, a.dtype);
-    if (tid == 0) *len_word = T1;
+    if (tid == 0 && !it.several) *len_word = T1;
     __syncthreads();
   } else {
+    if (!go) return;   // the ring item reports it
     const int tile = it.tile;
     const int t0 = tile * 32;
     if (!ROPE && t0 >= T0 && t0 + kG <= T1) {      // a key group made only of new rows (with a rotation always a fast tile)
@@ -1037,6 +1044,22 @@ __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint
       value_token<BITS>(c, h, t, row_ptr(a.v, row0 + (t - T0), a.H, h));
     __syncthreads();
   }
+}
+
+// Whether a run's items may store (Item::several): one thread looks for all of them, `left`
+// or to the end of the (sequence, head). What keeps a sequence from being stored at all is
+// checked by every item.
+template <bool ROPE>
+__device__ __noinline__ bool run_goes_on(const AppendArgs& a, int i, int h, int j, int T0, int T1, int left) {
+  const int slot = a.slot_ids ? a.slot_ids[i] : i;
+  if (slot < 0 || slot >= a.max_slots || static_cast<long long>(a.bt_stride) * kP < T1 || (ROPE && T1 > a.rope.max_pos))
+    return false;
+  int* len = a.lens + slot * a.H + h;
+  if (!goes_on(len, T0)) return false;
+  int lo;
+  const int total = 1 + tile_range(T0, T1, a.R, &lo);
+  looked(len, T0, T1, min(left, total - j), total);
+  return true;
 }
 
 // The staged key rows of a fast tile (first token t0) turned in place, each thread
@@ -1124,6 +1147,8 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArg
     cp_async_commit();
   }
   int s = 0;
+  __shared__ int run_go[2];   // verdict on the current run, by run_parity (the other one may still be read)
+  const int first = item;
   while (item < total) {
     Item in;   // the item kAhead ahead
     in.fast = false;
@@ -1133,6 +1158,8 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArg
       if (in.fast) tile_prefetch(a, in, stages + sn * kStageBytes, tile_refs[sn]);
     }
     cp_async_commit();
+    if ((item == first || i0.j == 0) && threadIdx.x == 0)
+      run_go[run_parity(a, i0)] = !i0.several || run_goes_on<ROPE>(a, i0.i, i0.h, i0.j, i0.T0, i0.T1, total - item);
     // One barrier before each item: the item's cp.async rows are in shared
     // memory, and the previous item is done with the staging buffer (a fast
     // tile's stage is refilled only kNumStages - 1 items later, past that
@@ -1150,13 +1177,14 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArg
         cp_async_wait_prev();
         __syncthreads();
       }
-      if (turns) fast_tile<BITS, DT>(a, i0, stages + s * kStageBytes, tile_refs[s], staging, prm);
+      if (turns) fast_tile<BITS, DT>(a, i0, stages + s * kStageBytes, tile_refs[s], staging, prm, run_go);
     } else if (ring_item_is_few(a, i0)) {
       __syncthreads();
-      ring_item_few<BITS, ROPE>(a, i0);
+      ring_item_few<BITS, ROPE>(a, i0, run_go[run_parity(a, i0)]);
     } else {
       __syncthreads();
-      other_item<BITS, ROPE>(a, i0, reinterpret_cast<uint8_t (*)[1536]>(staging), src, stages + s * kStageBytes);
+      other_item<BITS, ROPE>(a, i0, reinterpret_cast<uint8_t (*)[1536]>(staging), src, stages + s * kStageBytes,
+                             run_go[run_parity(a, i0)]);
     }
     if constexpr (kAhead == 2) {
       i0 = i1;

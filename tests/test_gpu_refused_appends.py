@@ -9,8 +9,8 @@ import s4kv_inputs as inp
 from plain_cache import INT8
 
 pytestmark = pytest.mark.gpu
-PLAIN = [INT8]        # formats of the plain append
-ROPE = [INT8, 8]      # of the rotating append
+PLAIN = [INT8, 4, 2]      # formats of the plain append
+ROPE = [INT8, 4, 2, 8]    # of the rotating append
 STEP = [INT8, 4, 2, 8]
 
 
