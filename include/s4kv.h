@@ -255,7 +255,12 @@ int s4kv_get_layout(const s4kv_cache* cache, s4kv_layout* out);
  * Effect: every key group completed by the new tokens is quantized into its two
  * pages, every value token leaving the R-window is quantized into its page
  * slot, the remaining new tokens go to the rings. Afterwards the slot is in the
- * canonical state of length T0 + new. One kernel launch. */
+ * canonical state of length T0 + new. One kernel launch.
+ * Of a sequence that is reported for its length, slot or table nothing is stored (the
+ * other sequences are appended), so a call made again by mistake changes nothing; of
+ * one with a page outside the pool everything but what that page would hold. Calls
+ * that append to the same slot of a layer must be ordered, on one stream for instance:
+ * while one runs, the slot's stored length holds no length. */
 int s4kv_append(s4kv_cache* cache, int layer, const void* k, const void* v, int num_new_tokens,
                 const int32_t* cu_new, const int32_t* slot_ids, const int32_t* seq_lens_before,
                 const int32_t* block_table, int bt_stride, int n, void* stream);

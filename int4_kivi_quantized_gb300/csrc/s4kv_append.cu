@@ -1204,9 +1204,11 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArg
 // ---- FP8 E4M3 pages ("4.4 KV Cache 量化", sections 4.1 and 4.2) ------------------
 // Every new token goes straight to its page: x / scale rounded to fp32, then the
 // saturating round-to-nearest-even conversion to E4M3. No ring, no group: an
-// item is (sequence, head, 32 new tokens); item 0 of a (sequence, head) checks
-// and advances the stored length. Warp w writes tokens w, w + 4, ...; lane l
-// owns channels 4l .. 4l+3 of a token (8 bytes of its key row, 8 of its value row).
+// item is (sequence, head, 32 new tokens); a CTA takes neighbouring ones, head by head.
+// Items of a (sequence, head) that goes on from stored tokens look at its length
+// together (goes_on), a run of them at once; else its item 0 checks and advances it.
+// Warp w writes tokens w, w + 4, ...; lane l owns channels 4l .. 4l+3 of a token (8
+// bytes of its key row, 8 of its value row).
 __device__ __forceinline__ uint32_t e4m3_of(float x, float scale) {
   return static_cast<uint32_t>(__nv_cvt_float_to_fp8(__fdiv_rn(x, scale), __NV_SATFINITE, __NV_E4M3));
 }
@@ -1217,7 +1219,11 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(AppendArgs a) {
   if (!build_prefix(a, pre, warp_tot)) return;
   const int total = pre[a.n];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+  const int ctas = static_cast<int>(gridDim.x), x = static_cast<int>(blockIdx.x);
+  const int each = total / ctas, more = total - each * ctas;   // the first `more` CTAs have one more
+  const int first = x * each + min(x, more), end = first + each + (x < more ? 1 : 0);
+  bool go = true;   // the verdict on the current (sequence, head)
+  for (int item = first; item < end; ++item) {
     int lo_i = 0, hi_i = a.n - 1;   // last i with pre[i] <= item
     while (lo_i < hi_i) {
       const int mid = (lo_i + hi_i + 1) >> 1;
@@ -1241,16 +1247,18 @@ __global__ void __launch_bounds__(kThreads) append_fp8_kernel(AppendArgs a) {
       continue;
     }
     const int* bt_row = a.block_table + static_cast<long long>(i) * a.bt_stride;
-    if (j == 0) {
+    const bool several = T0 != 0 && per > 1;
+    if (j == 0 || (several && item == first)) {
       int* len_word = a.lens + slot * a.H + h;
-      const int stored = *len_word;
-      if (T0 != 0 && stored != T0) {
-        if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_LENGTH, i);
-        continue;
-      }
+      go = T0 == 0 || (several ? goes_on(len_word, T0) : *len_word == T0);
       __syncthreads();   // every thread has read the stored length before it changes
-      if (tid == 0) *len_word = T1;
+      if (tid == 0 && go) {
+        if (several) looked(len_word, T0, T1, min(end - item, per - j), per);
+        else *len_word = T1;
+      }
+      if (tid == 0 && !go && j == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_LENGTH, i);
     }
+    if (!go) continue;
     const float ks = a.fp8_scale[h], vs = a.fp8_scale[a.H + h];
     const int n1 = min(ni, 32 * j + 32);
     for (int idx = 32 * j + warp; idx < n1; idx += kThreads / 32) {

@@ -9,9 +9,7 @@ import s4kv_inputs as inp
 from plain_cache import INT8
 
 pytestmark = pytest.mark.gpu
-PLAIN = [INT8, 4, 2]      # formats of the plain append
-ROPE = [INT8, 4, 2, 8]    # of the rotating append
-STEP = [INT8, 4, 2, 8]
+FORMATS = [INT8, 4, 2, 8]
 
 
 def _i32(*x):
@@ -49,7 +47,8 @@ def _refused(c, held):
 CALLS = [(30, 1), (31, 1), (10, 4), (10, 20), (8, 16), (16, 16), (32, 64), (33, 200), (5, 700), (1000, 1500)]
 
 
-@pytest.mark.parametrize("bits,rope", [(b, False) for b in PLAIN] + [(b, True) for b in ROPE])
+@pytest.mark.parametrize("bits", FORMATS)
+@pytest.mark.parametrize("rope", [False, True])
 @pytest.mark.parametrize("H", [1, 3, 8])
 @pytest.mark.parametrize("T0,new", CALLS)
 def test_a_call_made_again_stores_nothing(bits, rope, H, T0, new):
@@ -82,7 +81,8 @@ def test_a_call_made_again_stores_nothing(bits, rope, H, T0, new):
     assert lens == [0] * H + [T0 + 2 * new] * H
 
 
-@pytest.mark.parametrize("bits,rope", [(b, False) for b in PLAIN] + [(b, True) for b in ROPE])
+@pytest.mark.parametrize("bits", FORMATS)
+@pytest.mark.parametrize("rope", [False, True])
 @pytest.mark.parametrize("new", [1, 20, 300])
 def test_sequences_beside_a_refused_one_are_appended(bits, rope, new):
     """Of seven sequences every other one is refused: the pool is that of a call with the others alone."""
@@ -117,7 +117,7 @@ def test_sequences_beside_a_refused_one_are_appended(bits, rope, new):
     assert torch.equal(_held(a), _held(b))
 
 
-@pytest.mark.parametrize("bits", STEP)
+@pytest.mark.parametrize("bits", FORMATS)
 @pytest.mark.parametrize("T0", [1, 15, 16, 30, 31, 100])
 def test_a_decode_step_made_again_stores_nothing(bits, T0):
     H, Hq = 2, 8
@@ -144,7 +144,7 @@ def test_a_decode_step_made_again_stores_nothing(bits, T0):
     assert c.status() == (0, 0)
 
 
-@pytest.mark.parametrize("bits", [INT8, 4, 2, 8])
+@pytest.mark.parametrize("bits", FORMATS)
 @pytest.mark.parametrize("H", [1, 3, 5, 8, 64])
 def test_chunks_behind_stored_tokens(bits, H):
     """Chunks of whole pages behind stored tokens, in one call and in pieces, leave the same bytes."""
