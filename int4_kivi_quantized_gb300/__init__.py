@@ -336,7 +336,10 @@ def _address(t):
 class KVCache:
     """A cache bound to a torch-allocated device pool (torch provides memory only).
 
-    bits: 4 (default), 2, 8 (FP8 E4M3) or "int8" (one scale per 16-token block and head)."""
+    bits: 4 (default), 2, 8 (FP8 E4M3) or "int8" (one scale per 16-token block and head).
+
+    A call with stream= runs on that stream, and results that it makes itself are that stream's
+    memory, as under torch.cuda.stream(stream); order other streams behind it before they read them."""
 
     def __init__(self, num_layers, num_pages, num_kv_heads, residual_v, max_slots, dtype="fp16",
                  device="cuda", bits=4):
@@ -401,7 +404,7 @@ class KVCache:
         B, Hq, _ = q.shape
         if out is None:
             dt = torch.float32 if out_dtype == S4KV_F32 else self.torch_dtype
-            out = torch.empty((B, Hq, 128), dtype=dt, device=q.device)
+            out = self._made(stream, torch.empty, (B, Hq, 128), dtype=dt, device=q.device)
         if self.bits == S4KV_BITS_INT8:
             nbytes = self._window_bytes(B, 1, Hq, max_seq_len)
             ws, stream = self._scratch(nbytes, stream), self._handle(stream)
@@ -418,7 +421,7 @@ class KVCache:
         B, nq, Hq, _ = q.shape
         if out is None:
             dt = torch.float32 if out_dtype == S4KV_F32 else self.torch_dtype
-            out = torch.empty((B, nq, Hq, 128), dtype=dt, device=q.device)
+            out = self._made(stream, torch.empty, (B, nq, Hq, 128), dtype=dt, device=q.device)
         if self.bits == S4KV_BITS_INT8:
             nbytes = self._window_bytes(B, nq, Hq, max_seq_len)
             s4kv_multi_query_attention(self.h, layer, q, nq, Hq, block_table, block_table.shape[1], seq_lens, slot_ids, B,
@@ -456,6 +459,18 @@ class KVCache:
             return self._current_stream(self._index)
         return stream if isinstance(stream, int) else stream.cuda_stream
 
+    def _made(self, stream, make, *args, **kwargs):
+        """make(...), a result of a call on `stream`: of that stream's memory, and kept from it while
+        the current stream still uses what it was handed."""
+        if stream is None:
+            return make(*args, **kwargs)
+        import torch
+        st = torch.cuda.ExternalStream(stream, device=self.pool.device) if isinstance(stream, int) else stream
+        with torch.cuda.stream(st):
+            t = make(*args, **kwargs)
+        t.record_stream(torch.cuda.current_stream(self.pool.device))
+        return t
+
     def _scratch(self, nbytes, stream):
         """Scratch of one call, allocated on its stream: calls on other streams and captured graphs share none of it."""
         import torch
@@ -472,7 +487,7 @@ class KVCache:
             n = self._sizes[B, nq, Hq] = max(16, s4kv_window_workspace_bytes(self.h, B, nq, Hq, max_seq_len))
         return n
 
-    def _out(self, out, name, shape, out_dtype, like=None):
+    def _out(self, out, name, shape, out_dtype, stream, like=None):
         """`out`, checked, or a new tensor (like: a checked tensor of this shape, which torch is quicker to copy)."""
         import torch
         if out_dtype == self.cdtype:
@@ -483,8 +498,10 @@ class KVCache:
             raise ValueError("out_dtype is S4KV_F32 or the cache's dtype")
         if out is None:
             if like is None:
-                return torch.empty(shape, dtype=dt, device=self.pool.device)
-            return torch.empty_like(like) if like.dtype is dt else torch.empty_like(like, dtype=dt)
+                return self._made(stream, torch.empty, shape, dtype=dt, device=self.pool.device)
+            if like.dtype is dt:
+                return self._made(stream, torch.empty_like, like)
+            return self._made(stream, torch.empty_like, like, dtype=dt)
         self._tensor(out, name, dt, shape)
         return out
 
@@ -511,7 +528,7 @@ class KVCache:
         if q is not None:
             heads = self._tensor(q, "q", dt, (tokens, None, 128))[1]
             if q_out is None:
-                q_out = torch.empty_like(q)
+                q_out = self._made(stream, torch.empty_like, q)
             elif q_out is not q:
                 self._tensor(q_out, "q_out", dt, (tokens, heads, 128))
         elif q_out is not None:
@@ -534,7 +551,7 @@ class KVCache:
             raise ValueError("block_table has fewer rows than there are sequences")
         if slot_ids is not None:
             self._tensor(slot_ids, "slot_ids", torch.int32, (B,))
-        out = self._out(out, "out", (B, nq, Hq, 128), out_dtype, q)
+        out = self._out(out, "out", (B, nq, Hq, 128), out_dtype, stream, q)
         max_seq_len = int(max_seq_len)
         nbytes = self._window_bytes(B, nq, Hq, max_seq_len)
         ws = self._scratch(nbytes, stream)
@@ -564,8 +581,8 @@ class KVCache:
             self._tensor(slot_ids, "slot_ids", i32, (n,))
         num_rows = int(num_rows)
         shape = (num_rows, self.H, 128)
-        out_k = self._out(out_k, "out_k", shape, out_dtype)
-        out_v = self._out(out_v, "out_v", shape, out_dtype, out_k)
+        out_k = self._out(out_k, "out_k", shape, out_dtype, stream)
+        out_v = self._out(out_v, "out_v", shape, out_dtype, stream, out_k)
         _check(_lib.s4kv_gather(self.h, int(layer), block_table.data_ptr(), width, seq_lens.data_ptr(), _address(slot_ids),
                                 _address(first), cu_rows.data_ptr(), num_rows, n, out_k.data_ptr(), out_v.data_ptr(),
                                 out_dtype, self._handle(stream)), "s4kv_gather")
@@ -573,8 +590,8 @@ class KVCache:
 
     def dequant(self, layer, slot, block_table_row, seq_len, stream=None):
         import torch
-        k = torch.empty((self.H, seq_len, 128), dtype=torch.float32, device=self.pool.device)
-        v = torch.empty_like(k)
+        k = self._made(stream, torch.empty, (self.H, seq_len, 128), dtype=torch.float32, device=self.pool.device)
+        v = self._made(stream, torch.empty_like, k)
         s4kv_dequant_debug(self.h, layer, slot, block_table_row, seq_len, k, v, stream)
         return k, v
 
