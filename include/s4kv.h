@@ -100,8 +100,10 @@
  *   A byte holds c + 128. Tokens of the unfinished block (the newest T mod 16)
  *   wait in 16-bit rings of 16 rows and are quantized as the block fills; a
  *   block with an element that is not finite restores to values that are not.
- *   Attention takes values of any size; keys beyond 2^100 in magnitude, where
- *   a query sees them, may make its row NaN.
+ *   Attention takes values of any size, and queries and keys up to 2^100 in
+ *   magnitude whose products stay below it; beyond, where a query sees such a key,
+ *   its row may be NaN. (Elements below 2^-28 of the largest of a bf16 query may
+ *   lose bits.)
  *   Lane L = 4a + b (a in 0..7, b in 0..3); word (kp, L), kp in 0..3, is the 16
  *   bytes at kp*512 + L*16 of a half.
  *   Keys: word (kp, L) holds channels 32b + 8kp + 0..7 of tokens a and a + 8;
@@ -109,6 +111,11 @@
  *   Values: bytes 8u .. 8u+7 of word (kp, L), m = 2kp + u: channels 8a + m (lo) and
  *     64 + 8a + m (hi) as (token 2b, lo), (2b+1, lo), (2b, hi), (2b+1, hi),
  *     (2b+8, lo), (2b+9, lo), (2b+8, hi), (2b+9, hi).
+ * What attention on the other pages holds in f16, so that a magnitude beyond 65504
+ *   becomes an infinity: on 4- and 2-bit pages each query element times the key scale
+ *   of its channel and group, and each probability times a value scale (probabilities
+ *   up to 2^6 before their sum divides them); on FP8 pages the queries of decode and
+ *   multi-query calls. Windows on FP8 pages take queries as INT8 pages do.
  * Residual rings (cache dtype): key ring [slot][kv head][32][128], token t at
  *   row t mod 32; value ring [slot][kv head][R][128], token t at row t mod R.
  * Canonical state of a sequence of length T: keys of tokens < 32*floor(T/32)

@@ -82,6 +82,7 @@ struct WSmem {
   alignas(128) uint8_t region[kWarps][kRegionOf<FMT, NC>];
   alignas(16) float ptile[kByte<FMT> ? 1 : kWarps][32 * kPRow];
   alignas(16) uint4 q[NC == 16 ? kWarps : 1][NC == 16 ? 8 : 1][32];   // 16 columns: the queries as A operands, by slice and lane
+  float zscale[NC == 16 ? kWarps : 1][NC == 16 ? 16 : 1];   // and their score scales, by column
   alignas(8) uint64_t bar[kWarps][4];
 };
 // Behind it: the cost prefix of the line (int64 [B + 1]), or what a one-segment
@@ -238,6 +239,16 @@ __device__ __forceinline__ void add_only(float (&o)[4], const int (&opos)[2], in
   for (int e = 0; e < 4; ++e) o[e] = opos[e & 1] == only ? o[e] + t[e] : o[e];
 }
 
+// bf16 queries enter the MMAs as f16. Their range is the wider one, so each column is
+// taken at the power of two 2^k that brings its largest element to 2^14 .. 2^15: exact,
+// and elements down to 2^-28 of the largest keep every bit. k of a column whose largest
+// magnitude has the bits `top` (0 for zeros, infinities and NaN, which stay what they are).
+__device__ __forceinline__ int query_power(uint32_t top) {
+  const int e = static_cast<int>(top >> 7);
+  return top == 0 || e == 255 ? 0 : min(14 + 127 - e, 120);
+}
+__device__ __forceinline__ float power_of_two(int k) { return __int_as_float((k + 127) << 23); }   // -126 <= k <= 127
+
 // What INT8 accumulators lack of the true output, until the records are done.
 constexpr float kI8Rest = 262144.0f;
 
@@ -251,18 +262,24 @@ __device__ __forceinline__ uint32_t codes01(uint32_t w) { return less1152(__byte
 __device__ __forceinline__ uint32_t codes23(uint32_t w) { return less1152(__byte_perm(w, 0x64646464u, 0x4342)); }
 
 // One staged record of 16 tokens. Keys: lane (gi, ti) reads its words as the B
-// operand of tokens gi and gi + 8; q as A. qa: f16 queries, rows gi (and gi + 8);
-// zoff[ct] = -128 scale sum_c q_c (INT8). scale = sm_scale log2(e) (times the
-// key scale on FP8). Sixteen columns leave no registers for the queries: qs holds
-// them. kMask: tokens are masked by `cut` and the columns' positions.
+// operand of tokens gi and gi + 8; q as A. qa: f16 queries, rows gi (and gi + 8), each
+// column at a power of two of its own (query_power); zscale[ct] = sm_scale log2(e) over
+// that power, times the key scale (FP8) or the 2^24 of the codes' subnormals (INT8), and
+// zoff[ct] = -128 scale sum_c q_c (INT8).
+// Sixteen columns leave no registers for the queries and their scales: qs and zs hold
+// them (32 sequences of 1024 to 8192 tokens, 16 query tokens: 197.5 us, scales in registers
+// 199.6). kMask: tokens are masked by `cut` and the columns' positions.
 template <int FMT, int NC, bool kMask>
 __device__ __forceinline__ void byte_block(const char* rec, ByteState<NC>& s, const uint32_t (&qa)[8][2], const uint4 (*qs)[32],
-                                           const float (&zoff)[NC / 8], float scale, const Cut& cut,
+                                           const float (&zoff)[NC / 8], float zscale0, const float* zs, const Cut& cut,
                                            const int (&pos)[NC / 8], const int (&opos)[NC / 8][2]) {
   constexpr int CT = NC / 8;
   const int lane = threadIdx.x & 31, ti = lane & 3;
   float z[CT][4];
   float vscale = 1.0f;
+  float zscale[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) zscale[c] = NC == 16 ? zs[8 * c + (lane >> 2)] : zscale0;
   {
     // two chains of four MMAs for each eight tokens instead of one of eight
     float s0[4] = {0.0f, 0.0f, 0.0f, 0.0f}, s1[4] = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -302,9 +319,9 @@ __device__ __forceinline__ void byte_block(const char* rec, ByteState<NC>& s, co
     if constexpr (FMT == kI8) {
       const float2 sc = *reinterpret_cast<const float2*>(rec + Rec<kI8>::kKs);
       vscale = sc.y;
-      const float c1 = sc.x * (kMask ? scale : scale * 16777216.0f);
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
+        const float c1 = sc.x * (kMask ? zscale[c] * (1.0f / 16777216.0f) : zscale[c]);
         const float c2 = kMask ? 0.0f : sc.x * zoff[c];
         z[c][0] = fmaf(s0[2 * c], c1, c2);
         z[c][1] = fmaf(s0[2 * c + 1], c1, c2);
@@ -314,10 +331,10 @@ __device__ __forceinline__ void byte_block(const char* rec, ByteState<NC>& s, co
     } else {
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
-        z[c][0] = s0[2 * c] * scale;
-        z[c][1] = s0[2 * c + 1] * scale;
-        z[c][2] = s1[2 * c] * scale;
-        z[c][3] = s1[2 * c + 1] * scale;
+        z[c][0] = s0[2 * c] * zscale[c];
+        z[c][1] = s0[2 * c + 1] * zscale[c];
+        z[c][2] = s1[2 * c] * zscale[c];
+        z[c][3] = s1[2 * c + 1] * zscale[c];
       }
     }
   }
@@ -1201,21 +1218,40 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(WindowArgs a) {
         };
         for (int i = 0; i < n && i < kStagesOf<FMT>; ++i) issue(i, i);
         // queries: f16 operands, and (INT8) -128 scale sum_c q_c
-        const float ks = FMT == 8 ? a.fp8_scale[h] : 1.0f;
-        const float zscale = a.sm_scale_log2 * ks;
+        const float ks = FMT == 8 ? a.fp8_scale[h] : 0.0f;
         uint32_t qa[8][2];        // 8 columns: row gi, channels c_0 c_1 | c_2 c_3 of slice kk
-        float zoff[CT];
+        float zoff[CT], zscale0 = 0.0f;
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
+          uint4 row[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            row[j] = qrow[c] ? reinterpret_cast<const uint4*>(qrow[c])[4 * ti + j] : make_uint4(0u, 0u, 0u, 0u);
+          float up = 1.0f;
+          float zscale = a.sm_scale_log2 * (FMT == kI8 ? 16777216.0f : ks);
+          if (a.dtype == S4KV_BF16) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              top = __vmaxu2(__vmaxu2(__vmaxu2(__vmaxu2(top, row[j].x & 0x7fff7fffu), row[j].y & 0x7fff7fffu), row[j].z & 0x7fff7fffu),
+                             row[j].w & 0x7fff7fffu);
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int k = query_power(max(top & 0xffffu, top >> 16));
+            up = power_of_two(k);
+            zscale *= power_of_two(-k);
+          }
+          zscale0 = zscale;   // (8 columns)
+          if (NC == 16 && ti == 0) sm.zscale[warp][8 * c + gi] = zscale;
           float sum = 0.0f;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint4 w4 = qrow[c] ? reinterpret_cast<const uint4*>(qrow[c])[4 * ti + j] : make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+            const uint32_t w[4] = {row[j].x, row[j].y, row[j].z, row[j].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               uint32_t x = w[i];
-              if (a.dtype == S4KV_BF16) x = pack_f16x2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+              if (a.dtype == S4KV_BF16)
+                x = pack_f16x2(__uint_as_float(x << 16) * up, __uint_as_float(x & 0xffff0000u) * up);
               if constexpr (NC == 8) qa[2 * j + (i >> 1)][i & 1] = x;
               else reinterpret_cast<uint32_t*>(&sm.q[warp][2 * j + (i >> 1)][lane])[2 * (i & 1) + c] = x;
               if (FMT == kI8) {
@@ -1226,8 +1262,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(WindowArgs a) {
           }
           sum += __shfl_xor_sync(0xffffffffu, sum, 1);
           sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-          zoff[c] = -128.0f * a.sm_scale_log2 * sum;
+          zoff[c] = -128.0f / 16777216.0f * zscale * sum;
         }
+        if (NC == 16) __syncwarp();   // the columns' scales are there
         bool ok = true;
         int s = 0;
         for (int i = 0; i < n; ++i) {
@@ -1238,10 +1275,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(WindowArgs a) {
             }
             const char* rec = reinterpret_cast<const char*>(region + s * Rec<kI8>::kBytes);
             if (u0 + i < pl.nf) {
-              byte_block<FMT, NC, false>(rec, st, qa, sm.q[NC == 16 ? warp : 0], zoff, zscale, cut, pos, opos);
+              byte_block<FMT, NC, false>(rec, st, qa, sm.q[NC == 16 ? warp : 0], zoff, zscale0, sm.zscale[NC == 16 ? warp : 0], cut, pos, opos);
             } else {
               cut.tok0 = pl.block_of(u0 + i) * BT;
-              byte_block<FMT, NC, true>(rec, st, qa, sm.q[NC == 16 ? warp : 0], zoff, zscale, cut, pos, opos);
+              byte_block<FMT, NC, true>(rec, st, qa, sm.q[NC == 16 ? warp : 0], zoff, zscale0, sm.zscale[NC == 16 ? warp : 0], cut, pos, opos);
             }
           }
           if (i + kStagesOf<FMT> < n) issue(s, i + kStagesOf<FMT>);
