@@ -499,8 +499,8 @@ class KVCache:
         if out is None:
             if like is None:
                 return self._made(stream, torch.empty, shape, dtype=dt, device=self.pool.device)
-            if like.dtype is dt:
-                return self._made(stream, torch.empty_like, like)
+            if stream is None:
+                return torch.empty_like(like) if like.dtype is dt else torch.empty_like(like, dtype=dt)
             return self._made(stream, torch.empty_like, like, dtype=dt)
         self._tensor(out, name, dt, shape)
         return out
@@ -528,7 +528,7 @@ class KVCache:
         if q is not None:
             heads = self._tensor(q, "q", dt, (tokens, None, 128))[1]
             if q_out is None:
-                q_out = self._made(stream, torch.empty_like, q)
+                q_out = torch.empty_like(q) if stream is None else self._made(stream, torch.empty_like, q)
             elif q_out is not q:
                 self._tensor(q_out, "q_out", dt, (tokens, heads, 128))
         elif q_out is not None:
