@@ -252,7 +252,8 @@ int s4kv_get_layout(const s4kv_cache* cache, s4kv_layout* out);
  *   cu_new           int32 [n+1], non-decreasing, cu_new[0] = 0,
  *                    cu_new[n] = num_new_tokens.
  *   slot_ids         int32 [n] residual slot of each sequence (NULL: slot = i);
- *                    slots must be distinct within one call.
+ *                    slots must be distinct within one call (a slot named twice
+ *                    holds nothing of use until an append starts it afresh).
  *   seq_lens_before  int32 [n] current length T0 of each sequence; 0 starts the
  *                    slot afresh, any other value must equal the slot's stored
  *                    length (else S4KV_DEV_BAD_LENGTH).
@@ -399,6 +400,8 @@ int s4kv_window_attention(s4kv_cache* cache, int layer, const void* q, int num_q
  *                does not cover it (to the end of its last whole 32-token group on KIVI
  *                pages) S4KV_DEV_BAD_TABLE. Rows of a
  *                sequence that is reported, and of a page that is, are left as they were.
+ *                A sequence without rows is not looked at: its length, slot and table
+ *                row may hold anything.
  *   out_k, out_v [num_rows][H_kv][128] in out_dtype (S4KV_F32, or the cache dtype: the
  *                restored fp32 value rounded once), 16-byte aligned.
  * Every page format; one kernel launch; n up to 8192. Only the pages that the ranges
@@ -512,7 +515,8 @@ int s4kv_kv_bytes(const s4kv_config* cfg, double batch, double tokens, s4kv_kv_b
  *   S4KV_OPT_WINDOW_FORM   launch form of window calls and of attention on INT8
  *                          pages: 0 (default) by the call's size, 1 = slices over
  *                          all SMs and a combine kernel, 2 = one launch, a cluster of
- *                          CTAs for each (sequence, kv head, tile of columns). */
+ *                          CTAs for each (sequence, kv head, tile of columns), where
+ *                          these are at most 65535 (else as 1). */
 enum { S4KV_OPT_DECODE_WARPS = 1, S4KV_OPT_DECODE_IMPL = 2, S4KV_OPT_WAIT_NS = 3, S4KV_OPT_TAIL_COST = 4,
        S4KV_OPT_KEY_SPLIT = 5, S4KV_OPT_MQ_KERNEL = 6, S4KV_OPT_WINDOW_FORM = 7 };
 int s4kv_set_option(s4kv_cache* cache, int option, long long value);
