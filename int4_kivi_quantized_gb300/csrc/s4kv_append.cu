@@ -459,6 +459,7 @@ struct Item {
   bool fast;                         // a tile whose key group is made only of new rows
   bool several;                      // the stored length is looked at by the ring item and its tiles (goes_on);
                                      // else by the ring item alone, or not (a slot that starts afresh held any)
+  bool last;                         // of its (sequence, head)
 };
 
 __device__ __forceinline__ Item item_of(const AppendArgs& a, const int* pre, const int* seq, int item) {
@@ -483,13 +484,10 @@ __device__ __forceinline__ Item item_of(const AppendArgs& a, const int* pre, con
   it.j = r - h * per;
   it.tile = tlo + it.j - 1;
   it.several = per > 1 && it.T0 != 0;
+  it.last = it.j + 1 == per;
   it.fast = it.j >= 1 && kG * it.tile >= it.T0 && kG * it.tile + kG <= it.T1;
   return it;
 }
-
-// A CTA's items of one (sequence, head) are a run: its first item, or the CTA's, opens it.
-// Runs that follow one another differ in this bit.
-__device__ __forceinline__ int run_parity(const AppendArgs& a, const Item& it) { return (it.i * a.H + it.h) & 1; }
 
 // First item whose share of the work line starts at or after x: the work line
 // lays the items end to end in item order, a ring item weighing ring_weight and
@@ -518,9 +516,10 @@ __device__ __forceinline__ int item_from_cost(const AppendArgs& a, const int* pr
 
 // Issues the cp.async copies of a fast tile's key and value rows into a stage.
 // The rows of a whole new tile into its stage, and (thread 0) the tile's slot
-// and its two pool pages into ref[0..2], all in the calling threads' current
-// cp.async group. A table too narrow for the tile leaves ref alone (the tile
-// reports it and writes nothing).
+// and its two pool pages into ref[0..2], and the stored length where it is looked at
+// into ref[3], all in the calling threads' current cp.async group. A table too narrow
+// for the tile leaves ref alone (the tile reports it and writes nothing), a slot out of
+// range ref[3].
 __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
 }
@@ -531,6 +530,10 @@ __device__ __forceinline__ void tile_prefetch(const AppendArgs& a, const Item& i
     else ref[0] = it.i;
     cp_async4(ref + 1, bt_row + 2 * it.tile);
     cp_async4(ref + 2, bt_row + 2 * it.tile + 1);
+    if (it.several) {
+      const int slot = a.slot_ids ? a.slot_ids[it.i] : it.i;
+      if (slot >= 0 && slot < a.max_slots) cp_async4(ref + 3, a.lens + slot * a.H + it.h);
+    }
   }
   // thread: chunk q of rows t, t + 8, t + 16, t + 24
   const int t = threadIdx.x >> 4, q = threadIdx.x & 15;
@@ -601,14 +604,15 @@ __device__ __noinline__ void value_lane(const uint8_t* Vs, int row, int tok, uin
   if (flags) value_bytes_fix<BITS, DT>(flags, Vs, row, k, lo, sc, vc);
 }
 
+// Returns, as the other items do, whether the (sequence, head) is stored.
 template <int BITS, int DT>
-__device__ void fast_tile(const AppendArgs& a, const Item& it, const uint8_t* stage, const int* tile_ref,
-                          uint8_t* staging, float* prm, const int* run_go) {
+__device__ bool fast_tile(const AppendArgs& a, const Item& it, const uint8_t* stage, const int* tile_ref,
+                          uint8_t* staging, float* prm) {
   using F = Rec<BITS>;
   const int tid = threadIdx.x, w = tid >> 5, l = tid & 31;
   if (static_cast<long long>(a.bt_stride) * kP < it.T1) {
     if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_TABLE, it.i);
-    return;
+    return false;
   }
   // tile_ref: the slot and the tile's two pool pages, loaded with the tile's rows
   // (tile_prefetch) and checked before the records are written
@@ -773,12 +777,14 @@ __device__ void fast_tile(const AppendArgs& a, const Item& it, const uint8_t* st
   }
   // read before the barrier: once past it, thread 0 may refill this stage's refs
   const int slot = tile_ref[0], pp0 = tile_ref[1], pp1 = tile_ref[2];
+  bool go = !it.several || went_on(tile_ref[3], it.T0);
   __syncthreads();
   char* rec0 = nullptr;
   char* rec1 = nullptr;
   if (slot < 0 || slot >= a.max_slots) {
     if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_SLOT, slot);
-  } else if (run_go[run_parity(a, it)]) {   // (else the ring item reports the length)
+    go = false;
+  } else if (go) {   // (else the ring item reports the length)
     if (pp0 >= 0 && pp0 < a.num_pages) rec0 = a.pages + (static_cast<long long>(pp0) * a.H + it.h) * F::kBytes;
     else if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, pp0);
     if (pp1 >= 0 && pp1 < a.num_pages) rec1 = a.pages + (static_cast<long long>(pp1) * a.H + it.h) * F::kBytes;
@@ -793,6 +799,7 @@ __device__ void fast_tile(const AppendArgs& a, const Item& it, const uint8_t* st
     const int off = (q - (p1 ? kChunks : 0)) * 16;
     if (rec) *reinterpret_cast<uint4*>(rec + off) = *reinterpret_cast<const uint4*>((p1 ? st1 : st0) + off);
   }
+  return go;
 }
 
 // Copies the new rows bound for a ring: tokens [tb, T1) into rows t % mod. The
@@ -843,22 +850,22 @@ __device__ __forceinline__ bool ring_item_is_few(const AppendArgs& a, const Item
 }
 
 template <int BITS, bool ROPE = false>
-__device__ __forceinline__ void ring_item_few(const AppendArgs& a, const Item& it, bool go) {
+__device__ __forceinline__ bool ring_item_few(const AppendArgs& a, const Item& it) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i = it.i, h = it.h, T0 = it.T0, T1 = it.T1, row0 = it.row0;
   const int slot = a.slot_ids ? a.slot_ids[i] : i;
   if (slot < 0 || slot >= a.max_slots) {
     if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_SLOT, slot);
-    return;
+    return false;
   }
   if (static_cast<long long>(a.bt_stride) * kP < T1) {
     if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_TABLE, i);
-    return;
+    return false;
   }
   if constexpr (ROPE) {
     if (T1 > a.rope.max_pos) {   // a token past the rotation table: nothing of the sequence is stored
       if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_POSITION, i);
-      return;
+      return false;
     }
   }
   Ctx c{&a, a.block_table + static_cast<long long>(i) * a.bt_stride, slot};
@@ -867,7 +874,7 @@ __device__ __forceinline__ void ring_item_few(const AppendArgs& a, const Item& i
   const int Tk1 = T1 & ~(kG - 1);
   const int Tv0 = max(0, T0 - a.R), Tv1 = max(0, T1 - a.R);
   int* len_word = a.lens + slot * a.H + h;
-  const int stored = *len_word;
+  const int stored = __ldcg(len_word);
   const int tv = Tv0 + warp, vend = min(T0, Tv1);
   uint2 vraw = make_uint2(0u, 0u);
   int vpage = 0;
@@ -884,10 +891,10 @@ __device__ __forceinline__ void ring_item_few(const AppendArgs& a, const Item& i
   }
   if (tid < (T1 - vb) * 16)
     vfirst = reinterpret_cast<const uint4*>(row_ptr(a.v, row0 + (vb + tid / 16 - T0), a.H, h))[tid % 16];
-  if (it.several ? !go : T0 != 0 && stored != T0) {
+  if (it.several ? !went_on(stored, T0) : T0 != 0 && stored != T0) {
     if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_LENGTH, i);
     __syncthreads();
-    return;
+    return false;
   }
   if (tv < vend) value_token_row<BITS>(c, h, tv, vraw, vpage);
   __syncthreads();
@@ -895,27 +902,28 @@ __device__ __forceinline__ void ring_item_few(const AppendArgs& a, const Item& i
   ring_copy(vring, a.R, vb, T1, a.v, static_cast<long long>(row0) - T0, a.H, h, vfirst, a.rope, a.dtype);
   if (tid == 0 && !it.several) *len_word = T1;
   __syncthreads();
+  return true;
 }
 
 // Ring items and the tiles that are not whole new key groups.
 template <int BITS, bool ROPE = false>
-__device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint8_t (*stage)[1536], const uint16_t** src,
-                                       uint8_t* rows, bool go) {
+__device__ __noinline__ bool other_item(const AppendArgs& a, const Item it, uint8_t (*stage)[1536], const uint16_t** src,
+                                       uint8_t* rows) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i = it.i, h = it.h, j = it.j, T0 = it.T0, T1 = it.T1, row0 = it.row0;
   const int slot = a.slot_ids ? a.slot_ids[i] : i;
   if (slot < 0 || slot >= a.max_slots) {
     if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_SLOT, slot);
-    return;
+    return false;
   }
   if (static_cast<long long>(a.bt_stride) * kP < T1) {
     if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_TABLE, i);
-    return;
+    return false;
   }
   if constexpr (ROPE) {
     if (T1 > a.rope.max_pos) {   // a token past the rotation table: nothing of the sequence is stored
       if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_POSITION, i);
-      return;
+      return false;
     }
   }
   Ctx c{&a, a.block_table + static_cast<long long>(i) * a.bt_stride, slot};
@@ -931,7 +939,7 @@ __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint
     // first value token leaving the window per warp (ring row and page), and
     // each thread's first 16 bytes of the new rows bound for the rings.
     int* len_word = a.lens + slot * a.H + h;
-    const int stored = *len_word;
+    const int stored = __ldcg(len_word);
     const int vend = min(T0, Tv1);
     // A decode step's few leaving tokens (one per warp at most) go by the token
     // path, their rows and pages loaded together with the stored length.
@@ -952,10 +960,10 @@ __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint
     }
     if (tid < (T1 - vb) * 16)
       vfirst = reinterpret_cast<const uint4*>(row_ptr(a.v, row0 + (vb + tid / 16 - T0), a.H, h))[tid % 16];
-    if (it.several ? !go : T0 != 0 && stored != T0) {
+    if (it.several ? !went_on(stored, T0) : T0 != 0 && stored != T0) {
       if (tid == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_LENGTH, i);
       __syncthreads();
-      return;
+      return false;
     }
     const int Tk0 = T0 & ~(kG - 1);
     if (Tk0 < T0 && Tk0 + kG <= T1) {   // first key group mixes ring and new rows
@@ -1031,7 +1039,7 @@ __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint
     if (tid == 0 && !it.several) *len_word = T1;
     __syncthreads();
   } else {
-    if (!go) return;   // the ring item reports it
+    if (it.several && !goes_on(a.lens + slot * a.H + h, T0)) return false;   // the ring item reports it
     const int tile = it.tile;
     const int t0 = tile * 32;
     if (!ROPE && t0 >= T0 && t0 + kG <= T1) {      // a key group made only of new rows (with a rotation always a fast tile)
@@ -1044,22 +1052,15 @@ __device__ __noinline__ void other_item(const AppendArgs& a, const Item it, uint
       value_token<BITS>(c, h, t, row_ptr(a.v, row0 + (t - T0), a.H, h));
     __syncthreads();
   }
+  return true;
 }
 
-// Whether a run's items may store (Item::several): one thread looks for all of them, `left`
-// or to the end of the (sequence, head). What keeps a sequence from being stored at all is
-// checked by every item.
-template <bool ROPE>
-__device__ __noinline__ bool run_goes_on(const AppendArgs& a, int i, int h, int j, int T0, int T1, int left) {
+// A CTA's items of one (sequence, head), `done` of them, the last one item j, have looked at
+// its stored length (Item::several; one thread).
+__device__ __noinline__ void run_looked(const AppendArgs& a, int i, int h, int j, int T0, int T1, int done) {
   const int slot = a.slot_ids ? a.slot_ids[i] : i;
-  if (slot < 0 || slot >= a.max_slots || static_cast<long long>(a.bt_stride) * kP < T1 || (ROPE && T1 > a.rope.max_pos))
-    return false;
-  int* len = a.lens + slot * a.H + h;
-  if (!goes_on(len, T0)) return false;
   int lo;
-  const int total = 1 + tile_range(T0, T1, a.R, &lo);
-  looked(len, T0, T1, min(left, total - j), total);
-  return true;
+  looked(a.lens + slot * a.H + h, T0, T1, min(j + 1, done), 1 + tile_range(T0, T1, a.R, &lo));
 }
 
 // The staged key rows of a fast tile (first token t0) turned in place, each thread
@@ -1147,7 +1148,6 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArg
     cp_async_commit();
   }
   int s = 0;
-  __shared__ int run_go[2];   // verdict on the current run, by run_parity (the other one may still be read)
   const int first = item;
   while (item < total) {
     Item in;   // the item kAhead ahead
@@ -1158,8 +1158,7 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArg
       if (in.fast) tile_prefetch(a, in, stages + sn * kStageBytes, tile_refs[sn]);
     }
     cp_async_commit();
-    if ((item == first || i0.j == 0) && threadIdx.x == 0)
-      run_go[run_parity(a, i0)] = !i0.several || run_goes_on<ROPE>(a, i0.i, i0.h, i0.j, i0.T0, i0.T1, total - item);
+    bool go = false;
     // One barrier before each item: the item's cp.async rows are in shared
     // memory, and the previous item is done with the staging buffer (a fast
     // tile's stage is refilled only kNumStages - 1 items later, past that
@@ -1177,15 +1176,17 @@ __global__ void __launch_bounds__(kThreads, kAppendCtas) append_kernel(AppendArg
         cp_async_wait_prev();
         __syncthreads();
       }
-      if (turns) fast_tile<BITS, DT>(a, i0, stages + s * kStageBytes, tile_refs[s], staging, prm, run_go);
+      if (turns) go = fast_tile<BITS, DT>(a, i0, stages + s * kStageBytes, tile_refs[s], staging, prm);
     } else if (ring_item_is_few(a, i0)) {
       __syncthreads();
-      ring_item_few<BITS, ROPE>(a, i0, run_go[run_parity(a, i0)]);
+      go = ring_item_few<BITS, ROPE>(a, i0);
     } else {
       __syncthreads();
-      other_item<BITS, ROPE>(a, i0, reinterpret_cast<uint8_t (*)[1536]>(staging), src, stages + s * kStageBytes,
-                             run_go[run_parity(a, i0)]);
+      go = other_item<BITS, ROPE>(a, i0, reinterpret_cast<uint8_t (*)[1536]>(staging), src, stages + s * kStageBytes);
     }
+    // the end of this CTA's items of the (sequence, head): all of them have looked
+    if (threadIdx.x == 0 && i0.several && go && (i0.last || item + 1 == total))
+      run_looked(a, i0.i, i0.h, i0.j, i0.T0, i0.T1, item - first + 1);
     if constexpr (kAhead == 2) {
       i0 = i1;
       i1 = in;

@@ -286,10 +286,8 @@ __device__ __forceinline__ void report(int* status, int code, int detail, int ar
 // counts: the first turns T0 into minus its part, the others subtract theirs, the last one
 // leaves T1. So a length that is T1 already (the same append again) is not taken for one
 // that this launch made, and all items of a (sequence, head) decide alike.
-__device__ __forceinline__ bool goes_on(const int* len, int T0) {
-  const int v = __ldcg(len);
-  return v == T0 || v < 0;
-}
+__device__ __forceinline__ bool went_on(int v, int T0) { return v == T0 || v < 0; }
+__device__ __forceinline__ bool goes_on(const int* len, int T0) { return went_on(__ldcg(len), T0); }
 __device__ __forceinline__ void looked(int* len, int T0, int T1, int part, int total) {
   if (atomicCAS(len, T0, part < total ? -part : T1) != T0 && atomicAdd(len, -part) == part - total) atomicExch(len, T1);
 }
