@@ -1099,8 +1099,8 @@ __device__ __forceinline__ void turn_queries(const AppendArgs& a) {
 
 // Whether a CTA turns its share of the queries before its items or after them. Items
 // are bound by instructions and latency, queries by bytes, so some of an SM's CTAs start
-// with either. 16000 tokens, 8 kv heads, 32 query heads, 4-bit pages: 103.5 us (bytes
-// 51.3; without queries 55.4, without the rotation 46.8); queries in CTAs of their own,
+// with either. 16000 tokens, 8 kv heads, 32 query heads, 4-bit pages: 105 us (bytes
+// 51.3; without queries 56, without the rotation 46.8); queries in CTAs of their own,
 // as on 8-bit pages, 106.8 at the best share (a tile takes its CTA as long as before, so
 // fewer CTAs take longer over the tiles).
 __device__ __forceinline__ bool queries_first(const AppendArgs& a) { return (blockIdx.x / a.num_sms) & 1; }

@@ -11,14 +11,16 @@
 //  * a page made only of new tokens: both tensors of one kv head. A warp's next page
 //    loads (cp.async, each lane the 16-byte pieces that it will need itself, so no
 //    barrier) while this one is reduced, coded and written as a whole record;
-//  * the edge of a (sequence, head), keys and values apart: the page that earlier
-//    and new tokens share, the last page if it is not full, and the stored length;
+//  * the edge of a (sequence, head), keys and values by two warps of a CTA: the page
+//    that earlier and new tokens share, the last page if it is not full, and the
+//    stored length;
 //  * with a rotation, 16 heads of one query row, in CTAs of their own.
 // 512 bytes of rows in and 258 (256) of record out per token and kv head: bound by
 // those bytes, with the arithmetic of a rotation and a code per element close behind.
 // Measured (16000 tokens, 8 kv heads, bf16; bytes at a plain copy's 6783 GB/s): INT8
-// 17.3 us (bytes 14.3), rotated 25, with 32 query heads 66 (52.5); FP8 rotated 26 and 70.
-// One token of each of 128 sequences with its rotation and query: 5.
+// 16.4 us (bytes 14.3), rotated 23.7, with 32 query heads 67 (52.5); FP8 rotated 25 and 68.
+// INT8, behind 1000 stored tokens of each of 8 sequences, whose lengths every item looks at:
+// 19.5. One token of each of 128 sequences with its rotation and query: 5.
 // This unit is compiled without FMA contraction; every rounding is spelled out.
 
 #include "s4kv_common.cuh"
@@ -35,16 +37,16 @@ static_assert(R8::kKc == Rec<8>::kKc && R8::kVc == Rec<8>::kVc, "both formats ke
 constexpr int kWarps = 4;
 static_assert(kWarps == 4, "two pairs of warps, a barrier each");
 constexpr int kThreads = 32 * kWarps;
-// (plain appends of 16000 tokens at 3 / 4 / 5: 18.4 / 17.3 / 16.2 us; rotated with 32 query
-// heads 86 / 66 / 77)
+// (plain appends of 16000 tokens at 3 / 4 / 5: 17.4 / 16.4 / 15.9 us; rotated with 32 query
+// heads 71 / 67 / 76)
 #ifndef S4KV_APPEND8_CTAS
 #define S4KV_APPEND8_CTAS 4
 #endif
 constexpr int kCtas = S4KV_APPEND8_CTAS;   // resident CTAs per SM the registers are budgeted for
 // Query items (16 heads of a row) that turn in the time of a page. CTAs of their own, so
-// that both go on side by side: 16000 tokens, 8 kv heads, 32 query heads 66 us (bytes:
-// 52.5), against 73 where each warp does pages, then queries; with 1 / 2 / 3 here 80 /
-// 66 / 70.
+// that both go on side by side: 16000 tokens, 8 kv heads, 32 query heads 67 us (bytes:
+// 52.5), against 73 where each warp does pages, then queries; with 1 / 2 / 3 here 79 /
+// 67 / 71.
 constexpr long long kPageQueries = 2;
 constexpr int kStage = 16 * 512;           // a warp's page in flight: keys, then values
 constexpr float kTiny = 7.8886091e-31f;    // 2^-100
@@ -496,7 +498,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) append8_kernel(AppendArgs a) 
   {
     // Page items (slot, head), head by head within a slot. A warp has one head and
     // neighbouring slots where the heads divide the warps (so that few sequences' lengths
-    // are looked at), else whatever comes: the next one is dslot and dhead on.
+    // are looked at and counted: 16000 tokens behind 1000 of each of 8 sequences 19.5 us,
+    // slots all warps apart 25), else whatever comes: the next one is dslot and dhead on.
     int slot = static_cast<int>(w0) / a.H, h = static_cast<int>(w0) - slot * a.H, end = slots, dslot = a.dslot;
     if (a.dhead == 0) {
       const int x = slot, more = slots - a.each * a.dslot;   // the first `more` warps of a head have one more

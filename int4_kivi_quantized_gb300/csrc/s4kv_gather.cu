@@ -13,9 +13,12 @@
 // brings them there.
 //
 // Measured (8 prompts of 1900 to 2048 tokens, 8 kv heads, into 16-bit rows; bytes at a
-// plain copy's 6783 GB/s): INT8 and FP8 16.5 us (bytes 14.3), 4-bit 17 (13.1), 2-bit 16
-// (11.9); histories of 336 MB of rows 96 (74.3; a fill of those rows alone 84: writes go
-// slower than copies).
+// plain copy's 6783 GB/s): INT8 and FP8 16.5 us (bytes 14.3), 4-bit 17.7 (13.1), 2-bit 16
+// (11.9); histories of 336 MB of rows 96.8 (74.3; a fill of those rows alone 84: writes go
+// slower than copies), of 671 MB of fp32 rows 181 (124). 300000 tokens x heads with 1, 2, 5 and
+// 8 kv heads: 4-bit 58, 57, 57, 47 (31), 2-bit 56, 54, 54, 43 (28), INT8 46, 46, 57, 48 (34):
+// with one or two heads the 4- and 2-bit key warps of every other page have nothing to do (a
+// group goes with its first page), with five some of the second row of CTAs.
 //
 // Page slots: sequence i starts at slot cu_rows[i] / 16 + 2 i; a range of x rows
 // touches at most x / 16 + 2 pages, so sequences do not overlap, and a slot finds

@@ -35,12 +35,15 @@
 //
 // Measured (GB300, a captured graph's time a call; bytes: the visible records, rings,
 // queries and outputs at the rate of a plain copy, 6783 GB/s): INT8 pages, one sequence
-// of 256 tokens, one kv head 6.3 us (latency); 8 kv heads of 4 queries, 32 sequences of
-// 1024 to 8192 tokens 55 (bytes 44.8); 16 of 777 to 8191 with four query positions 39
+// of 256 tokens, one kv head 6.4 us (latency); 8 kv heads of 4 queries, 32 sequences of
+// 1024 to 8192 tokens 54.5 (bytes 44.8); 16 of 777 to 8191 with four query positions 39.5
 // (21.9: 16 columns leave three warps a scheduler, and each waits on its own chain of
 // score, exponential and value MMAs); 32 of 32768, 4 kv heads of 7 queries, 167 (158.7).
-// 4-bit pages, 64 sequences behind a window of 4096, 8 kv heads: 82 (61.3: arithmetic,
-// and the two cut blocks of each segment).
+// 64 sequences behind a window of 4096, 8 kv heads: 4-bit pages 82.5 (61.3), 2-bit 81
+// (41.8), FP8 92.5 (79.4), INT8 89.5 (79.7). On 4- and 2-bit pages that is the arithmetic of
+// the codes, and the cut blocks of each segment, which go one by one and wait for their own
+// loads: the sinks', the window's first, and those that the residual reaches (five of them
+// at R = 128), about an eighth of the work line. Outputs in 32 bits take the same times.
 //
 // A masked token's key and value never meet arithmetic that could carry an
 // infinity or a NaN of theirs into the result: scores are selected, probabilities
