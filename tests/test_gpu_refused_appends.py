@@ -173,3 +173,105 @@ def test_chunks_behind_stored_tokens(bits, H):
     for other in pools[1:]:
         for (k0, v0), (k1, v1) in zip(pools[0], other):
             assert torch.equal(k0, k1) and torch.equal(v0, v1)
+
+
+@pytest.mark.parametrize("bits", FORMATS)
+@pytest.mark.parametrize("rope", [False, True])
+@pytest.mark.parametrize("seed", range(6))
+def test_ragged_calls_with_some_sequences_refused(bits, rope, seed):
+    """Random lengths, chunks, slots and refusals (lengths already reached, others, slots and tables out of range
+    beside them): the pool is that of the same calls with the accepted sequences alone."""
+    rng = torch.Generator().manual_seed(100 + seed)
+    pick = lambda lo, hi: int(torch.randint(lo, hi + 1, (1,), generator=rng))  # noqa: E731
+    H, n = (1, 2, 3, 4, 8, 5)[seed], pick(3, 40)
+    most = 900
+    pages = -(-most // 16)
+    bt = torch.randperm(n * pages, generator=rng).int().cuda().view(n, pages)
+    slots = torch.randperm(n, generator=rng).tolist()
+    table = _rope(most)
+    a, b = (_cache(bits, H, n * pages, n) for _ in range(2))
+
+    def append(c, which, before, new, k, v, ids):
+        cu = [0]
+        for x in new:
+            cu.append(cu[-1] + x)
+        args = (0, k, v, _i32(*cu), _i32(*before), bt[which].contiguous())
+        if rope:
+            c.append_rope(*args, table, slot_ids=_i32(*ids))
+        else:
+            c.append(*args, slot_ids=_i32(*ids))
+    at = [0] * n
+    for call in range(5):
+        new = [pick(0, (3, 40, 200)[pick(0, 2)]) for _ in range(n)]
+        new = [min(x, most - t - 201) for x, t in zip(new, at)]
+        before, ids, good = list(at), list(slots), []
+        for i in range(n):
+            how = pick(0, 5) if at[i] > 0 and call else 0
+            if how == 1 and new[i] > 0 and at[i] > new[i]:
+                before[i] = at[i] - new[i]            # the slot stands at the length that the call would leave
+            elif how == 2:
+                before[i] = at[i] + 1 + pick(0, 9)
+            elif how == 3:
+                ids[i] = n + pick(0, 3)
+            else:
+                good.append(i)
+        rows = [_rows(1000 * seed + 100 * call + i, new[i], H) for i in range(n)]
+        append(a, list(range(n)), before, new, torch.cat([r[0] for r in rows]), torch.cat([r[1] for r in rows]), ids)
+        rc, detail = a.status()
+        assert (rc == 0) == (len(good) == n)
+        append(b, good, [before[i] for i in good], [new[i] for i in good], torch.cat([rows[i][0] for i in good]),
+               torch.cat([rows[i][1] for i in good]), [slots[i] for i in good])
+        assert b.status() == (0, 0)
+        for i in good:
+            at[i] += new[i]
+        assert torch.equal(_held(a), _held(b)), call
+    for i in range(n):
+        lens = a.pool[a.layout.lens_offset:].view(torch.int32)[slots[i] * H:slots[i] * H + H].tolist()
+        assert lens == [at[i]] * H
+
+
+@pytest.mark.parametrize("bits", FORMATS)
+def test_chunks_of_other_slots_and_layers_at_once(bits):
+    """Chunks behind stored tokens on three streams, two slots of one layer and one of another, and a captured
+    chunk replayed: each leaves what it leaves alone."""
+    H, T0, new = 4, 40, 300
+    pages = -(-(T0 + 2 * new) // 16)
+    bt = torch.arange(2 * pages, dtype=torch.int32, device="cuda").view(2, pages)
+    rows = [[_rows(10 * w + x, T0 if x == 0 else new, H) for x in range(3)] for w in range(3)]
+    where = [(0, 0), (0, 1), (1, 0)]           # (layer, slot)
+    streams = [torch.cuda.Stream() for _ in where]
+    held = []
+    for together in (False, True):
+        c = s4.KVCache(2, 2 * pages, H, 32, 2, "bf16", bits=bits)
+        c.pool[c.layout.layer_offset:].zero_()
+        one = [(_i32(0, T0), _i32(0), _i32(0, new), _i32(T0), _i32(T0 + new), bt[s:s + 1].contiguous(), _i32(s)) for _, s in where]
+        for (layer, _), r, o in zip(where, rows, one):
+            c.append(layer, *r[0], o[0], o[1], o[5], slot_ids=o[6])
+        torch.cuda.synchronize()
+        for x, before in ((1, 3), (2, 4)):
+            for (layer, _), r, o, st in zip(where, rows, one, streams):
+                c.append(layer, *r[x], o[2], o[before], o[5], slot_ids=o[6], stream=st if together else None)
+        torch.cuda.synchronize()
+        assert c.status() == (0, 0)
+        held.append(_held(c))
+    assert torch.equal(*held)
+    lens = c.pool[c.layout.lens_offset:c.layout.lens_offset + 16 * H].view(torch.int32).tolist()
+    assert lens == [T0 + 2 * new] * 3 * H + [0] * H
+    # the same chunk captured, its length advanced on the device
+    c = s4.KVCache(1, pages, H, 32, 1, "bf16", bits=bits)
+    d = s4.KVCache(1, pages, H, 32, 1, "bf16", bits=bits)
+    for x in (c, d):
+        x.pool[x.layout.layer_offset:].zero_()
+        x.append(0, *rows[0][0], _i32(0, T0), _i32(0), bt[:1])
+    k, v, cu, before, row = *(x.clone() for x in rows[0][1]), _i32(0, new), _i32(T0), bt[:1].contiguous()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        c.append(0, k, v, cu, before, row)
+        before.add_(new)
+    for x in (1, 2):
+        k.copy_(rows[0][x][0])
+        v.copy_(rows[0][x][1])
+        gr.replay()
+        d.append(0, *rows[0][x], _i32(0, new), _i32(T0 + (x - 1) * new), bt[:1])
+    assert c.status() == (0, 0) and d.status() == (0, 0)
+    assert torch.equal(_held(c), _held(d))
