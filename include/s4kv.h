@@ -390,6 +390,53 @@ int s4kv_window_attention(s4kv_cache* cache, int layer, const void* q, int num_q
                           const int32_t* seq_lens, const int32_t* slot_ids, int B, float sm_scale, void* out,
                           int out_dtype, void* workspace, size_t ws_bytes, int max_seq_len, void* stream);
 
+/* A score form: what becomes of the product x = sm_scale q . k_t of the query at
+ * position p (head j) and token t before the softmax, and which tokens a query sees.
+ *     z_t = f(x) - slopes[j] |p - t|,  f(x) = cap tanh(x / cap), or x where cap is 0
+ *     t is visible when t <= hi and (t >= lo or t < num_sinks)
+ *     lo = max(0, p - window + 1, first[query])   (without the parts left out)
+ *     hi = min(max(p, prefix[sequence] - 1), T - 1)
+ * A query that sees nothing gets zeros. first and prefix may hold any values. */
+typedef struct {
+  float cap;               /* 0: no cap; finite, > 0 otherwise */
+  const float* slopes;     /* device, fp32 [num_q_heads] (finite), or NULL */
+  int window;              /* newest tokens visible, the query's own included; 0: no window */
+  int num_sinks;           /* first tokens visible whatever window and first say */
+  const int32_t* first;    /* device, by query token: the first token of its document, or NULL */
+  const int32_t* prefix;   /* device, by sequence: its first tokens see one another whole, or NULL */
+} s4kv_scores;
+
+/* Attention of prompts and prompt chunks: the newest tokens of n sequences, as many
+ * of each as its chunk has (none to all of them), over every cached token of theirs,
+ * causal and with a score form. They have been appended before.
+ *   scores       or NULL: plain causal attention.
+ *   q, out       [num_q][num_q_heads][128], ragged by sequence: sequence i owns rows
+ *                [cu_q[i], cu_q[i+1]), its newest tokens in order; cu_q int32 [n+1],
+ *                non-decreasing, cu_q[0] = 0, cu_q[n] = num_q. out in out_dtype
+ *                (S4KV_F32 or the cache dtype). scores->first has num_q entries.
+ *   seq_lens[i]  T_i, equal to the slot's stored length and at least the chunk (else
+ *                S4KV_DEV_BAD_LENGTH and zero rows). A sequence without a chunk is not
+ *                looked at: its length, slot and table row may hold anything.
+ *   max_seq_len, sum_seq_lens   at least every seq_lens[i], and their sum, of the
+ *                sequences that have a chunk (those beyond are S4KV_DEV_BAD_LENGTH).
+ *   workspace    s4kv_prompt_workspace_bytes of the same sizes, 16-byte aligned, any
+ *                contents, used only during the call (stream-ordered): the cached tokens
+ *                restored (512 bytes a token and kv head), and partial outputs.
+ * Every page format; num_q_heads / H_kv 1..8, n up to 4096, num_q * group up to 2^30.
+ * Two kernel launches, or three: the cached tokens that a chunk can see are restored
+ * to f16 once, matrix operands from then on; chunks of few rows split the cache's length and
+ * combine. Restored keys and values beyond 65504 in magnitude count as infinities there.
+ * A query that sees a token whose value row is not finite (or so large) gets NaN; tokens
+ * that it does not see never reach its row, whatever they hold. Short chunks of equal length
+ * (1 to 16 tokens) are read faster by s4kv_score_attention. */
+int s4kv_prompt_workspace_bytes(const s4kv_cache* cache, int n, int num_q, int num_q_heads, int max_seq_len,
+                                long long sum_seq_lens, size_t* bytes);
+int s4kv_prompt_attention(s4kv_cache* cache, int layer, const s4kv_scores* scores, const void* q, int num_q,
+                          const int32_t* cu_q, int num_q_heads, const int32_t* block_table, int bt_stride,
+                          const int32_t* seq_lens, const int32_t* slot_ids, int n, float sm_scale, void* out,
+                          int out_dtype, void* workspace, size_t ws_bytes, int max_seq_len,
+                          long long sum_seq_lens, void* stream);
+
 /* Restores token ranges of n sequences into dense rows: what attention sees of
  * them, for a dense kernel over a cached prefix or for moving a cache elsewhere.
  *   cu_rows      int32 [n+1], non-decreasing, cu_rows[0] = 0, cu_rows[n] = num_rows:

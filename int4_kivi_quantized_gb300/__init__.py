@@ -65,6 +65,11 @@ class s4kv_rope(ctypes.Structure):
                 ("interleaved", ctypes.c_int)]
 
 
+class s4kv_scores(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("window", ctypes.c_int),
+                ("num_sinks", ctypes.c_int), ("first", ctypes.c_void_p), ("prefix", ctypes.c_void_p)]
+
+
 class s4kv_kv_bytes_report(ctypes.Structure):
     _fields_ = [(n, ctypes.c_double) for n in (
         "fp16_equiv_bytes", "code_bytes", "meta_bytes", "residual_bytes", "paged_bytes")]
@@ -91,6 +96,9 @@ def _load():
         "s4kv_append_rope": [P, I, ctypes.POINTER(s4kv_rope), P, P, I, P, P, P, P, I, I, P, I, P, P],
         "s4kv_window_workspace_bytes": [P, I, I, I, I, ctypes.POINTER(SZ)],
         "s4kv_window_attention": [P, I, P, I, I, I, I, P, I, P, P, I, ctypes.c_float, P, I, P, SZ, I, P],
+        "s4kv_prompt_workspace_bytes": [P, I, I, I, I, ctypes.c_longlong, ctypes.POINTER(SZ)],
+        "s4kv_prompt_attention": [P, I, ctypes.POINTER(s4kv_scores), P, I, P, I, P, I, P, P, I, ctypes.c_float, P, I, P,
+                                  SZ, I, ctypes.c_longlong, P],
         "s4kv_gather": [P, I, P, I, P, P, P, P, I, I, P, P, I, P],
         "s4kv_dequant_debug": [P, I, I, P, I, P, P, P],
         "s4kv_get_status": [P, P, ctypes.POINTER(I)],
@@ -263,6 +271,23 @@ def s4kv_window_attention(h, layer, q, num_q_tokens, num_q_heads, window, num_si
            "s4kv_window_attention")
 
 
+def s4kv_prompt_workspace_bytes(h, n, num_q, num_q_heads, max_seq_len, sum_seq_lens) -> int:
+    out = ctypes.c_size_t()
+    _check(_lib.s4kv_prompt_workspace_bytes(h, int(n), int(num_q), int(num_q_heads), int(max_seq_len), int(sum_seq_lens),
+                                            ctypes.byref(out)), "s4kv_prompt_workspace_bytes")
+    return out.value
+
+
+def s4kv_prompt_attention(h, layer, scores, q, num_q, cu_q, num_q_heads, block_table, bt_stride, seq_lens, slot_ids, n,
+                          sm_scale, out, out_dtype, workspace, ws_bytes, max_seq_len, sum_seq_lens, stream=None):
+    """Causal attention of ragged prompt chunks with a score form (an s4kv_scores, or None)."""
+    _check(_lib.s4kv_prompt_attention(h, int(layer), None if scores is None else ctypes.byref(scores), _ptr(q), int(num_q),
+                                      _ptr(cu_q), int(num_q_heads), _ptr(block_table), int(bt_stride), _ptr(seq_lens),
+                                      _ptr(slot_ids), int(n), float(sm_scale), _ptr(out), int(out_dtype), _ptr(workspace),
+                                      int(ws_bytes), int(max_seq_len), int(sum_seq_lens), _stream(stream)),
+           "s4kv_prompt_attention")
+
+
 def s4kv_gather(h, layer, block_table, bt_stride, seq_lens, slot_ids, first_token, cu_rows, num_rows, n, out_k, out_v,
                 out_dtype, stream=None):
     """Restores token ranges of n sequences into dense rows."""
@@ -317,6 +342,25 @@ class Rope:
         self.ref = ctypes.byref(self.c)
 
 
+class Scores:
+    """A model's score form for attend and prompt: scores capped at cap tanh(x / cap) (0: as they
+    are), less slopes[head] |p - t| (fp32 [H_q] on the cache's device, kept alive by this object),
+    within the newest `window` tokens (0: all) and the first `num_sinks`."""
+
+    def __init__(self, cap=0.0, slopes=None, window=0, num_sinks=0):
+        import torch
+        if slopes is not None and (slopes.dim() != 1 or slopes.dtype != torch.float32 or not slopes.is_contiguous()):
+            raise ValueError("the slopes are a contiguous fp32 tensor [H_q]")
+        if not 0.0 <= cap < float("inf") or window < 0 or num_sinks < 0:
+            raise ValueError("cap, window and num_sinks are finite and not negative")
+        self.cap, self.slopes = float(cap), slopes
+        wide = 0x7fffffff
+        self.window, self.num_sinks = min(int(window), wide), min(int(num_sinks), wide)
+
+    def c(self, first, prefix):
+        return s4kv_scores(self.cap, _address(self.slopes), self.window, self.num_sinks, _address(first), _address(prefix))
+
+
 def _on_its_device(f):
     """A method that runs with the cache's device as the current one."""
     @functools.wraps(f)
@@ -331,6 +375,9 @@ def _on_its_device(f):
 
 def _address(t):
     return None if t is None else t.data_ptr()
+
+
+_PLAIN = Scores()
 
 
 class KVCache:
@@ -561,6 +608,49 @@ class KVCache:
                                           width, seq_lens.data_ptr(), _address(slot_ids), B, float(sm_scale), out.data_ptr(),
                                           out_dtype, ws.data_ptr(), nbytes, max_seq_len, self._handle(stream)),
                "s4kv_window_attention")
+        return out
+
+    def _form(self, scores, first, prefix, queries, n, Hq):
+        """The s4kv_scores of a call: `first` has the shape `queries`, `prefix` one entry a sequence."""
+        import torch
+        if scores is None:
+            scores = _PLAIN
+        if scores.slopes is not None:
+            self._tensor(scores.slopes, "slopes", torch.float32, (Hq,))
+        if first is not None:
+            self._tensor(first, "first", torch.int32, queries)
+        if prefix is not None:
+            self._tensor(prefix, "prefix", torch.int32, (n,))
+        return scores.c(first, prefix)
+
+    @_on_its_device
+    def prompt(self, layer, q, cu_q, block_table, seq_lens, max_seq_len, sum_seq_lens=None, scores=None, first=None,
+               prefix=None, out=None, out_dtype=S4KV_F32, slot_ids=None, sm_scale=0.0, stream=None):
+        """Causal attention of prompt chunks, q [tokens, H_q, 128] -> out of the same shape: rows
+        cu_q[i] .. cu_q[i + 1] are sequence i's newest tokens, appended before. scores: a Scores;
+        first [tokens]: the first token that each query's document has; prefix [n]: how many first
+        tokens see one another whole. max_seq_len and sum_seq_lens bound the sequences' lengths and
+        their sum (n max_seq_len without it): scratch of 512 bytes a token and kv head is taken."""
+        import torch
+        i32, n = torch.int32, seq_lens.shape[0]
+        tokens, Hq, _ = self._tensor(q, "q", self.torch_dtype, (None, None, 128))
+        self._tensor(cu_q, "cu_q", i32, (n + 1,))
+        self._tensor(seq_lens, "seq_lens", i32, (n,))
+        rows, width = self._tensor(block_table, "block_table", i32, (None, None))
+        if rows < n:
+            raise ValueError("block_table has fewer rows than there are sequences")
+        if slot_ids is not None:
+            self._tensor(slot_ids, "slot_ids", i32, (n,))
+        form = self._form(scores, first, prefix, (tokens,), n, Hq)
+        out = self._out(out, "out", (tokens, Hq, 128), out_dtype, stream, q)
+        max_seq_len = int(max_seq_len)
+        total = n * max_seq_len if sum_seq_lens is None else int(sum_seq_lens)
+        nbytes = s4kv_prompt_workspace_bytes(self.h, n, tokens, Hq, max_seq_len, total)
+        ws = self._scratch(max(16, nbytes), stream)
+        _check(_lib.s4kv_prompt_attention(self.h, int(layer), ctypes.byref(form), q.data_ptr(), tokens, cu_q.data_ptr(), Hq,
+                                          block_table.data_ptr(), width, seq_lens.data_ptr(), _address(slot_ids), n,
+                                          float(sm_scale), out.data_ptr(), out_dtype, ws.data_ptr(), nbytes, max_seq_len,
+                                          total, self._handle(stream)), "s4kv_prompt_attention")
         return out
 
     @_on_its_device

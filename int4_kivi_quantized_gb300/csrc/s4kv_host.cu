@@ -1,7 +1,7 @@
 // Host side of the s4kv C ABI: argument checks, pool layout, launches and the
 // status word. Declarations and the byte format are in include/s4kv.h.
 
-#include "s4kv_common.cuh"
+#include "s4kv_prompt.cuh"
 
 #include <cmath>
 #include <cstring>
@@ -505,7 +505,6 @@ int window_call(s4kv_cache* cache, DecodeArgs d, int nq, int window, int sinks, 
   const cudaError_t e = launch_window(a, cache->num_sms, st);
   return e == cudaSuccess ? S4KV_OK : S4KV_ERR_CUDA;
 }
-constexpr int kNoWindow = 1 << 30;   // wider than any sequence
 
 // Columns a multi-query warp holds (both page formats).
 int mq_cols_per_warp(const s4kv_cache*) { return 2 * kMaxGroup; }
@@ -711,6 +710,148 @@ int s4kv_window_attention(s4kv_cache* cache, int layer, const void* q, int num_q
                                       sm_scale, out, out_dtype, workspace, max_seq_len);
   return window_call(cache, a, num_q_tokens, window < kNoWindow ? window : kNoWindow,
                      num_sinks < kNoWindow ? num_sinks : kNoWindow, static_cast<cudaStream_t>(stream));
+}
+
+namespace {
+// A score form's arguments (null: none), checked.
+int score_form_of(const s4kv_scores* s, ScoreForm* f) {
+  *f = ScoreForm{nullptr, nullptr, nullptr, 0.0f, kNoWindow, 0};
+  if (!s) return S4KV_OK;
+  if (!(s->cap >= 0.0f) || std::isinf(s->cap) || s->window < 0 || s->num_sinks < 0) return S4KV_ERR_INVALID_ARG;
+  f->slopes = s->slopes;
+  f->first = s->first;
+  f->prefix = s->prefix;
+  f->cap = s->cap;
+  f->window = s->window == 0 || s->window > kNoWindow ? kNoWindow : s->window;
+  f->sinks = s->num_sinks < kNoWindow ? s->num_sinks : kNoWindow;
+  return S4KV_OK;
+}
+
+// Sizes of a prompt call: tiles at most, and the most splits that its workspace has room for.
+struct PromptSizes {
+  int q_tiles, kv_tiles, most;
+  size_t tile_bytes, bad_bytes, part_bytes;
+  size_t total() const { return tile_bytes + bad_bytes + part_bytes; }
+};
+int prompt_sizes(const s4kv_cache* c, int n, int num_q, int num_q_heads, int max_seq_len, long long sum_seq_lens, PromptSizes* z) {
+  if (!c || n < 0 || n > 4096 || num_q < 0 || num_q_heads <= 0 || max_seq_len < 0 || sum_seq_lens < 0) return S4KV_ERR_INVALID_ARG;
+  const int H = c->cfg.num_kv_heads;
+  if (num_q_heads % H) return S4KV_ERR_INVALID_ARG;
+  const int g = num_q_heads / H;
+  if (g > kMaxGroup) return S4KV_ERR_UNSUPPORTED;
+  const long long most_kv = static_cast<long long>(n) * ((max_seq_len + static_cast<long long>(kKvTile) - 1) / kKvTile);
+  const long long rows = static_cast<long long>(num_q) * g;
+  if (most_kv > 0x7fffffffLL || rows > (1LL << 30)) return S4KV_ERR_INVALID_ARG;
+  const long long by_sum = sum_seq_lens / kKvTile + n;   // each sequence may end inside a tile
+  z->kv_tiles = static_cast<int>(most_kv < by_sum ? most_kv : by_sum);
+  const long long used = n < num_q ? n : num_q;          // sequences that can have queries
+  z->q_tiles = static_cast<int>((rows + (kQRows - 1) * used) / kQRows);
+  const long long items = static_cast<long long>(z->q_tiles) * H;
+  // splits fill the GPU about twice over, at most
+  const long long most = items > 0 ? (2LL * c->num_sms + items - 1) / items : 1;
+  z->most = static_cast<int>(most < kMaxSplits ? most : kMaxSplits);
+  z->tile_bytes = static_cast<size_t>(z->kv_tiles) * H * 2 * kTileBytes;
+  z->bad_bytes = static_cast<size_t>(z->kv_tiles) * H * 16;
+  z->part_bytes = z->most > 1 ? static_cast<size_t>(items) * z->most * kQRows * (kD + 2) * sizeof(float) : 0;
+  return S4KV_OK;
+}
+
+// Splits of a call's kv tiles. A CTA walks `tiles` of them, and the GPU holds one CTA per SM: the
+// fewest passes over the GPU times a pass's tiles, where a CTA's start and end are worth three
+// tiles and a combine two, and as much again as the partial outputs it reads.
+int prompt_splits(const PromptSizes& z, int H, int num_sms, long long tiles) {
+  const long long items = static_cast<long long>(z.q_tiles) * H;
+  int best = 1;
+  double least = 1e300;
+  for (int s = 1; s <= z.most && s <= tiles; ++s) {
+    const double waves = static_cast<double>((items * s + num_sms - 1) / num_sms);
+    const double cost = waves * (static_cast<double>((tiles + s - 1) / s) + 3.0) + (s > 1 ? 2.0 + 0.04 * static_cast<double>(items * s) : 0.0);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+}  // namespace
+
+int s4kv_prompt_workspace_bytes(const s4kv_cache* cache, int n, int num_q, int num_q_heads, int max_seq_len,
+                                long long sum_seq_lens, size_t* bytes) {
+  if (!bytes) return S4KV_ERR_INVALID_ARG;
+  PromptSizes z;
+  const int rc = prompt_sizes(cache, n, num_q, num_q_heads, max_seq_len, sum_seq_lens, &z);
+  if (rc != S4KV_OK) return rc;
+  *bytes = z.total();
+  return S4KV_OK;
+}
+
+int s4kv_prompt_attention(s4kv_cache* cache, int layer, const s4kv_scores* scores, const void* q, int num_q,
+                          const int32_t* cu_q, int num_q_heads, const int32_t* block_table, int bt_stride,
+                          const int32_t* seq_lens, const int32_t* slot_ids, int n, float sm_scale, void* out,
+                          int out_dtype, void* workspace, size_t ws_bytes, int max_seq_len, long long sum_seq_lens,
+                          void* stream) {
+  if (!cache || layer < 0 || layer >= cache->cfg.num_layers) return S4KV_ERR_INVALID_ARG;
+  PromptSizes z;
+  int rc = prompt_sizes(cache, n, num_q, num_q_heads, max_seq_len, sum_seq_lens, &z);
+  if (rc != S4KV_OK) return rc;
+  PromptArgs a{};
+  rc = score_form_of(scores, &a.form);
+  if (rc != S4KV_OK) return rc;
+  const s4kv_config& c = cache->cfg;
+  if (out_dtype != S4KV_F32 && out_dtype != c.dtype) return S4KV_ERR_INVALID_ARG;
+  if (!on_cache_device(cache)) return S4KV_ERR_INVALID_ARG;
+  if (n == 0) return num_q == 0 ? S4KV_OK : S4KV_ERR_INVALID_ARG;
+  if (!cu_q || !block_table || !seq_lens || bt_stride <= 0) return S4KV_ERR_INVALID_ARG;
+  if (num_q == 0) return S4KV_OK;
+  if (!q || !out || !aligned16(q) || !aligned16(out)) return S4KV_ERR_INVALID_ARG;
+  if (ws_bytes < z.total()) return S4KV_ERR_WORKSPACE_TOO_SMALL;
+  if (!workspace || !aligned16(workspace)) return S4KV_ERR_INVALID_ARG;
+  const char* base = cache->pool + cache->lay.layer_offset + static_cast<size_t>(layer) * cache->lay.layer_stride;
+  a.pages = base;
+  a.kring = base + cache->lay.kring_offset;
+  a.vring = base + cache->lay.vring_offset;
+  a.lens = reinterpret_cast<const int*>(cache->pool + cache->lay.lens_offset) +
+           static_cast<size_t>(layer) * c.max_slots * c.num_kv_heads;
+  a.status = reinterpret_cast<int*>(cache->pool + cache->lay.status_offset);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.slot_ids = slot_ids;
+  a.cu_q = cu_q;
+  a.q = static_cast<const uint16_t*>(q);
+  a.out = out;
+  a.fp8_scale = fp8_scales_of(cache, layer);
+  a.tiles = static_cast<char*>(workspace);
+  a.bad = reinterpret_cast<uint32_t*>(a.tiles + z.tile_bytes);
+  a.part = reinterpret_cast<float*>(a.tiles + z.tile_bytes + z.bad_bytes);
+  a.kring_slot = cache->lay.kring_slot_stride / 2;
+  a.kring_head = cache->lay.kring_head_stride / 2;
+  a.vring_slot = cache->lay.vring_slot_stride / 2;
+  a.vring_head = cache->lay.vring_head_stride / 2;
+  a.wait_ns = cache->wait_ns;
+  a.sm_scale = sm_scale > 0.0f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(kD));
+  a.bt_stride = bt_stride;
+  a.n = n;
+  a.num_q = num_q;
+  a.Hq = num_q_heads;
+  a.H = c.num_kv_heads;
+  a.g = num_q_heads / c.num_kv_heads;
+  a.R = c.residual_v;
+  a.num_pages = c.num_pages;
+  a.max_slots = c.max_slots;
+  a.dtype = c.dtype;
+  a.out_dtype = out_dtype;
+  a.bits = cache->bits;
+  a.max_seq_len = max_seq_len;
+  a.kv_tiles = z.kv_tiles;
+  a.q_tiles = z.q_tiles;
+  // kv tiles of a CTA, at most: of the longest sequence, or of a window and the rows' positions
+  long long seen = max_seq_len;
+  const long long span = static_cast<long long>(a.form.window) + (num_q < kQRows / a.g + 1 ? num_q : kQRows / a.g + 1) + a.form.sinks;
+  if (!a.form.prefix && span < seen) seen = span;
+  a.splits = prompt_splits(z, a.H, cache->num_sms, (seen + kKvTile - 1) / kKvTile);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (z.kv_tiles > 0 && launch_tiles(a, st) != cudaSuccess) return S4KV_ERR_CUDA;
+  return launch_prompt(a, st) == cudaSuccess ? S4KV_OK : S4KV_ERR_CUDA;
 }
 
 int s4kv_gather(s4kv_cache* cache, int layer, const int32_t* block_table, int bt_stride,

@@ -1,0 +1,141 @@
+// The first launch of prompt attention: every cached token that a chunk may see, restored from
+// its page or ring into tiles of matrix operands.
+//
+// A tile is 128 tokens of one kv head, keys then values, f16, each as two halves of 64 channels
+// of 128 rows (tokens) of 128 bytes whose 16-byte chunks c sit at c xor (row mod 8): the image
+// that tcgen05 reads, as a K-major operand (keys) and as an MN-major one (values), so the attention
+// kernel fetches a tensor's tile with one bulk copy. f16 keeps 11 bits of a restored value
+// where the caches' bf16 would keep 8: a key's rounding then moves a score by 2^-11 of its
+// terms at most. Values beyond f16's range become infinities; a value row with an element
+// that is not finite (then) is stored as zeros where it is not and gets a bit, so that queries which
+// do not see it never meet it.
+//
+// One CTA a tile: warps 0 .. 3 a key group of 32 tokens each, warps 4 .. 7 the values of
+// 32 tokens. Bound by the bytes it writes, most of which stay in the L2 cache for the
+// attention kernel.
+
+#include "s4kv_prompt.cuh"
+#include "s4kv_restore.cuh"
+
+namespace s4kv {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+
+// Eight channels of row r0 + token of a tile's tensor. bits: of the tokens whose rows are not
+// finite (values), or null (keys).
+struct TileRows {
+  char* tile;
+  int r0;
+  uint32_t* bits;
+  __device__ __forceinline__ void operator()(int token, int c, const float (&y)[8]) const {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __half2 x = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+      w[i] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    const int r = r0 + token;
+    if (bits) {
+      bool wild = false;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) wild = wild || (w[i] & 0x7c00u) == 0x7c00u || (w[i] & 0x7c000000u) == 0x7c000000u;
+      if (wild) {
+        *bits |= 1u << (r & 31);
+        w[0] = w[1] = w[2] = w[3] = 0u;
+      }
+    }
+    store(c, r, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+  __device__ __forceinline__ void store(int c, int r, uint4 w) const {
+    *reinterpret_cast<uint4*>(tile + (c >> 3) * (kTileBytes / 2) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = w;
+  }
+  // zeros in rows r0 + lo .. r0 + hi - 1
+  __device__ __forceinline__ void clear(int lo, int hi) const {
+    const int lane = threadIdx.x & 31;
+    for (int t = lo + (lane >> 4); t < hi; t += 2) store(lane & 15, r0 + t, make_uint4(0u, 0u, 0u, 0u));
+  }
+};
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads, 3) tiles_kernel(PromptArgs a) {
+  stream_wait();
+  Place p;
+  const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int where = find_tile<kThreads, false>(a, blockIdx.x, p);
+  if (where == kMalformed && blockIdx.x == 0 && h == 0 && threadIdx.x == 0)
+    report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_CU, a.n);
+  if (where != kFound) return;
+  const int m = a.cu_q[p.b + 1] - a.cu_q[p.b], T = a.seq_lens[p.b], slot = a.slot_ids ? a.slot_ids[p.b] : p.b;
+  int arg;
+  if (refused(a, p, m, T, slot, h, arg)) return;   // (the attention kernel says so)
+  const int t_tile = p.tile * kKvTile;
+  // a tile that lies between the sinks and every query's window is not looked at
+  if (t_tile + kKvTile <= T - m - a.form.window + 1 && t_tile >= a.form.sinks) return;
+  const bool values = warp >= 4;
+  const int w = warp & 3, t0 = t_tile + 32 * w;   // this warp's 32 tokens
+  const long long at = (static_cast<long long>(p.kv0) + p.tile) * a.H + h;
+  uint32_t bits = 0;
+  const TileRows rows{a.tiles + (2 * at + values) * kTileBytes, 32 * w, values ? &bits : nullptr};
+  const int* bt = a.block_table + static_cast<long long>(p.b) * a.bt_stride;
+  const int Tk = FMT == 8 ? T : FMT == kI8 ? T / kP * kP : T & ~(kG - 1);
+  const int Tv = FMT == 8 ? T : FMT == kI8 ? Tk : max(0, T - a.R);
+  const int quant = values ? Tv : Tk, mod = FMT == kI8 ? kP : values ? a.R : kG;
+  const uint16_t* ring = values ? reinterpret_cast<const uint16_t*>(a.vring) + slot * a.vring_slot + h * a.vring_head
+                                : reinterpret_cast<const uint16_t*>(a.kring) + slot * a.kring_slot + h * a.kring_head;
+  auto record = [&](int logical) -> const char* {   // null (reported) outside the pool
+    const int pp = bt[logical];
+    if (pp >= 0 && pp < a.num_pages) return a.pages + (static_cast<long long>(pp) * a.H + h) * Rec<FMT>::kBytes;
+    if (lane == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, pp);
+    return nullptr;
+  };
+  if (!kByte<FMT> && !values && t0 + kG <= Tk) {
+    if constexpr (!kByte<FMT>) {   // a whole key group: both pages' records hold its metadata
+      const char* r0 = record(t0 / kP);
+      const char* r1 = record(t0 / kP + 1);
+      if (r0 && r1) put_key_group<FMT>(r0, r1, 0, kG, rows);
+      else rows.clear(0, kG);
+    }
+  } else {
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      const int tp = t0 + half * kP, end = min(max(T - tp, 0), kP);          // tokens [0, end) of this page are there
+      const int held = min(max(quant - tp, 0), end);                       // [0, held) in its record
+      const TileRows here{rows.tile, rows.r0 + half * kP, rows.bits};
+      if (held > 0) {
+        const char* rec = record(tp / kP);
+        if (!rec) here.clear(0, held);
+        else if (values) put_values<FMT>(a.fp8_scale + a.H + h, rec, 0, held, here);
+        else if constexpr (kByte<FMT>) put_keys<FMT>(a.fp8_scale + h, rec, 0, held, here);
+      }
+      if (FMT != 8 && end > held) put_ring(ring, mod, tp, held, end, a.dtype, here);
+      here.clear(end, kP);   // behind the last token: zeros, which a probability of zero leaves alone
+    }
+  }
+  if (values) {
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if (lane == 0) a.bad[4 * at + w] = bits;
+  }
+}
+
+template <int FMT>
+cudaError_t run(const PromptArgs& a, cudaStream_t st) {
+  void (*f)(PromptArgs) = tiles_kernel<FMT>;
+  const cudaError_t c = prefer_max_shared(reinterpret_cast<const void*>(f));
+  if (c != cudaSuccess) return c;
+  return launch_behind(f, dim3(static_cast<unsigned>(a.kv_tiles), static_cast<unsigned>(a.H)), dim3(kThreads), 0, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_tiles(const PromptArgs& a, cudaStream_t st) {
+  switch (a.bits) {
+    case S4KV_BITS_INT8: return run<S4KV_BITS_INT8>(a, st);
+    case 8: return run<8>(a, st);
+    case 2: return run<2>(a, st);
+    default: return run<4>(a, st);
+  }
+}
+
+}  // namespace s4kv

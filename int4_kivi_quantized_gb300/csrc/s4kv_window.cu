@@ -52,6 +52,7 @@
 // a row is not finite, the block is done query by query.
 
 #include "s4kv_kernels.cuh"
+#include "s4kv_score.cuh"
 
 #include <mutex>
 
@@ -241,16 +242,6 @@ __device__ __forceinline__ void add_only(float (&o)[4], const int (&opos)[2], in
 #pragma unroll
   for (int e = 0; e < 4; ++e) o[e] = opos[e & 1] == only ? o[e] + t[e] : o[e];
 }
-
-// bf16 queries enter the MMAs as f16. Their range is the wider one, so each column is
-// taken at the power of two 2^k that brings its largest element to 2^14 .. 2^15: exact,
-// and elements down to 2^-28 of the largest keep every bit. k of a column whose largest
-// magnitude has the bits `top` (0 for zeros, infinities and NaN, which stay what they are).
-__device__ __forceinline__ int query_power(uint32_t top) {
-  const int e = static_cast<int>(top >> 7);
-  return top == 0 || e == 255 ? 0 : min(14 + 127 - e, 120);
-}
-__device__ __forceinline__ float power_of_two(int k) { return __int_as_float((k + 127) << 23); }   // -126 <= k <= 127
 
 // What INT8 accumulators lack of the true output, until the records are done.
 constexpr float kI8Rest = 262144.0f;
