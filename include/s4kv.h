@@ -398,13 +398,24 @@ int s4kv_window_attention(s4kv_cache* cache, int layer, const void* q, int num_q
  *     hi = min(max(p, prefix[sequence] - 1), T - 1)
  * A query that sees nothing gets zeros. first and prefix may hold any values. */
 typedef struct {
-  float cap;               /* 0: no cap; finite, > 0 otherwise */
+  float cap;               /* 0: no cap; 2^-60 .. 2^60 otherwise */
   const float* slopes;     /* device, fp32 [num_q_heads] (finite), or NULL */
   int window;              /* newest tokens visible, the query's own included; 0: no window */
   int num_sinks;           /* first tokens visible whatever window and first say */
   const int32_t* first;    /* device, by query token: the first token of its document, or NULL */
   const int32_t* prefix;   /* device, by sequence: its first tokens see one another whole, or NULL */
 } s4kv_scores;
+
+/* Causal attention of the last num_q_tokens tokens of each sequence with a score form:
+ * one token of a decode step, or up to 16 draft or chunk tokens. scores->first has
+ * B num_q_tokens entries, scores->prefix B; scores may not be NULL. Arguments, limits,
+ * workspace (s4kv_window_workspace_bytes), errors, launches and S4KV_OPT_WINDOW_FORM are
+ * those of s4kv_window_attention, and so is what it reads: only blocks that a query
+ * of the call may see (with num_sinks and every query's range taken together). */
+int s4kv_score_attention(s4kv_cache* cache, int layer, const s4kv_scores* scores, const void* q, int num_q_tokens,
+                         int num_q_heads, const int32_t* block_table, int bt_stride, const int32_t* seq_lens,
+                         const int32_t* slot_ids, int B, float sm_scale, void* out, int out_dtype, void* workspace,
+                         size_t ws_bytes, int max_seq_len, void* stream);
 
 /* Attention of prompts and prompt chunks: the newest tokens of n sequences, as many
  * of each as its chunk has (none to all of them), over every cached token of theirs,

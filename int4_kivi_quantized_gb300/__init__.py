@@ -96,6 +96,7 @@ def _load():
         "s4kv_append_rope": [P, I, ctypes.POINTER(s4kv_rope), P, P, I, P, P, P, P, I, I, P, I, P, P],
         "s4kv_window_workspace_bytes": [P, I, I, I, I, ctypes.POINTER(SZ)],
         "s4kv_window_attention": [P, I, P, I, I, I, I, P, I, P, P, I, ctypes.c_float, P, I, P, SZ, I, P],
+        "s4kv_score_attention": [P, I, ctypes.POINTER(s4kv_scores), P, I, I, P, I, P, P, I, ctypes.c_float, P, I, P, SZ, I, P],
         "s4kv_prompt_workspace_bytes": [P, I, I, I, I, ctypes.c_longlong, ctypes.POINTER(SZ)],
         "s4kv_prompt_attention": [P, I, ctypes.POINTER(s4kv_scores), P, I, P, I, P, I, P, P, I, ctypes.c_float, P, I, P,
                                   SZ, I, ctypes.c_longlong, P],
@@ -271,6 +272,15 @@ def s4kv_window_attention(h, layer, q, num_q_tokens, num_q_heads, window, num_si
            "s4kv_window_attention")
 
 
+def s4kv_score_attention(h, layer, scores: s4kv_scores, q, num_q_tokens, num_q_heads, block_table, bt_stride, seq_lens,
+                         slot_ids, B, sm_scale, out, out_dtype, workspace, ws_bytes, max_seq_len, stream=None):
+    """Causal attention of the last tokens with a score form."""
+    _check(_lib.s4kv_score_attention(h, int(layer), ctypes.byref(scores), _ptr(q), int(num_q_tokens), int(num_q_heads),
+                                     _ptr(block_table), int(bt_stride), _ptr(seq_lens), _ptr(slot_ids), int(B),
+                                     float(sm_scale), _ptr(out), int(out_dtype), _ptr(workspace), int(ws_bytes),
+                                     int(max_seq_len), _stream(stream)), "s4kv_score_attention")
+
+
 def s4kv_prompt_workspace_bytes(h, n, num_q, num_q_heads, max_seq_len, sum_seq_lens) -> int:
     out = ctypes.c_size_t()
     _check(_lib.s4kv_prompt_workspace_bytes(h, int(n), int(num_q), int(num_q_heads), int(max_seq_len), int(sum_seq_lens),
@@ -351,8 +361,10 @@ class Scores:
         import torch
         if slopes is not None and (slopes.dim() != 1 or slopes.dtype != torch.float32 or not slopes.is_contiguous()):
             raise ValueError("the slopes are a contiguous fp32 tensor [H_q]")
-        if not 0.0 <= cap < float("inf") or window < 0 or num_sinks < 0:
-            raise ValueError("cap, window and num_sinks are finite and not negative")
+        if cap != 0 and not 2.0 ** -60 <= cap <= 2.0 ** 60:
+            raise ValueError("a cap is 2^-60 .. 2^60, or 0 for none")
+        if window < 0 or num_sinks < 0:
+            raise ValueError("window and num_sinks are not negative")
         self.cap, self.slopes = float(cap), slopes
         wide = 0x7fffffff
         self.window, self.num_sinks = min(int(window), wide), min(int(num_sinks), wide)
@@ -622,6 +634,31 @@ class KVCache:
         if prefix is not None:
             self._tensor(prefix, "prefix", torch.int32, (n,))
         return scores.c(first, prefix)
+
+    @_on_its_device
+    def attend(self, layer, q, block_table, seq_lens, max_seq_len, scores, first=None, prefix=None, out=None,
+               out_dtype=S4KV_F32, slot_ids=None, sm_scale=0.0, stream=None):
+        """Causal attention of the last nq tokens (1 to 16), q [B, nq, H_q, 128] -> out of the same shape,
+        with a score form (scores: a Scores). first [B, nq]: the first token that each query's document
+        has; prefix [B]: how many first tokens see one another whole."""
+        import torch
+        B, nq, Hq, _ = self._tensor(q, "q", self.torch_dtype, (None, None, None, 128))
+        rows, width = self._tensor(block_table, "block_table", torch.int32, (None, None))
+        self._tensor(seq_lens, "seq_lens", torch.int32, (B,))
+        if rows < B:
+            raise ValueError("block_table has fewer rows than there are sequences")
+        if slot_ids is not None:
+            self._tensor(slot_ids, "slot_ids", torch.int32, (B,))
+        form = self._form(scores, first, prefix, (B, nq), B, Hq)
+        out = self._out(out, "out", (B, nq, Hq, 128), out_dtype, stream, q)
+        max_seq_len = int(max_seq_len)
+        nbytes = self._window_bytes(B, nq, Hq, max_seq_len)
+        ws = self._scratch(nbytes, stream)
+        _check(_lib.s4kv_score_attention(self.h, int(layer), ctypes.byref(form), q.data_ptr(), nq, Hq, block_table.data_ptr(),
+                                         width, seq_lens.data_ptr(), _address(slot_ids), B, float(sm_scale), out.data_ptr(),
+                                         out_dtype, ws.data_ptr(), nbytes, max_seq_len, self._handle(stream)),
+               "s4kv_score_attention")
+        return out
 
     @_on_its_device
     def prompt(self, layer, q, cu_q, block_table, seq_lens, max_seq_len, sum_seq_lens=None, scores=None, first=None,

@@ -24,6 +24,7 @@ SOURCES = {
     "s4kv_noalloc.cu": [],
     "s4kv_append8.cu": EXACT,
     "s4kv_window.cu": [],
+    "s4kv_scored.cu": [],
     "s4kv_gather.cu": EXACT,
     "s4kv_tiles.cu": EXACT,
     "s4kv_prompt.cu": [],
@@ -56,7 +57,8 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     headers = [os.path.join(CSRC, "s4kv_common.cuh"), os.path.join(CSRC, "s4kv_kernels.cuh"),
                os.path.join(CSRC, "s4kv_rope.cuh"), os.path.join(CSRC, "s4kv_quant.cuh"),
                os.path.join(CSRC, "s4kv_restore.cuh"), os.path.join(CSRC, "s4kv_tcgen05.cuh"),
-               os.path.join(CSRC, "s4kv_score.cuh"), os.path.join(CSRC, "s4kv_prompt.cuh"),
+               os.path.join(CSRC, "s4kv_score.cuh"), os.path.join(CSRC, "s4kv_window.cuh"),
+               os.path.join(CSRC, "s4kv_prompt.cuh"),
                os.path.join(ROOT, "include", "s4kv.h"),
                __file__]
     jobs = []

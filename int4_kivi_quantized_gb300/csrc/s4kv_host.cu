@@ -491,17 +491,20 @@ DecodeArgs attention_args(s4kv_cache* cache, int layer, const void* q, int num_q
 
 // The window kernel on the current arguments (checked by the callers): nq query
 // tokens, `window` newest tokens and `sinks` first ones visible.
-int window_call(s4kv_cache* cache, DecodeArgs d, int nq, int window, int sinks, cudaStream_t st) {
-  WindowArgs a;
-  static_cast<DecodeArgs&>(a) = d;
+void window_args(const s4kv_cache* cache, const DecodeArgs& d, int nq, int window, int sinks, WindowArgs* a) {
+  static_cast<DecodeArgs&>(*a) = d;
   const int cols = nq * d.g;
-  a.nq = nq;
-  a.window = window;
-  a.sinks = sinks;
-  a.form = cache->window_form;
-  a.tiles = window_tiles(cache, cols);
-  a.pcols = window_pcols(cache, cols);
-  a.grid_warps = cache->num_sms * window_warps_per_sm();
+  a->nq = nq;
+  a->window = window;
+  a->sinks = sinks;
+  a->form = cache->window_form;
+  a->tiles = window_tiles(cache, cols);
+  a->pcols = window_pcols(cache, cols);
+  a->grid_warps = cache->num_sms * window_warps_per_sm();
+}
+int window_call(s4kv_cache* cache, const DecodeArgs& d, int nq, int window, int sinks, cudaStream_t st) {
+  WindowArgs a;
+  window_args(cache, d, nq, window, sinks, &a);
   const cudaError_t e = launch_window(a, cache->num_sms, st);
   return e == cudaSuccess ? S4KV_OK : S4KV_ERR_CUDA;
 }
@@ -717,7 +720,8 @@ namespace {
 int score_form_of(const s4kv_scores* s, ScoreForm* f) {
   *f = ScoreForm{nullptr, nullptr, nullptr, 0.0f, kNoWindow, 0};
   if (!s) return S4KV_OK;
-  if (!(s->cap >= 0.0f) || std::isinf(s->cap) || s->window < 0 || s->num_sinks < 0) return S4KV_ERR_INVALID_ARG;
+  if (s->window < 0 || s->num_sinks < 0) return S4KV_ERR_INVALID_ARG;
+  if (s->cap != 0.0f && !(s->cap >= 0x1p-60f && s->cap <= 0x1p60f)) return S4KV_ERR_INVALID_ARG;   // (its inverse is at hand)
   f->slopes = s->slopes;
   f->first = s->first;
   f->prefix = s->prefix;
@@ -727,6 +731,37 @@ int score_form_of(const s4kv_scores* s, ScoreForm* f) {
   return S4KV_OK;
 }
 
+}  // namespace
+
+int s4kv_score_attention(s4kv_cache* cache, int layer, const s4kv_scores* scores, const void* q, int num_q_tokens,
+                         int num_q_heads, const int32_t* block_table, int bt_stride, const int32_t* seq_lens,
+                         const int32_t* slot_ids, int B, float sm_scale, void* out, int out_dtype, void* workspace,
+                         size_t ws_bytes, int max_seq_len, void* stream) {
+  if (!cache || layer < 0 || layer >= cache->cfg.num_layers || B < 0 || max_seq_len < 0 || !scores) return S4KV_ERR_INVALID_ARG;
+  ScoredArgs a;
+  int rc = score_form_of(scores, &a.score);
+  if (rc != S4KV_OK) return rc;
+  if (!on_cache_device(cache)) return S4KV_ERR_INVALID_ARG;
+  if (B == 0) return S4KV_OK;
+  const s4kv_config& c = cache->cfg;
+  if (B > 4096 || num_q_heads <= 0 || num_q_heads % c.num_kv_heads) return S4KV_ERR_INVALID_ARG;
+  const int g = num_q_heads / c.num_kv_heads;
+  rc = mq_shape_ok(cache, num_q_tokens, g);
+  if (rc != S4KV_OK) return rc;
+  if (!q || !out || !block_table || !seq_lens || bt_stride <= 0 || !aligned16(q) || !aligned16(out))
+    return S4KV_ERR_INVALID_ARG;
+  if (out_dtype != S4KV_F32 && out_dtype != c.dtype) return S4KV_ERR_INVALID_ARG;
+  if (ws_bytes < window_ws_bytes(cache, B, num_q_tokens * g)) return S4KV_ERR_WORKSPACE_TOO_SMALL;
+  if (!workspace || !aligned16(workspace)) return S4KV_ERR_INVALID_ARG;
+  const DecodeArgs d = attention_args(cache, layer, q, num_q_heads, block_table, bt_stride, seq_lens, slot_ids, B,
+                                      sm_scale, out, out_dtype, workspace, max_seq_len);
+  window_args(cache, d, num_q_tokens, a.score.window, a.score.sinks, &a);
+  a.cap2 = a.score.cap * 1.4426950408889634f;
+  a.icap2 = a.score.cap > 0.0f ? 1.0f / a.cap2 : 0.0f;
+  return launch_scored(a, cache->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? S4KV_OK : S4KV_ERR_CUDA;
+}
+
+namespace {
 // Sizes of a prompt call: tiles at most, and the most splits that its workspace has room for.
 struct PromptSizes {
   int q_tiles, kv_tiles, most;

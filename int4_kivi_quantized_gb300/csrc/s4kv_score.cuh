@@ -21,6 +21,13 @@ struct ScoreForm {
 };
 constexpr int kNoWindow = 1 << 30;   // wider than any sequence
 
+// Attention of the newest tokens with a score form (s4kv_score_attention).
+struct ScoredArgs : WindowArgs {
+  ScoreForm score;
+  float cap2, icap2;        // cap log2(e) and its inverse; 0: no cap
+};
+cudaError_t launch_scored(const ScoredArgs& a, int num_sms, cudaStream_t st);
+
 // tanh(x) = x P(x^2) for |x| <= 1, P the polynomial of least relative error on [0, 1] (a
 // weighted least-squares fit, 5.0e-8 in exact arithmetic, 1.6e-7 evaluated in binary32).
 __host__ __device__ constexpr float tanh_coef(int i) {

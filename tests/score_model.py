@@ -94,3 +94,26 @@ def compare(got, want, tol, what=""):
     err = (got.double() - want).abs()
     assert bool((err <= tol).all()), f"{what}: error {float(err.max()):.3e}, {float((err / tol).max()):.2f} of the bound"
     return float((err / tol).max()) if err.numel() else 0.0
+
+
+def attend_bound(q, K, V, mk, mv, positions, P, seen, out, out_dtype, bits, cap=0.0, slopes=None, scale=SCALE):
+    """How far attention of the newest tokens with a score form may be from `out`: plain_cache.bound
+    (the arithmetic up to the scores and from the probabilities on is that of windows), with the
+    form's own errors on the scores as in prompt_bound."""
+    from plain_cache import bound
+    base = bound(q, K, V, mk, mv, P, seen.to(q.device), out, out_dtype, bits, scale)
+    H, g = K.shape[1], q.shape[1] // K.shape[1]
+    rep = lambda x: x.repeat_interleave(g, 1)  # noqa: E731
+    fin = lambda x: torch.nan_to_num(x.double(), 0, 0, 0).abs()  # noqa: E731
+    see = seen.to(q.device)
+    S = torch.einsum("qhd,thd->qht", q.double().abs(), rep(fin(K) + mk.double()))
+    S = torch.where(see[:, None], S, torch.zeros_like(S)).amax(-1) * scale
+    dz = torch.zeros_like(S)
+    if cap:
+        dz = dz + torch.minimum(S, torch.full_like(S, cap)) * 2.0 ** -21 + 2.0 ** -21
+    if slopes is not None:
+        t = torch.arange(K.shape[0], device=q.device)
+        far = torch.stack([torch.where(see[i], (t - p).abs(), torch.zeros_like(t)).amax() for i, p in enumerate(positions)])
+        dz = dz + 3 * 2.0 ** -24 * (slopes.double().abs()[None] * far[:, None].double() + S)
+    A = torch.einsum("qht,thd->qhd", P, rep(fin(V) + mv.double()))
+    return base + 2 * (torch.exp2(dz * LOG2E)[..., None] - 1) * A
