@@ -448,6 +448,49 @@ int s4kv_prompt_attention(s4kv_cache* cache, int layer, const s4kv_scores* score
                           int out_dtype, void* workspace, size_t ws_bytes, int max_seq_len,
                           long long sum_seq_lens, void* stream);
 
+/* Page accounting on the device, for programs whose block table lives there (a captured
+ * decode step can take its own pages). refs: int32 [num_pages], device, 16-byte aligned, the
+ * caller's: how many block-table entries name each page, 0 for a free one; all zeros
+ * before the first call. block_table: int32 [rows][bt_stride], a row for each slot; an
+ * entry that names no page is -1. slot_ids: int32 [n] or NULL (row i for sequence i).
+ * n up to 4096, rows up to 65536. Calls on the same refs must be ordered, on one stream
+ * for instance. One kernel launch each.
+ *
+ * s4kv_take_pages: sequence i grows from lens[i] to new_lens[i] tokens: entries
+ * ceil(lens / 16) .. ceil(new_lens / 16) - 1 of its row get free pages (refs 1), the lowest
+ * numbered first, in the order of the sequences and their entries. taken[i] is the number
+ * of them, or -1 where too few pages are free for this sequence and those before it (those
+ * served and not): its row is left as it was, and so are the rows behind it that want pages.
+ * A sequence with a row outside the table (or named twice in the call, each of them), a
+ * negative length or one that shrinks, or pages beyond bt_stride gets -1 and the status
+ * S4KV_DEV_BAD_SLOT, _BAD_LENGTH, _BAD_TABLE; it counts for no pages.
+ *
+ * s4kv_release_pages: entries ceil(first / 16) .. ceil(last / 16) - 1 of each row become -1, and their
+ * pages' refs go down by one; entries that are -1 already are passed over. first = 0 and
+ * last = the length gives a finished sequence's pages back. Behind a window: first = the sinks
+ * rounded up, last = the window's start rounded down, to whole blocks (32 tokens of KIVI
+ * pages, 16 of the others). An entry outside the pool, or of a page that nobody holds, is
+ * S4KV_DEV_BAD_PAGE. */
+int s4kv_take_pages(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int bt_stride, int rows, const int32_t* lens,
+                    const int32_t* new_lens, const int32_t* slot_ids, int n, int32_t* taken, void* stream);
+int s4kv_release_pages(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int bt_stride, int rows, const int32_t* first,
+                       const int32_t* last, const int32_t* slot_ids, int n, void* stream);
+
+/* Forks: fork i continues the sequence of slot src[i] (seq_lens[i] tokens in every layer) in slot
+ * dst[i], as if the same tokens had been appended there. refs, block_table and taken as above
+ * (rows up to max_slots; a row is a slot). Pages that nothing will be written to any more are
+ * shared: dst's entries name them too and refs go up by one (entries that are -1 stay so).
+ * The others are taken as s4kv_take_pages takes them, and their records, the rings and the
+ * stored lengths are copied in every layer. What dst's row and slot held before is overwritten:
+ * release its pages first.
+ * A source may be forked many times in a call, and goes on itself. A dst named twice, or a
+ * source of the same call, or either outside the table is S4KV_DEV_BAD_SLOT, a stored length other
+ * than seq_lens[i] S4KV_DEV_BAD_LENGTH, a row too narrow S4KV_DEV_BAD_TABLE: taken -1, and
+ * nothing of that fork is done, as for one without enough free pages (which reports nothing).
+ * Appends to src and calls that read dst must be ordered with it. Two kernel launches. */
+int s4kv_fork(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int bt_stride, int rows, const int32_t* src,
+              const int32_t* dst, const int32_t* seq_lens, int n, int32_t* taken, void* stream);
+
 /* Restores token ranges of n sequences into dense rows: what attention sees of
  * them, for a dense kernel over a cached prefix or for moving a cache elsewhere.
  *   cu_rows      int32 [n+1], non-decreasing, cu_rows[0] = 0, cu_rows[n] = num_rows:

@@ -100,6 +100,9 @@ def _load():
         "s4kv_prompt_workspace_bytes": [P, I, I, I, I, ctypes.c_longlong, ctypes.POINTER(SZ)],
         "s4kv_prompt_attention": [P, I, ctypes.POINTER(s4kv_scores), P, I, P, I, P, I, P, P, I, ctypes.c_float, P, I, P,
                                   SZ, I, ctypes.c_longlong, P],
+        "s4kv_take_pages": [P, P, P, I, I, P, P, P, I, P, P],
+        "s4kv_release_pages": [P, P, P, I, I, P, P, P, I, P],
+        "s4kv_fork": [P, P, P, I, I, P, P, P, I, P, P],
         "s4kv_gather": [P, I, P, I, P, P, P, P, I, I, P, P, I, P],
         "s4kv_dequant_debug": [P, I, I, P, I, P, P, P],
         "s4kv_get_status": [P, P, ctypes.POINTER(I)],
@@ -296,6 +299,24 @@ def s4kv_prompt_attention(h, layer, scores, q, num_q, cu_q, num_q_heads, block_t
                                       _ptr(slot_ids), int(n), float(sm_scale), _ptr(out), int(out_dtype), _ptr(workspace),
                                       int(ws_bytes), int(max_seq_len), int(sum_seq_lens), _stream(stream)),
            "s4kv_prompt_attention")
+
+
+def s4kv_take_pages(h, refs, block_table, bt_stride, rows, lens, new_lens, slot_ids, n, taken, stream=None):
+    """Free pages into the table rows of growing sequences."""
+    _check(_lib.s4kv_take_pages(h, _ptr(refs), _ptr(block_table), int(bt_stride), int(rows), _ptr(lens), _ptr(new_lens),
+                                _ptr(slot_ids), int(n), _ptr(taken), _stream(stream)), "s4kv_take_pages")
+
+
+def s4kv_release_pages(h, refs, block_table, bt_stride, rows, first, last, slot_ids, n, stream=None):
+    """Table entries given up, their pages' counts down by one."""
+    _check(_lib.s4kv_release_pages(h, _ptr(refs), _ptr(block_table), int(bt_stride), int(rows), _ptr(first), _ptr(last),
+                                   _ptr(slot_ids), int(n), _stream(stream)), "s4kv_release_pages")
+
+
+def s4kv_fork(h, refs, block_table, bt_stride, rows, src, dst, seq_lens, n, taken, stream=None):
+    """Sequences continued in other slots on shared pages."""
+    _check(_lib.s4kv_fork(h, _ptr(refs), _ptr(block_table), int(bt_stride), int(rows), _ptr(src), _ptr(dst), _ptr(seq_lens),
+                          int(n), _ptr(taken), _stream(stream)), "s4kv_fork")
 
 
 def s4kv_gather(h, layer, block_table, bt_stride, seq_lens, slot_ids, first_token, cu_rows, num_rows, n, out_k, out_v,
@@ -714,6 +735,68 @@ class KVCache:
                                 _address(first), cu_rows.data_ptr(), num_rows, n, out_k.data_ptr(), out_v.data_ptr(),
                                 out_dtype, self._handle(stream)), "s4kv_gather")
         return out_k, out_v
+
+    def _pages(self, refs, block_table, slot_ids, n):
+        """Checks what the calls on pages share; the table's (rows, width)."""
+        import torch
+        self._tensor(refs, "refs", torch.int32, (self.cfg.num_pages,))
+        rows, width = self._tensor(block_table, "block_table", torch.int32, (None, None))
+        if slot_ids is not None:
+            self._tensor(slot_ids, "slot_ids", torch.int32, (n,))
+        elif rows < n:
+            raise ValueError("block_table has fewer rows than there are sequences")
+        return rows, width
+
+    def _taken(self, taken, n, stream):
+        import torch
+        if taken is None:
+            return self._made(stream, torch.empty, (n,), dtype=torch.int32, device=self.pool.device)
+        self._tensor(taken, "taken", torch.int32, (n,))
+        return taken
+
+    @_on_its_device
+    def take_pages(self, refs, block_table, lens, new_lens, slot_ids=None, taken=None, stream=None):
+        """Free pages (refs [num_pages]: the table entries that name each; 0: free) for sequences that
+        grow from `lens` to `new_lens` tokens, into their rows of block_table [slots, entries], lowest
+        page first. Returns `taken` [n]: how many each got, -1 where too few are free."""
+        import torch
+        n = lens.shape[0]
+        self._tensor(lens, "lens", torch.int32, (n,))
+        self._tensor(new_lens, "new_lens", torch.int32, (n,))
+        rows, width = self._pages(refs, block_table, slot_ids, n)
+        taken = self._taken(taken, n, stream)
+        _check(_lib.s4kv_take_pages(self.h, refs.data_ptr(), block_table.data_ptr(), width, rows, lens.data_ptr(),
+                                    new_lens.data_ptr(), _address(slot_ids), n, taken.data_ptr(), self._handle(stream)),
+               "s4kv_take_pages")
+        return taken
+
+    @_on_its_device
+    def release_pages(self, refs, block_table, first, last, slot_ids=None, stream=None):
+        """Gives up the pages of tokens first .. last - 1 of each sequence (whole pages from `first`
+        on, the one that holds `last` - 1 included): their entries become -1, their counts go down."""
+        import torch
+        n = first.shape[0]
+        self._tensor(first, "first", torch.int32, (n,))
+        self._tensor(last, "last", torch.int32, (n,))
+        rows, width = self._pages(refs, block_table, slot_ids, n)
+        _check(_lib.s4kv_release_pages(self.h, refs.data_ptr(), block_table.data_ptr(), width, rows, first.data_ptr(),
+                                       last.data_ptr(), _address(slot_ids), n, self._handle(stream)), "s4kv_release_pages")
+
+    @_on_its_device
+    def fork(self, refs, block_table, src, dst, seq_lens, taken=None, stream=None):
+        """Continues the sequences of slots src (seq_lens tokens) in slots dst too, in every layer: pages
+        that are done with are shared (refs up by one), the others taken and copied, rings and
+        lengths copied. block_table has a row for each slot. Returns `taken` [n] as take_pages does."""
+        import torch
+        n = src.shape[0]
+        self._tensor(src, "src", torch.int32, (n,))
+        self._tensor(dst, "dst", torch.int32, (n,))
+        self._tensor(seq_lens, "seq_lens", torch.int32, (n,))
+        rows, width = self._pages(refs, block_table, src, n)
+        taken = self._taken(taken, n, stream)
+        _check(_lib.s4kv_fork(self.h, refs.data_ptr(), block_table.data_ptr(), width, rows, src.data_ptr(), dst.data_ptr(),
+                              seq_lens.data_ptr(), n, taken.data_ptr(), self._handle(stream)), "s4kv_fork")
+        return taken
 
     def dequant(self, layer, slot, block_table_row, seq_len, stream=None):
         import torch

@@ -28,6 +28,7 @@ SOURCES = {
     "s4kv_gather.cu": EXACT,
     "s4kv_tiles.cu": EXACT,
     "s4kv_prompt.cu": [],
+    "s4kv_pages.cu": [],
 }
 
 
@@ -59,6 +60,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
                os.path.join(CSRC, "s4kv_restore.cuh"), os.path.join(CSRC, "s4kv_tcgen05.cuh"),
                os.path.join(CSRC, "s4kv_score.cuh"), os.path.join(CSRC, "s4kv_window.cuh"),
                os.path.join(CSRC, "s4kv_prompt.cuh"),
+               os.path.join(CSRC, "s4kv_pages.cuh"),
                os.path.join(ROOT, "include", "s4kv.h"),
                __file__]
     jobs = []

@@ -1,6 +1,7 @@
 // Host side of the s4kv C ABI: argument checks, pool layout, launches and the
 // status word. Declarations and the byte format are in include/s4kv.h.
 
+#include "s4kv_pages.cuh"
 #include "s4kv_prompt.cuh"
 
 #include <cmath>
@@ -887,6 +888,80 @@ int s4kv_prompt_attention(s4kv_cache* cache, int layer, const s4kv_scores* score
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (z.kv_tiles > 0 && launch_tiles(a, st) != cudaSuccess) return S4KV_ERR_CUDA;
   return launch_prompt(a, st) == cudaSuccess ? S4KV_OK : S4KV_ERR_CUDA;
+}
+
+namespace {
+// What the calls on pages have in common, checked.
+int page_args(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int bt_stride, int rows, const int32_t* from,
+              const int32_t* to, int n, PageArgs* a) {
+  if (!cache || n < 0 || n > kMaxPageJobs || rows < 0 || rows > kMaxPageRows) return S4KV_ERR_INVALID_ARG;
+  if (!on_cache_device(cache)) return S4KV_ERR_INVALID_ARG;
+  if (n == 0) return S4KV_OK;
+  if (!refs || !aligned16(refs) || !block_table || bt_stride <= 0 || !from || !to) return S4KV_ERR_INVALID_ARG;
+  *a = PageArgs{};
+  a->status = reinterpret_cast<int*>(cache->pool + cache->lay.status_offset);
+  a->refs = refs;
+  a->table = block_table;
+  a->from = from;
+  a->to = to;
+  a->bt_stride = bt_stride;
+  a->rows = rows;
+  a->n = n;
+  a->num_pages = cache->cfg.num_pages;
+  return S4KV_OK;
+}
+}  // namespace
+
+int s4kv_take_pages(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int bt_stride, int rows, const int32_t* lens,
+                    const int32_t* new_lens, const int32_t* slot_ids, int n, int32_t* taken, void* stream) {
+  PageArgs a;
+  const int rc = page_args(cache, refs, block_table, bt_stride, rows, lens, new_lens, n, &a);
+  if (rc != S4KV_OK || n == 0) return rc;
+  if (!taken || (!slot_ids && n > rows)) return S4KV_ERR_INVALID_ARG;
+  a.slot_ids = slot_ids;
+  a.taken = taken;
+  return launch_take(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? S4KV_OK : S4KV_ERR_CUDA;
+}
+
+int s4kv_release_pages(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int bt_stride, int rows, const int32_t* first,
+                       const int32_t* last, const int32_t* slot_ids, int n, void* stream) {
+  PageArgs a;
+  const int rc = page_args(cache, refs, block_table, bt_stride, rows, first, last, n, &a);
+  if (rc != S4KV_OK || n == 0) return rc;
+  if (!slot_ids && n > rows) return S4KV_ERR_INVALID_ARG;
+  a.slot_ids = slot_ids;
+  return launch_release(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? S4KV_OK : S4KV_ERR_CUDA;
+}
+
+int s4kv_fork(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int bt_stride, int rows, const int32_t* src,
+              const int32_t* dst, const int32_t* seq_lens, int n, int32_t* taken, void* stream) {
+  PageArgs a;
+  const int rc = page_args(cache, refs, block_table, bt_stride, rows, src, dst, n, &a);
+  if (rc != S4KV_OK || n == 0) return rc;
+  const s4kv_config& c = cache->cfg;
+  if (!seq_lens || !taken || rows > c.max_slots) return S4KV_ERR_INVALID_ARG;
+  if (c.num_layers > 65535) return S4KV_ERR_UNSUPPORTED;   // (a grid's second dimension)
+  a.seq_lens = seq_lens;
+  a.taken = taken;
+  a.pool_layers = cache->pool + cache->lay.layer_offset;
+  a.lens = reinterpret_cast<int*>(cache->pool + cache->lay.lens_offset);
+  a.layer_stride = cache->lay.layer_stride;
+  a.kring_offset = cache->lay.kring_offset;
+  a.vring_offset = cache->lay.vring_offset;
+  a.kring_slot = cache->lay.kring_slot_stride;
+  a.vring_slot = cache->lay.vring_slot_stride;
+  a.kring_head = cache->lay.kring_head_stride;
+  a.vring_head = cache->lay.vring_head_stride;
+  a.page_bytes = cache->lay.page_stride;
+  a.layers = c.num_layers;
+  a.H = c.num_kv_heads;
+  a.R = c.residual_v;
+  a.max_slots = c.max_slots;
+  a.bits = cache->bits;
+  // KIVI: from the older of the first ring value and the first ring key, at most R or 31 tokens apart,
+  // both ends inside a page
+  a.pages_at_most = cache->bits == 8 ? 1 : cache->bits == S4KV_BITS_INT8 ? 0 : ((a.R > kG ? a.R : kG) + 2 * kP - 2) / kP + 1;
+  return launch_fork(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? S4KV_OK : S4KV_ERR_CUDA;
 }
 
 int s4kv_gather(s4kv_cache* cache, int layer, const int32_t* block_table, int bt_stride,

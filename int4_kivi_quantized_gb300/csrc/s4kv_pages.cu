@@ -1,0 +1,302 @@
+// Page accounting on the device (s4kv_take_pages, s4kv_release_pages) and forks (s4kv_fork):
+// refs[p] counts the block-table entries that name page p, 0 is free.
+//
+// Giving out pages is a scan: sequence i's pages are the free ones of rank need_1 + .. +
+// need_(i-1) on, and the page of rank k is the k-th zero of refs. One CTA does it, as a scheduler's
+// step asks for some hundred pages: it stops at the tile of refs where enough are found. What
+// bounds it is latency: the launch, the lengths, one or two tiles, the entries.
+//
+// A fork then copies what both sequences would go on writing (the pages from the first
+// unfinished one on, the rings), a CTA for each page, or head's rings, of each layer, 16 bytes a
+// thread and load, eight loads in flight: bound by those bytes, read and written once.
+
+#include "s4kv_pages.cuh"
+
+namespace s4kv {
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kEach = 16;                     // neighbouring counts of a thread
+constexpr int kTile = kThreads * kEach;
+
+__device__ __forceinline__ unsigned add_to(unsigned a, unsigned b) { return min(a + b, 0x7fffffffu); }   // (both below 2^31)
+
+// Exclusive sum over the CTA, and the total, saturating.
+__device__ __forceinline__ unsigned block_scan(unsigned x, unsigned& total) {
+  __shared__ unsigned tot[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned s = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(0xffffffffu, s, o);
+    if (lane >= o) s = add_to(s, y);
+  }
+  __syncthreads();   // the totals of the call before are read
+  if (lane == 31) tot[warp] = s;
+  __syncthreads();
+  unsigned t = tot[lane], before = 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned y = __shfl_up_sync(0xffffffffu, t, o);
+    if (lane >= o) t = add_to(t, y);
+  }
+  total = __shfl_sync(0xffffffffu, t, 31);
+  before = __shfl_sync(0xffffffffu, t, max(warp - 1, 0));
+  const unsigned mine = __shfl_up_sync(0xffffffffu, s, 1);
+  return add_to(warp > 0 ? before : 0u, lane > 0 ? mine : 0u);
+}
+
+__device__ __forceinline__ int pages_for(int tokens) { return static_cast<int>((static_cast<unsigned>(tokens) + kP - 1) / kP); }
+
+// Sequence i of the call: its table row, and the entries [e0, e1) that it wants pages for.
+struct Want {
+  int row, e0, e1;
+};
+template <bool FORK>
+__device__ __forceinline__ Want want_of(const PageArgs& a, int i) {
+  if (FORK) {
+    const int T = a.seq_lens[i];
+    return Want{a.to[i], held_of(a.bits, T, a.R).done, pages_for(T)};
+  }
+  return Want{a.slot_ids ? a.slot_ids[i] : i, pages_for(a.from[i]), pages_for(a.to[i])};
+}
+
+template <bool FORK>
+__global__ void __launch_bounds__(kThreads, 1) give_kernel(PageArgs a) {
+  __shared__ unsigned pre[kMaxPageJobs + 1];                  // pages wanted by the sequences before
+  __shared__ unsigned seen[kMaxPageRows / 32], twice[kMaxPageRows / 32], source[FORK ? kMaxPageRows / 32 : 1];   // rows, a bit each
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < (a.rows + 31) / 32; i += kThreads) {
+    seen[i] = twice[i] = 0u;
+    if (FORK) source[i] = 0u;
+  }
+  stream_wait();
+  __syncthreads();
+  auto row_ok = [&](int r) { return r >= 0 && r < a.rows; };
+  auto bit = [&](const unsigned* set, int r) { return (set[r >> 5] >> (r & 31)) & 1u; };
+  for (int i = tid; i < a.n; i += kThreads) {
+    const int r = FORK ? a.to[i] : a.slot_ids ? a.slot_ids[i] : i;
+    if (row_ok(r) && (atomicOr(&seen[r >> 5], 1u << (r & 31)) >> (r & 31)) & 1u) atomicOr(&twice[r >> 5], 1u << (r & 31));
+    if (FORK && row_ok(a.from[i])) atomicOr(&source[a.from[i] >> 5], 1u << (a.from[i] & 31));
+  }
+  __syncthreads();
+  // why sequence i gets nothing, whatever is free: 0 if it may
+  auto refused = [&](int i, int& arg) -> int {
+    const int r = FORK ? a.to[i] : a.slot_ids ? a.slot_ids[i] : i;
+    arg = r;
+    if (!row_ok(r) || bit(twice, r) || (FORK && (!row_ok(a.from[i]) || bit(source, r)))) return S4KV_DEV_BAD_SLOT;
+    arg = i;
+    if (FORK ? a.seq_lens[i] < 0 : (a.from[i] < 0 || a.to[i] < a.from[i])) return S4KV_DEV_BAD_LENGTH;
+    if (pages_for(FORK ? a.seq_lens[i] : a.to[i]) > a.bt_stride) return S4KV_DEV_BAD_TABLE;
+    return 0;
+  };
+  if (FORK) {   // a warp a fork: every layer and head of the source holds as many tokens
+    for (int i = warp; i < a.n; i += kThreads / 32) {
+      int arg, why = refused(i, arg);
+      if (!why) {
+        bool other = false;
+        for (int k = lane; k < a.layers * a.H; k += 32)
+          other = other || __ldcg(a.lens + (static_cast<size_t>(k / a.H) * a.max_slots + a.from[i]) * a.H + k % a.H) != a.seq_lens[i];
+        if (__any_sync(0xffffffffu, other)) why = S4KV_DEV_BAD_LENGTH;
+      }
+      if (lane == 0) {
+        if (why) report(a.status, S4KV_ERR_DEVICE, why, arg);
+        const Want w = want_of<FORK>(a, i);
+        pre[i + 1] = why ? 0u : static_cast<unsigned>(w.e1 - w.e0);
+        a.taken[i] = why ? -1 : 0;
+      }
+    }
+  } else {
+    for (int i = tid; i < a.n; i += kThreads) {
+      int arg;
+      const int why = refused(i, arg);
+      if (why) report(a.status, S4KV_ERR_DEVICE, why, arg);
+      const Want w = want_of<FORK>(a, i);
+      pre[i + 1] = why ? 0u : static_cast<unsigned>(w.e1 - w.e0);
+      a.taken[i] = why ? -1 : 0;
+    }
+  }
+  __syncthreads();
+  unsigned total;
+  {   // sums in place: four neighbouring sequences a thread
+    constexpr int kSeqs = kMaxPageJobs / kThreads;
+    unsigned x[kSeqs], mine = 0;
+#pragma unroll
+    for (int k = 0; k < kSeqs; ++k) {
+      x[k] = kSeqs * tid + k < a.n ? pre[kSeqs * tid + k + 1] : 0u;
+      mine = add_to(mine, x[k]);
+    }
+    unsigned at = block_scan(mine, total);
+#pragma unroll
+    for (int k = 0; k < kSeqs; ++k) {
+      at = add_to(at, x[k]);
+      if (kSeqs * tid + k < a.n) pre[kSeqs * tid + k + 1] = at;
+    }
+    if (tid == 0) pre[0] = 0u;
+  }
+  // free pages of a tile of counts: a bit for each of this thread's
+  auto look = [&](int base) -> unsigned {
+    unsigned z = 0;
+    const int p = base + tid * kEach;
+    if (p + kEach <= a.num_pages) {
+#pragma unroll
+      for (int k = 0; k < kEach / 4; ++k) {
+        const int4 v = *reinterpret_cast<const int4*>(a.refs + p + 4 * k);
+        z |= ((v.x == 0 ? 1u : 0u) | (v.y == 0 ? 2u : 0u) | (v.z == 0 ? 4u : 0u) | (v.w == 0 ? 8u : 0u)) << (4 * k);
+      }
+    } else {
+      for (int k = 0; k < kEach; ++k)
+        if (p + k < a.num_pages && a.refs[p + k] == 0) z |= 1u << k;
+    }
+    return z;
+  };
+  // enough of them, or all there are (the last tile looked at is at hand again if it is the first)
+  unsigned found = 0, z0 = 0;
+  for (int base = 0; found < total && base < a.num_pages; base += kTile) {
+    const unsigned z = look(base);
+    if (base == 0) z0 = z;
+    unsigned here;
+    block_scan(__popc(z), here);
+    found = add_to(found, here);
+  }
+  __syncthreads();
+  unsigned granted = total;
+  if (found < total) {   // sequences in order, while they can be served
+    int lo = 0, hi = a.n;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= found) lo = mid; else hi = mid - 1;
+    }
+    granted = pre[lo];
+  }
+  for (int i = tid; i < a.n; i += kThreads) {
+    const Want w = want_of<FORK>(a, i);
+    if (a.taken[i] == 0 && w.e1 > w.e0) a.taken[i] = pre[i + 1] <= granted ? w.e1 - w.e0 : -1;
+  }
+  unsigned rank0 = 0;
+  for (int base = 0; rank0 < granted && base < a.num_pages; base += kTile) {
+    unsigned z = base == 0 ? z0 : look(base), here;
+    unsigned k = rank0 + block_scan(__popc(z), here);
+    rank0 += here;
+    while (z && k < granted) {
+      const int p = base + tid * kEach + __ffs(z) - 1;
+      z &= z - 1;
+      int lo = 0, hi = a.n - 1;   // the last sequence with pre <= k
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= k) lo = mid; else hi = mid - 1;
+      }
+      const Want w = want_of<FORK>(a, lo);
+      a.table[static_cast<long long>(w.row) * a.bt_stride + w.e0 + (k - pre[lo])] = p;
+      a.refs[p] = 1;
+      ++k;
+    }
+  }
+}
+
+constexpr int kRelease = 256;
+__global__ void __launch_bounds__(kRelease) release_kernel(PageArgs a) {
+  stream_wait();
+  const int i = blockIdx.x, row = a.slot_ids ? a.slot_ids[i] : i, first = a.from[i], last = a.to[i];
+  int why = 0;
+  if (row < 0 || row >= a.rows) why = S4KV_DEV_BAD_SLOT;
+  else if (first < 0 || last < 0) why = S4KV_DEV_BAD_LENGTH;
+  else if (last > first && pages_for(last) > a.bt_stride) why = S4KV_DEV_BAD_TABLE;
+  if (why) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) report(a.status, S4KV_ERR_DEVICE, why, why == S4KV_DEV_BAD_SLOT ? row : i);
+    return;
+  }
+  const int e1 = last > first ? pages_for(last) : 0;
+  int* entries = a.table + static_cast<long long>(row) * a.bt_stride;
+  for (int e = pages_for(first) + blockIdx.y * kRelease + threadIdx.x; e < e1; e += gridDim.y * kRelease) {
+    const int p = atomicExch(entries + e, -1);   // (a row named twice: only one of them gets it)
+    if (p == -1) continue;
+    if (p < 0 || p >= a.num_pages) {
+      report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, p);
+    } else if (atomicSub(a.refs + p, 1) <= 0) {   // nobody had it
+      atomicAdd(a.refs + p, 1);
+      report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, p);
+    }
+  }
+}
+
+constexpr int kCopy = 256;
+// `bytes` (a multiple of 16) by the CTA.
+__device__ __forceinline__ void copy_bytes(char* dst, const char* src, int bytes) {
+  const int n = bytes / 16;
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+  constexpr int kAhead = 8;
+  for (int i0 = threadIdx.x; i0 < n; i0 += kAhead * kCopy) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (i0 + k * kCopy < n) v[k] = s[i0 + k * kCopy];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+      if (i0 + k * kCopy < n) d[i0 + k * kCopy] = v[k];
+  }
+}
+
+// blockIdx: x the part (page, head's rings and length, the shared entries), y the layer, z the fork.
+__global__ void __launch_bounds__(kCopy) fork_kernel(PageArgs a) {
+  stream_wait();
+  const int i = blockIdx.z, layer = blockIdx.y, part = blockIdx.x;
+  if (a.taken[i] < 0) return;
+  const int src = a.from[i], dst = a.to[i], T = a.seq_lens[i];
+  const Held x = held_of(a.bits, T, a.R);
+  const int* from = a.table + static_cast<long long>(src) * a.bt_stride;
+  int* to = a.table + static_cast<long long>(dst) * a.bt_stride;
+  char* base = a.pool_layers + layer * a.layer_stride;
+  if (part < a.pages_at_most) {
+    const int e = x.done + part;
+    if (e >= x.held) return;
+    const int p = from[e], q = to[e];
+    if (p < 0 || p >= a.num_pages) {
+      if (threadIdx.x == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, p);
+      return;
+    }
+    copy_bytes(base + q * a.page_bytes, base + p * a.page_bytes, static_cast<int>(a.page_bytes));
+  } else if (part < a.pages_at_most + a.H) {
+    const int h = part - a.pages_at_most;
+    char* k = base + a.kring_offset + h * a.kring_head;
+    char* v = base + a.vring_offset + h * a.vring_head;
+    copy_bytes(k + dst * a.kring_slot, k + src * a.kring_slot, x.krows * kD * 2);
+    copy_bytes(v + dst * a.vring_slot, v + src * a.vring_slot, x.vrows * kD * 2);
+    if (threadIdx.x == 0) a.lens[(static_cast<size_t>(layer) * a.max_slots + dst) * a.H + h] = T;
+  } else if (layer == 0) {
+    for (int e = (part - a.pages_at_most - a.H) * kCopy + threadIdx.x; e < x.done; e += kCopy * (gridDim.x - a.pages_at_most - a.H)) {
+      int p = from[e];
+      if (p < -1 || p >= a.num_pages) {
+        report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, p);
+        p = -1;
+      }
+      to[e] = p;
+      if (p >= 0) atomicAdd(a.refs + p, 1);   // (-1: given away already)
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_take(const PageArgs& a, cudaStream_t st) {
+  return launch_behind(give_kernel<false>, dim3(1), dim3(kThreads), 0, st, a);
+}
+
+cudaError_t launch_release(const PageArgs& a, cudaStream_t st) {
+  int more = (a.bt_stride + kRelease - 1) / kRelease;   // CTAs of a long row
+  if (more > 16) more = 16;
+  return launch_behind(release_kernel, dim3(static_cast<unsigned>(a.n), static_cast<unsigned>(more)), dim3(kRelease), 0, st, a);
+}
+
+cudaError_t launch_fork(const PageArgs& a, cudaStream_t st) {
+  cudaError_t e = launch_behind(give_kernel<true>, dim3(1), dim3(kThreads), 0, st, a);
+  if (e != cudaSuccess) return e;
+  const unsigned parts = static_cast<unsigned>(a.pages_at_most + a.H);
+  // the shared entries: with the first layer's parts (y = 0), a CTA for every 256
+  int more = (a.bt_stride + kCopy - 1) / kCopy;
+  if (more > 8) more = 8;
+  return launch_behind(fork_kernel, dim3(parts + more, static_cast<unsigned>(a.layers), static_cast<unsigned>(a.n)), dim3(kCopy), 0, st, a);
+}
+
+}  // namespace s4kv
