@@ -884,6 +884,10 @@ int s4kv_prompt_attention(s4kv_cache* cache, int layer, const s4kv_scores* score
   long long seen = max_seq_len;
   const long long span = static_cast<long long>(a.form.window) + (num_q < kQRows / a.g + 1 ? num_q : kQRows / a.g + 1) + a.form.sinks;
   if (!a.form.prefix && span < seen) seen = span;
+  // kv tiles of all sequences that a window leaves: each has the window's and its chunk's tokens, whose ends
+  // may cut two more tiles, and the sinks'
+  const long long left = (static_cast<long long>(n) * a.form.window + num_q) / kKvTile + static_cast<long long>(n) * (3 + a.form.sinks / kKvTile);
+  a.kv_grid = a.form.window < kNoWindow && left < z.kv_tiles ? static_cast<int>(left) : z.kv_tiles;
   a.splits = prompt_splits(z, a.H, cache->num_sms, (seen + kKvTile - 1) / kKvTile);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (z.kv_tiles > 0 && launch_tiles(a, st) != cudaSuccess) return S4KV_ERR_CUDA;

@@ -23,12 +23,16 @@
 #include "s4kv_tcgen05.cuh"
 
 #include <mutex>
+#include <type_traits>
 
 namespace s4kv {
 namespace {
 
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
-constexpr int kThreads = 320;
+constexpr int kRowWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 384;        // (two more warps make a warpgroup of the last four)
+// Registers: 168 a thread at launch, 208 for the rows' two warpgroups and 88 for the third.
+constexpr int kRegsRow = 208, kRegsRest = 88;
+static_assert(2 * kRegsRow + kRegsRest <= 3 * 168, "the shares are what the launch holds");
 constexpr int kBufs = 5;
 constexpr float kLazyP = 8.0f;       // P up to 2^8 before its sum divides it: exact enough in f16, and rescales are rare
 constexpr int kQBytes = 128 * kD * 2;
@@ -36,23 +40,50 @@ constexpr int kSmemBytes = 2 * kQBytes + kBufs * kTileBytes + 1024;
 // tensor memory columns: S (and P) of tile s at 128 s, O at 256 + 128 s
 constexpr uint32_t kTmemCols = 512;
 
-// D[tmem] (+)= A[tmem] B: A is K-major f16 pairs, a row a lane.
-__device__ __forceinline__ void umma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool acc) {
+// The MMAs, by descriptors in two words: the upper one is the same for every operand (rows of 128
+// swizzled bytes, eight of them 1024 bytes), the lower one a start address / 16 plus the leading
+// byte offset / 16 at bit 16, so that the next K-step is an addition (umma_desc composes a
+// descriptor's fields, ten instructions between two MMAs).
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (kSw128 << 29);
+constexpr uint32_t kDescK = 1u << 16;                     // K-major: unused
+constexpr uint32_t kDescMn = (16384u >> 4) << 16;         // MN-major: from one 64 channels to the next
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_low), "r"(b_low), "r"(kDescHigh), "r"(idesc), "r"(acc ? 1u : 0u)
       : "memory");
 }
-// Shared-memory descriptor of a 128-byte swizzled MN-major operand: rows of 64 elements of MN, the
-// next 64 `lbo` bytes on, the next eight rows (of K) 1024 bytes on.
-__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t lbo) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(kSw128) << 61);
+// A in tensor memory: f16 pairs, a row a lane.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_low), "r"(kDescHigh), "r"(idesc), "r"(acc ? 1u : 0u)
+      : "memory");
+}
+// One lane of a converged warp, the same every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 constexpr uint32_t kIdescQK = umma_idesc(128, 128);
 constexpr uint32_t kIdescPV = umma_idesc(128, 128) | (1u << 16);   // B is MN-major
 
+// mbar_try_wait that lets the thread sleep inside for up to `ns`: warps that poll take the shared
+// memory's bandwidth from the operands (a 32k prompt: 750 us, polling 823).
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t* bar, uint32_t parity, uint32_t ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(ns)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -65,30 +96,21 @@ struct PromptSmem {
   uint32_t tmem;
 };
 
-// A row's output (y: 32 channels from c0 on).
-__device__ __forceinline__ void store32(void* out, int dtype, long long row, int c0, const float (&y)[32]) {
-  const long long idx = row * kD + c0;
-  if (dtype == S4KV_F32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + idx);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-  } else {
-    uint4* p = reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + idx);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint4 w;
-      w.x = pack_in_dtype(y[8 * i], y[8 * i + 1], dtype);
-      w.y = pack_in_dtype(y[8 * i + 2], y[8 * i + 3], dtype);
-      w.z = pack_in_dtype(y[8 * i + 4], y[8 * i + 5], dtype);
-      w.w = pack_in_dtype(y[8 * i + 6], y[8 * i + 7], dtype);
-      p[i] = w;
-    }
-  }
-}
-
 __device__ __forceinline__ float* part_rows(const PromptArgs& a, long long item) { return a.part + item * (kQRows * kD); }
 __device__ __forceinline__ float* part_ml(const PromptArgs& a, long long item) {
   return a.part + static_cast<long long>(a.q_tiles) * a.H * a.splits * (kQRows * kD) + item * (2 * kQRows);
+}
+
+// The larger (smaller) of three numbers: one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float y;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
 }
 
 // One row's scores of a kv tile, from S to log2 units.
@@ -98,36 +120,55 @@ struct RowScore {
   float slope2;    // slope log2(e)
 };
 
-template <bool CAP, bool SLOPE>
-__device__ __forceinline__ void score_form(float (&x)[128], const RowScore& f, float rel) {
-  if constexpr (CAP) {
-    float top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 128; ++i) top = fmaxf(top, fabsf(x[i]));
-    // (a score that is NaN does not show in `top` and stays NaN in both forms)
-    if (__all_sync(0xffffffffu, top * f.mul <= 1.0f)) {
-      const float2 mul2 = make_float2(f.mul, f.mul), cap2 = make_float2(f.cap2, f.cap2);
-#pragma unroll
-      for (int i = 0; i < 128; i += 2) {
-        const float2 u = __fmul2_rn(make_float2(x[i], x[i + 1]), mul2), w = __fmul2_rn(u, u);
-        float2 p = make_float2(tanh_coef(6), tanh_coef(6));
-#pragma unroll
-        for (int k = 5; k >= 0; --k) p = __ffma2_rn(p, w, make_float2(tanh_coef(k), tanh_coef(k)));
-        p = __fmul2_rn(__fmul2_rn(u, cap2), p);
-        x[i] = p.x;
-        x[i + 1] = p.y;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 128; ++i) x[i] = f.cap2 * tanh_any(x[i] * f.mul);
-    }
-  } else if constexpr (SLOPE) {
-#pragma unroll
-    for (int i = 0; i < 128; ++i) x[i] *= f.mul;
+// tanh(x) = x P(x^2) for |x| <= kNearCap, where the scores of a model trained with a cap are: four
+// coefficients, off by 5.5e-7 relative, instead of the seven that |x| <= 1 takes.
+constexpr float kNearCap = 0.5f;
+constexpr int kNearCoefs = 4;
+__host__ __device__ constexpr float near_coef(int i) {
+  constexpr float c[kNearCoefs] = {0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.04440222680568695f};
+  return c[i];
+}
+// The same from S to log2 units: S Q(S^2) with Q's coefficients at hand per row.
+struct NearCap {
+  float c[kNearCoefs];
+  __device__ __forceinline__ float2 inner(float2 s) const {   // Q(S^2)
+    const float2 w = __fmul2_rn(s, s);
+    float2 p = __ffma2_rn(w, make_float2(c[3], c[3]), make_float2(c[2], c[2]));
+    p = __ffma2_rn(p, w, make_float2(c[1], c[1]));
+    return __ffma2_rn(p, w, make_float2(c[0], c[0]));
   }
-  if constexpr (SLOPE) {   // rel: the query's position less the tile's first token
+  __device__ __forceinline__ float operator()(float s) const { return s * inner(make_float2(s, s)).x; }
+};
+
+// x from S to capped scores in log2 units. `top`: the row's largest |S|.
+__device__ __forceinline__ void through_cap(float (&x)[128], const RowScore& f, const NearCap& near, bool near_zero, float top) {
+  if (near_zero) {
 #pragma unroll
-    for (int i = 0; i < 128; ++i) x[i] = fmaf(-f.slope2, fabsf(static_cast<float>(i) - rel), x[i]);
+    for (int i = 0; i < 128; i += 2) {
+      const float2 s = make_float2(x[i], x[i + 1]), y = __fmul2_rn(s, near.inner(s));
+      x[i] = y.x;
+      x[i + 1] = y.y;
+    }
+  } else if (__all_sync(0xffffffffu, top * f.mul <= 1.0f)) {
+    const float2 mul2 = make_float2(f.mul, f.mul), cap2 = make_float2(f.cap2, f.cap2);
+#pragma unroll
+    for (int i = 0; i < 128; i += 2) {
+      const float2 u = __fmul2_rn(make_float2(x[i], x[i + 1]), mul2), w = __fmul2_rn(u, u);
+      float2 p = make_float2(tanh_coef(6), tanh_coef(6));
+#pragma unroll
+      for (int k = 5; k >= 0; --k) p = __ffma2_rn(p, w, make_float2(tanh_coef(k), tanh_coef(k)));
+      p = __fmul2_rn(__fmul2_rn(u, cap2), p);
+      x[i] = p.x;
+      x[i + 1] = p.y;
+    }
+  } else {   // cap - 2 cap / (1 + exp(2 x)): off by 2^-22 of the cap, which the largest scores here pass
+    const float by = f.mul * 2.8853900817779268f, down = -2.0f * f.cap2;
+#pragma unroll
+    for (int i = 0; i < 128; ++i) {
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_fast(x[i] * by)));
+      x[i] = fmaf(down, r, f.cap2);
+    }
   }
 }
 
@@ -139,6 +180,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
   char* q_tiles = reinterpret_cast<char*>(smem_raw) + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   char* ring = q_tiles + 2 * kQBytes;
   if (tid == 0) {
+    sm.abort = 0;
+    sm.lo = 0x7fffffff;
+    sm.hi = -1;
+  }
+  stream_wait();
+  Place pl;
+  // the last tiles of a sequence, whose rows see the most, start first
+  const int where = find_tile<kThreads, true>(a, static_cast<int>(gridDim.x - 1 - blockIdx.x), pl);
+  if (where != kFound) return;
+  const int h = blockIdx.y, z = blockIdx.z, b = pl.b, g = a.g, cu0 = pl.cu0, m = pl.m, T = pl.T;
+  const int row0 = pl.tile * kQRows;
+  const int rows = static_cast<int>(min(static_cast<long long>(kQRows), static_cast<long long>(m) * g - row0));
+  const int tiles = rows > 128 ? 2 : 1;
+  // a row's token of the chunk; its row of q and out
+  const int tok0 = row0 / g, rem0 = row0 - tok0 * g, by_g = 65536 / g + 1;   // x / g = x by_g >> 16 for x < 264, g <= 8
+  auto token_of = [&](int r) { return tok0 + ((rem0 + r) * by_g >> 16); };
+  auto out_row = [&](int r) -> long long {
+    const int i = token_of(r);
+    return (static_cast<long long>(cu0) + i) * a.Hq + h * g + (row0 + r - i * g);
+  };
+  if (tid == 0) {
     for (int i = 0; i < kBufs; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 1);
@@ -149,35 +211,17 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
       mbar_init(&sm.odone[s], 1);
     }
     mbar_init(&sm.drain, 1);
-    sm.abort = 0;
-    sm.lo = 0x7fffffff;
-    sm.hi = -1;
   }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  stream_wait();
-  Place pl;
-  // the last tiles of a sequence, whose rows see the most, start first
-  const int where = find_tile<kThreads, true>(a, static_cast<int>(gridDim.x - 1 - blockIdx.x), pl);
-  if (where != kFound) return;
-  const int h = blockIdx.y, z = blockIdx.z, b = pl.b, g = a.g;
-  const int cu0 = a.cu_q[b], m = a.cu_q[b + 1] - cu0, T = a.seq_lens[b], slot = a.slot_ids ? a.slot_ids[b] : b;
+  const int slot = a.slot_ids ? a.slot_ids[b] : b;
   int arg;
-  const int why = refused(a, pl, m, T, slot, h, arg);
+  const int why = refused(a, pl, slot, h, arg);
   if (why && tid == 0) report(a.status, S4KV_ERR_DEVICE, why, arg);
-  const int row0 = pl.tile * kQRows;
-  const int rows = static_cast<int>(min(static_cast<long long>(kQRows), static_cast<long long>(m) * g - row0));
-  const int tiles = rows > 128 ? 2 : 1;
-  // a row's token of the chunk; its row of q and out
-  auto token_of = [&](int r) { return (row0 + r) / g; };
-  auto out_row = [&](int r) -> long long {
-    const int i = token_of(r);
-    return (static_cast<long long>(cu0) + i) * a.Hq + h * g + (row0 + r - i * g);
-  };
 
   // ---- what each row sees; the queries as f16 operands ----
   Span sp{0, 0x7fffffff};   // (rows past the last one: everything, so that they ask for no masks)
   int pos = 0;
-  if (tid < kQRows && !why) {
+  if (warp < kRowWarps && !why) {
     if (tid < rows) {
       const int i = token_of(tid);
       pos = T - m + i;
@@ -191,28 +235,33 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
       atomicMax(&sm.hi, hi);
     }
     const int c = lane & 15;
-#pragma unroll 4
+    uint4 v[16];   // every load first
+#pragma unroll
     for (int k = 0; k < 16; ++k) {
       const int r = 32 * warp + 2 * k + (lane >> 4);
-      uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (r < rows) v = reinterpret_cast<const uint4*>(a.q + out_row(r) * kD)[c];
+      v[k] = r < rows ? reinterpret_cast<const uint4*>(a.q + out_row(r) * kD)[c] : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int r = 32 * warp + 2 * k + (lane >> 4);
       float down = 1.0f;
       if (a.dtype == S4KV_BF16) {
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t top = 0;
+        uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+        uint32_t top = 0;   // the largest magnitude's bits, in the upper half
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fff0000u, (w[i] << 16) & 0x7fff0000u));
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const int pw = query_power(max(top & 0xffffu, top >> 16));
+        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // to 2^3 .. 2^4, for the same reason as query_power's 2^14: powers of the scores' scale stay normal numbers
+        const int e = static_cast<int>(top >> 23), pw = top == 0 || e == 255 ? 0 : min(3 + 127 - e, 126);
         const float up = power_of_two(pw);
         down = power_of_two(-pw);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
-        v = make_uint4(w[0], w[1], w[2], w[3]);
+        v[k] = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      *reinterpret_cast<uint4*>(q_tiles + (r >> 7) * kQBytes + sw128_off(r & 127, 8 * c, 128)) = v;
+      *reinterpret_cast<uint4*>(q_tiles + (r >> 7) * kQBytes + sw128_off(r & 127, 8 * c, 128)) = v[k];
       if (c == 0) sm.up[r] = down;
     }
     fence_proxy_async();
@@ -225,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
-  // kv tiles that some row sees: the sinks' [0, sa), then [jb, je)
+  // kv tiles that some row sees: the sinks' [0, sa), then [jb, je) (restored all: the sequence's range holds them)
   const int last = sm.hi;
   const int sa = why ? 0 : (min(a.form.sinks, last + 1) + kKvTile - 1) / kKvTile;
   const int jb = max(sa, sm.lo == 0x7fffffff ? sa : sm.lo / kKvTile), je = why || sm.lo == 0x7fffffff ? jb : last / kKvTile + 1;
@@ -233,213 +282,323 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
   const int i0 = static_cast<int>(static_cast<long long>(all) * z / a.splits);
   const int cnt = static_cast<int>(static_cast<long long>(all) * (z + 1) / a.splits) - i0;
   auto kv_of = [&](int i) { return i0 + i < sa ? i0 + i : jb + (i0 + i - sa); };
-  auto tile_at = [&](int i) { return (static_cast<long long>(pl.kv0) + kv_of(i)) * a.H + h; };
+  const KvRange kept = kv_range(a, m, max(T, 1));
+  auto tile_at = [&](int i) { return (static_cast<long long>(pl.kv0) + kept.at(kv_of(i))) * a.H + h; };
 
   volatile int* flag = &sm.abort;
   // Bounded: false, and the flag that ends every role's loop raised, when it runs out.
   auto wait = [&](uint64_t* bar, int parity) -> bool {
-    if (a.wait_ns > 0 && mbar_try_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
+    unsigned long long t0 = 0;
     for (unsigned it = 1; a.wait_ns > 0; ++it) {
-      if (mbar_try_wait(bar, parity)) return true;
+      if (mbar_try_wait_for(bar, parity, 20000u)) return true;
       if (*flag) return false;
-      if ((it & 15u) == 0 && static_cast<long long>(global_ns() - t0) > a.wait_ns) break;
+      if ((it & 15u) == 0) {   // (reading the timer takes longer than most waits)
+        const unsigned long long now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (static_cast<long long>(now - t0) > a.wait_ns) break;
+      }
     }
     *flag = 1;
     return false;
   };
 
-  if (warp == kLoadWarp) {
-    if (lane == 0) {
-      int sent = 0;
-      bool ok = true;
-      for (int it = 0; it < 2 * cnt; ++it) {
-        const int s = it % kBufs;
-        if (it >= kBufs) ok = wait(&sm.empty[s], (it / kBufs - 1) & 1);
-        if (!ok) break;
-        mbar_expect_tx(&sm.full[s], kTileBytes);
-        asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                         smem_u32(ring + s * kTileBytes)),
-                     "l"(a.tiles + (2 * tile_at(it >> 1) + (it & 1)) * kTileBytes), "r"(kTileBytes), "r"(smem_u32(&sm.full[s]))
-                     : "memory");
-        sent = it + 1;
+  if (warp >= kRowWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == kLoadWarp) {
+      if (lane == 0) {
+        int sent = 0;
+        bool ok = true;
+        for (int it = 0; it < 2 * cnt; ++it) {
+          const int s = it % kBufs;
+          if (it >= kBufs) ok = wait(&sm.empty[s], (it / kBufs - 1) & 1);
+          if (!ok) break;
+          mbar_expect_tx(&sm.full[s], kTileBytes);
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                           smem_u32(ring + s * kTileBytes)),
+                       "l"(a.tiles + (2 * tile_at(it >> 1) + (it & 1)) * kTileBytes), "r"(kTileBytes), "r"(smem_u32(&sm.full[s]))
+                       : "memory");
+          sent = it + 1;
+        }
+        // every copy has landed before the CTA ends
+        for (int it = max(0, sent - kBufs); it < sent; ++it) mbar_wait(&sm.full[it % kBufs], (it / kBufs) & 1, kDrainNs);
       }
-      // every copy has landed before the CTA ends
-      for (int it = max(0, sent - kBufs); it < sent; ++it) mbar_wait(&sm.full[it % kBufs], (it / kBufs) & 1, kDrainNs);
-    }
-    __syncwarp();
-  } else if (warp == kMmaWarp) {
-    if (lane == 0 && cnt > 0) {
-      const uint32_t q_s = smem_u32(q_tiles), ring_s = smem_u32(ring);
-      auto qk = [&](int s, int i) {
-        const uint32_t k_s = ring_s + ((2 * i) % kBufs) * kTileBytes;
+      __syncwarp();
+    } else if (warp == kMmaWarp) {
+      // The whole warp walks the loop, so that addresses and counters are uniform; one lane issues.
+      const uint32_t q_low = (smem_u32(q_tiles) >> 4) | kDescK, k_low = (smem_u32(ring) >> 4) | kDescK, v_low = (smem_u32(ring) >> 4) | kDescMn;
+      auto qk = [&](int s, int slot) {
+        const uint32_t b = k_low + slot * (kTileBytes >> 4), q = q_low + s * (kQBytes >> 4);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          umma_f16(tmem + 128 * s, umma_desc(q_s + s * kQBytes + (j >> 2) * 16384 + (j & 3) * 32, 1024, kSw128),
-                   umma_desc(k_s + (j >> 2) * 16384 + (j & 3) * 32, 1024, kSw128), kIdescQK, j > 0);
+        for (int j = 0; j < 8; ++j) {   // 16 channels: 32 bytes, or on to the other 64 channels
+          const uint32_t at = (j >> 2) * (16384 >> 4) + (j & 3) * (32 >> 4);
+          umma_ss(tmem + 128 * s, q + at, b + at, kIdescQK, j > 0);
+        }
         umma_commit(&sm.sfull[s]);
       };
-      auto pv = [&](int s, int i) {
-        const uint32_t v_s = ring_s + ((2 * i + 1) % kBufs) * kTileBytes;
+      auto pv = [&](int s, int slot, bool acc) {
+        const uint32_t b = v_low + slot * (kTileBytes >> 4);
 #pragma unroll
         for (int j = 0; j < 8; ++j)   // 16 tokens: 8 columns of P, 16 rows of 128 bytes
-          umma_f16_ta(tmem + 256 + 128 * s, tmem + 128 * s + 8 * j, umma_desc_mn(v_s + j * 2048, 16384), kIdescPV, i > 0 || j > 0);
+          umma_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * j, b + j * (2048 >> 4), kIdescPV, acc || j > 0);
         umma_commit(&sm.odone[s]);
       };
-      bool ok = wait(&sm.full[0], 0);
-      if (ok) {
-        tc_fence_after();
-        for (int s = 0; s < tiles; ++s) qk(s, 0);
-        umma_commit(&sm.empty[0]);
-      }
-      for (int i = 0; ok && i < cnt; ++i) {
-        const int vi = 2 * i + 1, ki = 2 * i + 2;
-        ok = wait(&sm.full[vi % kBufs], (vi / kBufs) & 1);
-        for (int s = 0; ok && s < tiles; ++s) {
-          ok = wait(&sm.pfull[s], i & 1);
-          if (!ok) break;
+      auto all_wait = [&](uint64_t* bar, int parity) -> bool { return __all_sync(0xffffffffu, wait(bar, parity)); };
+      if (cnt > 0) {
+        bool ok = all_wait(&sm.full[0], 0);
+        if (ok) {
           tc_fence_after();
-          pv(s, i);
-          if (s == tiles - 1) umma_commit(&sm.empty[vi % kBufs]);
-          if (i + 1 < cnt) {
-            if (s == 0) ok = wait(&sm.full[ki % kBufs], (ki / kBufs) & 1);
+          if (elect_one()) {
+            qk(0, 0);
+            if (tiles == 2) qk(1, 0);
+            umma_commit(&sm.empty[0]);
+          }
+          __syncwarp();
+        }
+        int slot = 0, round = 0;   // of the ring; the parity of its rounds
+        auto step = [&]() {
+          slot = slot + 1 == kBufs ? 0 : slot + 1;
+          round ^= slot == 0;
+        };
+        for (int i = 0; ok && i < cnt; ++i) {
+          const bool more = i + 1 < cnt;
+          // (the waits for copies, long there, go where the other tile's MMAs are still running)
+          step();
+          ok = all_wait(&sm.full[slot], round);              // values of tile i
+          const int vslot = slot;
+          step();
+          if (ok && more) ok = all_wait(&sm.full[slot], round);   // keys of tile i + 1
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (s >= tiles) break;
+            ok = ok && all_wait(&sm.pfull[s], i & 1);
             if (!ok) break;
-            qk(s, i + 1);
-            if (s == tiles - 1) umma_commit(&sm.empty[ki % kBufs]);
+            tc_fence_after();
+            if (elect_one()) {
+              pv(s, vslot, i > 0);
+              if (s == tiles - 1) umma_commit(&sm.empty[vslot]);
+              if (more) {
+                qk(s, slot);
+                if (s == tiles - 1) umma_commit(&sm.empty[slot]);
+              }
+            }
+            __syncwarp();
           }
         }
+        // no MMA is in flight when the CTA ends
+        if (elect_one()) umma_commit(&sm.drain);
+        __syncwarp();
+        mbar_wait(&sm.drain, 0, kDrainNs);
+        if (!ok && lane == 0) report(a.status, S4KV_ERR_DEVICE_TIMEOUT, S4KV_DEV_TIMEOUT, b);
       }
-      // no MMA is in flight when the CTA ends
-      umma_commit(&sm.drain);
-      mbar_wait(&sm.drain, 0, kDrainNs);
-      if (!ok) report(a.status, S4KV_ERR_DEVICE_TIMEOUT, S4KV_DEV_TIMEOUT, b);
-    }
-    __syncwarp();
-  } else if ((warp >> 2) < tiles) {
-    const int s = warp >> 2;
-    const uint32_t t_row = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t s_at = tmem + 128 * s + t_row, o_at = tmem + 256 + 128 * s + t_row;
-    constexpr float kLog2e = 1.4426950408889634f;
-    RowScore f;
-    const float scale = a.sm_scale * sm.up[tid];
-    f.mul = CAP ? scale / a.form.cap : scale * kLog2e;
-    f.cap2 = CAP ? a.form.cap * kLog2e : 0.0f;
-    f.slope2 = SLOPE ? a.form.slopes[h * g + (row0 + tid) % g] * kLog2e : 0.0f;
-    float mx = -INFINITY, l = 0.0f;
-    bool ok = true;
-    for (int i = 0; i < cnt; ++i) {
-      const int t0 = kv_of(i) * kKvTile;
-      const uint4 wild = *reinterpret_cast<const uint4*>(a.bad + 4 * tile_at(i));
-      ok = __all_sync(0xffffffffu, wait(&sm.sfull[s], i & 1));
-      if (!ok) break;
-      tc_fence_after();
-      float x[128];
-      {
-        uint32_t(&r)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(x);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) tmem_ld32(s_at + 32 * k, r[k]);
-        tmem_wait_ld();
-      }
-      score_form<CAP, SLOPE>(x, f, static_cast<float>(pos - t0));
-      const bool whole = t0 + kKvTile - 1 <= sp.hi && (t0 >= sp.lo || t0 + kKvTile <= a.form.sinks) && (wild.x | wild.y | wild.z | wild.w) == 0;
-      if (!__all_sync(0xffffffffu, whole)) {
-        // bits of the tokens that the row sees, 32 at a time
-        const uint32_t wilds[4] = {wild.x, wild.y, wild.z, wild.w};
-        auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int t = t0 + 32 * k;
-          // (hi may be the largest int)
-          const uint32_t seen = below(sp.hi - t >= 31 ? 32 : sp.hi - t + 1) & (~below(sp.lo - t) | below(a.form.sinks - t));
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float& y = x[32 * k + j];
-            y = (seen >> j) & 1u ? y : -INFINITY;
-          }
-          const uint32_t poison = seen & wilds[k];
-          if (poison)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if ((poison >> j) & 1u) x[32 * k + j] = __int_as_float(0x7fffffff);
-        }
-      }
-      float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int j = 0; j < 128; j += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t4[e] = fmaxf(t4[e], fmaxf(x[j + 2 * e], x[j + 2 * e + 1]));
-      float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
-      constexpr bool kRaw = !CAP && !SLOPE;   // x are still S
-      if (kRaw) top *= f.mul;
-      if (__any_sync(0xffffffffu, top > mx + kLazyP)) {
-        const float mn = top > mx + kLazyP ? top : mx;
-        const float al = mx == -INFINITY ? 0.0f : exp2_fast(mx - mn);   // (nothing so far: l and O are zeros)
-        if (i > 0) {
-          ok = __all_sync(0xffffffffu, wait(&sm.odone[s], (i - 1) & 1));
-          if (!ok) break;
-          tc_fence_after();
-          const float by = mx == mn ? 1.0f : al;
-          l *= by;
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {
-            uint32_t o[32];
-            tmem_ld32(o_at + 32 * k, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
-            tmem_st32(o_at + 32 * k, o);
-          }
-          tmem_wait_st();
-        }
-        mx = mn;
-      }
-      const float base = mx == -INFINITY ? 0.0f : mx;   // (a row that has seen nothing: every p is zero)
-      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-      const float2 mul2 = make_float2(kRaw ? f.mul : 1.0f, kRaw ? f.mul : 1.0f), base2 = make_float2(-base, -base);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t w[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          float2 y = make_float2(x[64 * k + 2 * j], x[64 * k + 2 * j + 1]);
-          y = kRaw ? __ffma2_rn(y, mul2, base2) : __fadd2_rn(y, base2);
-          y = make_float2(exp2_fast(y.x), exp2_fast(y.y));
-          sum[j & 1] = __fadd2_rn(sum[j & 1], y);
-          w[j] = pack_f16x2(y.x, y.y);
-        }
-        tmem_st32(s_at + 32 * k, w);
-      }
-      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-      tmem_wait_st();
-      tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.pfull[s]);
     }
-    // ---- the rows' output, or their part of it ----
-    if (ok && cnt > 0) ok = __all_sync(0xffffffffu, wait(&sm.odone[s], (cnt - 1) & 1));
-    tc_fence_after();
-    const bool some = ok && cnt > 0;
-    const long long item = (static_cast<long long>(gridDim.x - 1 - blockIdx.x) * a.H + h) * a.splits + z;
-    const float inv = a.splits > 1 ? 1.0f : l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
-#pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-      uint32_t o[32];
-      if (some) {
-        tmem_ld32(o_at + 32 * k, o);
-        tmem_wait_ld();
-      }
-      float y[32];
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsRow));
+    if ((warp >> 2) < tiles) {
+      const int s = warp >> 2;
+      const uint32_t t_row = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+      const uint32_t s_at = tmem + 128 * s + t_row, o_at = tmem + 256 + 128 * s + t_row;
+      constexpr float kLog2e = 1.4426950408889634f;
+      RowScore f;
+      const float scale = a.sm_scale * sm.up[tid];
+      f.mul = CAP ? scale / a.form.cap : scale * kLog2e;
+      f.cap2 = CAP ? a.form.cap * kLog2e : 0.0f;
+      f.slope2 = SLOPE ? a.form.slopes[h * g + (row0 + tid) % g] * kLog2e : 0.0f;
+      NearCap near;
+      {
+        float by = f.cap2 * f.mul;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) y[j] = some ? __uint_as_float(o[j]) * inv : 0.0f;
-      if (tid < rows) {
-        if (a.splits == 1) store32(a.out, a.out_dtype, out_row(tid), 32 * k, y);
-        else if (some) store32(part_rows(a, item), S4KV_F32, tid, 32 * k, y);
+        for (int k = 0; k < kNearCoefs; ++k, by *= f.mul * f.mul) near.c[k] = near_coef(k) * by;
       }
-    }
-    if (a.splits > 1 && tid < rows) {
-      float* ml = part_ml(a, item) + 2 * tid;
-      ml[0] = some ? mx : -INFINITY;
-      ml[1] = some ? l : 0.0f;
+      float mx = -INFINITY, l = 0.0f;
+      bool ok = true;
+      auto wild_of = [&](int i) { return *reinterpret_cast<const uint4*>(a.bad + 4 * tile_at(i)); };
+      uint4 next = cnt > 0 ? wild_of(0) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < cnt; ++i) {
+        const int t0 = kv_of(i) * kKvTile;
+        const uint4 wild = next;
+        if (i + 1 < cnt) next = wild_of(i + 1);
+        const bool whole = __all_sync(0xffffffffu, t0 + kKvTile - 1 <= sp.hi && (t0 >= sp.lo || t0 + kKvTile <= a.form.sinks) &&
+                                                       (wild.x | wild.y | wild.z | wild.w) == 0);
+        ok = __all_sync(0xffffffffu, wait(&sm.sfull[s], i & 1));
+        if (!ok) break;
+        tc_fence_after();
+        float x[128];
+        {
+          uint32_t(&r)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(x);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) tmem_ld32(s_at + 32 * k, r[k]);
+          tmem_wait_ld();
+        }
+        auto largest = [&]() {
+          float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int j = 0; j < 128; j += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], x[j + 2 * e], x[j + 2 * e + 1]);
+          return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+        };
+        // Scores stay S until their exponentials where nothing has to be done to each before (kRaw): no
+        // slopes, and with a cap, every score near zero against it and seen.
+        bool raw = !SLOPE;
+        float top = 0.0f;   // in log2 units
+        if constexpr (CAP) {
+          float t4[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
+#pragma unroll
+          for (int j = 0; j < 128; j += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t4[e] = min3(t4[e], x[j + 2 * e], x[j + 2 * e + 1]);
+          const float least = fminf(fminf(t4[0], t4[1]), fminf(t4[2], t4[3]));
+          top = largest();
+          const float far = fmaxf(top, -least);
+          // (the last coefficient has the seventh power of f.mul: a normal number, or it is not used)
+          const bool near_zero = __all_sync(0xffffffffu, far * f.mul <= kNearCap && fabsf(near.c[kNearCoefs - 1]) > 1e-36f);
+          raw = raw && whole && near_zero;
+          if (raw) top = near(top);
+          else through_cap(x, f, near, near_zero, far);
+        }
+        if constexpr (SLOPE) {
+          const float rel = static_cast<float>(pos - t0);
+          const float in = CAP ? 1.0f : f.mul;
+          if (__all_sync(0xffffffffu, rel >= 127.0f)) {   // every token before the query: the distance falls along the row
+            const float2 in2 = make_float2(in, in), by2 = make_float2(f.slope2, f.slope2), at2 = make_float2(-f.slope2 * rel, -f.slope2 * rel);
+#pragma unroll
+            for (int j = 0; j < 128; j += 2) {
+              const float2 bias = __ffma2_rn(by2, make_float2(static_cast<float>(j), static_cast<float>(j + 1)), at2);
+              const float2 y = CAP ? __fadd2_rn(make_float2(x[j], x[j + 1]), bias) : __ffma2_rn(make_float2(x[j], x[j + 1]), in2, bias);
+              x[j] = y.x;
+              x[j + 1] = y.y;
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 128; ++j) x[j] = fmaf(-f.slope2, fabsf(static_cast<float>(j) - rel), x[j] * in);
+          }
+        }
+        if (!whole) {
+          // bits of the tokens that the row sees, 32 at a time
+          const uint32_t wilds[4] = {wild.x, wild.y, wild.z, wild.w};
+          auto below = [](int n) -> uint32_t { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int t = t0 + 32 * k;
+            // (hi may be the largest int)
+            const uint32_t seen = below(sp.hi - t >= 31 ? 32 : sp.hi - t + 1) & (~below(sp.lo - t) | below(a.form.sinks - t));
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              float& y = x[32 * k + j];
+              y = (seen >> j) & 1u ? y : -INFINITY;
+            }
+            const uint32_t poison = seen & wilds[k];
+            if (poison)
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if ((poison >> j) & 1u) x[32 * k + j] = __int_as_float(0x7fffffff);
+          }
+        }
+        if (!CAP || !raw) top = largest();
+        if (!CAP && !SLOPE) top *= f.mul;
+        if (__any_sync(0xffffffffu, top > mx + kLazyP)) {
+          const float mn = top > mx + kLazyP ? top : mx;
+          const float by = mx == mn ? 1.0f : mx == -INFINITY ? 0.0f : exp2_fast(mx - mn);   // (nothing so far: l and O are zeros)
+          if (i > 0) {
+            ok = __all_sync(0xffffffffu, wait(&sm.odone[s], (i - 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            l *= by;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              uint32_t o[32];
+              tmem_ld32(o_at + 32 * k, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * by);
+              tmem_st32(o_at + 32 * k, o);
+            }
+            tmem_wait_st();
+          }
+          mx = mn;
+        }
+        const float base = mx == -INFINITY ? 0.0f : mx;   // (a row that has seen nothing: every p is zero)
+        float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        auto exponentials = [&](auto how) {   // how: 0 of x - base, 1 of x mul - base, 2 of the cap near zero - base
+          constexpr int kHow = decltype(how)::value;
+          const float2 base2 = make_float2(-base, -base), mul2 = make_float2(f.mul, f.mul);
+          auto pair = [&](int j) -> uint32_t {
+            float2 y = make_float2(x[2 * j], x[2 * j + 1]);
+            if (kHow == 0) y = __fadd2_rn(y, base2);
+            if (kHow == 1) y = __ffma2_rn(y, mul2, base2);
+            if (kHow == 2) y = __ffma2_rn(y, near.inner(y), base2);
+            y = make_float2(exp2_fast(y.x), exp2_fast(y.y));
+            sum[j & 1] = __fadd2_rn(sum[j & 1], y);
+            return pack_f16x2(y.x, y.y);
+          };
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = pair(32 * k + j);
+            tmem_st32(s_at + 32 * k, w);
+          }
+        };
+        if (CAP && !SLOPE && raw) exponentials(std::integral_constant<int, 2>{});
+        else exponentials(std::integral_constant<int, CAP || SLOPE ? 0 : 1>{});
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.pfull[s]);
+      }
+      // ---- the rows' output, or their part of it ----
+      if (ok && cnt > 0) ok = __all_sync(0xffffffffu, wait(&sm.odone[s], (cnt - 1) & 1));
+      tc_fence_after();
+      const bool some = ok && cnt > 0;
+      const long long item = (static_cast<long long>(gridDim.x - 1 - blockIdx.x) * a.H + h) * a.splits + z;
+      const float inv = a.splits > 1 ? 1.0f : l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
+      // Through the queries' place in shared memory (nothing reads them any more), so that a warp writes whole
+      // rows: 16 chunks of 16 bytes, chunk c of row r at c xor (r mod 16). 32 bits: in two goes.
+      char* stage = q_tiles + s * kQBytes + (warp & 3) * 32 * 256;
+      const bool f32 = a.splits > 1 || a.out_dtype == S4KV_F32;
+      char* to = reinterpret_cast<char*>(a.splits > 1 ? part_rows(a, item) : a.out);
+#pragma unroll 1
+      for (int go = 0; go < (f32 ? 2 : 1); ++go) {
+#pragma unroll 1
+        for (int k = 0; k < (f32 ? 2 : 4); ++k) {   // 32 channels
+          uint32_t o[32];
+          if (some) {
+            tmem_ld32(o_at + 64 * go + 32 * k, o);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = some ? __float_as_uint(__uint_as_float(o[j]) * inv) : 0u;
+          auto put = [&](int c, uint4 w) { *reinterpret_cast<uint4*>(stage + lane * 256 + ((c ^ (lane & 15)) << 4)) = w; };
+          if (f32) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c) put(8 * k + c, make_uint4(o[4 * c], o[4 * c + 1], o[4 * c + 2], o[4 * c + 3]));
+          } else {
+            auto two = [&](int j) { return pack_in_dtype(__uint_as_float(o[j]), __uint_as_float(o[j + 1]), a.out_dtype); };
+#pragma unroll
+            for (int c = 0; c < 4; ++c) put(4 * k + c, make_uint4(two(8 * c), two(8 * c + 2), two(8 * c + 4), two(8 * c + 6)));
+          }
+        }
+        __syncwarp();
+        if (a.splits == 1 || some) {
+#pragma unroll 4
+          for (int k = 0; k < 16; ++k) {
+            const int r = 2 * k + (lane >> 4), c = lane & 15, row = tid - lane + r;
+            if (row < rows) {
+              const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 256 + ((c ^ (r & 15)) << 4));
+              const long long at = a.splits > 1 ? row : out_row(row);
+              reinterpret_cast<uint4*>(to + at * kD * (f32 ? 4 : 2) + 256 * go)[c] = w;
+            }
+          }
+        }
+        __syncwarp();
+      }
+      if (a.splits > 1 && tid < rows) {
+        float* ml = part_ml(a, item) + 2 * tid;
+        ml[0] = some ? mx : -INFINITY;
+        ml[1] = some ? l : 0.0f;
+      }
     }
   }
   tc_fence_before();
@@ -458,36 +617,50 @@ __global__ void __launch_bounds__(256) prompt_join_kernel(PromptArgs a) {
   const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int cu0 = a.cu_q[pl.b], m = a.cu_q[pl.b + 1] - cu0;
   const long long item0 = (static_cast<long long>(blockIdx.x) * a.H + h) * a.splits;
+  const int r0 = 32 * blockIdx.z + 4 * warp;
+  const long long at0 = static_cast<long long>(pl.tile) * kQRows + r0, left = static_cast<long long>(m) * a.g - at0;
+  if (left <= 0) return;
+  const int n = left < 4 ? static_cast<int>(left) : 4;
+  float w[4], inv[4];   // lane = part: its weight in row k; 1 / the row's sum
+#pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int r = 32 * blockIdx.z + 4 * warp + k;
-    const long long at = static_cast<long long>(pl.tile) * kQRows + r;
-    if (at >= static_cast<long long>(m) * a.g) return;
     float mi = -INFINITY, li = 0.0f;
-    if (lane < a.splits) {
-      const float* ml = part_ml(a, item0 + lane) + 2 * r;
-      mi = __ldcg(ml);
-      li = __ldcg(ml + 1);
+    if (k < n && lane < a.splits) {
+      const float2 ml = __ldcg(reinterpret_cast<const float2*>(part_ml(a, item0 + lane)) + r0 + k);
+      mi = ml.x;
+      li = ml.y;
     }
     const float M = warp_max(mi);
     // a part that saw nothing has l = 0 (and may have no rows at all); one with a NaN keeps it
-    const float w = li == 0.0f ? 0.0f : M == -INFINITY ? 1.0f : exp2_fast(mi - M);
-    const float L = warp_sum(w * li);
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int s = 0; s < a.splits; ++s) {
-      const float ws = __shfl_sync(0xffffffffu, w, s), ls = __shfl_sync(0xffffffffu, li, s);
-      if (ls == 0.0f) continue;
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(part_rows(a, item0 + s) + r * kD) + lane);
-      o = make_float4(fmaf(ws, y.x, o.x), fmaf(ws, y.y, o.y), fmaf(ws, y.z, o.z), fmaf(ws, y.w, o.w));
+    w[k] = li == 0.0f ? 0.0f : M == -INFINITY ? 1.0f : exp2_fast(mi - M);
+    const float L = warp_sum(w[k] * li);
+    if (li == 0.0f) w[k] = -1.0f;   // nothing to read
+    inv[k] = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
+  }
+  float4 o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int s = 0; s < a.splits; ++s)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float ws = __shfl_sync(0xffffffffu, w[k], s);
+      if (ws == -1.0f) continue;
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(part_rows(a, item0 + s) + (r0 + k) * kD) + lane);
+      o[k] = make_float4(fmaf(ws, y.x, o[k].x), fmaf(ws, y.y, o[k].y), fmaf(ws, y.z, o[k].z), fmaf(ws, y.w, o[k].w));
     }
-    const float inv = L > 0.0f ? 1.0f / L : L == L ? 0.0f : L;
-    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (k >= n) break;
+    const float4 y = make_float4(o[k].x * inv[k], o[k].y * inv[k], o[k].z * inv[k], o[k].w * inv[k]);
+    const long long at = at0 + k;
     const int i = static_cast<int>(at / a.g);
     const long long row = (static_cast<long long>(cu0) + i) * a.Hq + h * a.g + (at - static_cast<long long>(i) * a.g);
     if (a.out_dtype == S4KV_F32) {
-      reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kD)[lane] = o;
+      reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kD)[lane] = y;
     } else {
       reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * kD)[lane] =
-          make_uint2(pack_in_dtype(o.x, o.y, a.out_dtype), pack_in_dtype(o.z, o.w, a.out_dtype));
+          make_uint2(pack_in_dtype(y.x, y.y, a.out_dtype), pack_in_dtype(y.z, y.w, a.out_dtype));
     }
   }
 }

@@ -31,13 +31,14 @@ struct PromptArgs {
   const float* fp8_scale;
   ScoreForm form;
   char* tiles;
-  uint32_t* bad;            // [kv tile][H][4]
+  uint32_t* bad;            // [kv tile][H][4]: a bit a token
   float* part;              // [q tile][H][split][256][128], then [q tile][H][split][256][2]
   long long kring_slot, kring_head, vring_slot, vring_head;
   long long wait_ns;
   float sm_scale;
   int bt_stride, n, num_q, Hq, H, g, R, num_pages, max_slots, dtype, out_dtype, bits, max_seq_len;
   int kv_tiles, q_tiles;    // at most, of the call
+  int kv_grid;              // kv tiles that a window leaves, at most
   int splits;
 };
 
@@ -51,12 +52,27 @@ namespace {
 __device__ __forceinline__ int q_tiles_of(const PromptArgs& a, int m) {
   return m > 0 ? static_cast<int>((static_cast<long long>(m) * a.g + kQRows - 1) / kQRows) : 0;
 }
+// The kv tiles of a sequence that some query of its chunk may see: the sinks' [0, sinks) and [first, end).
+struct KvRange {
+  int sinks, first, end;
+  __device__ __forceinline__ int count() const { return sinks + end - first; }
+  __device__ __forceinline__ int at(int j) const { return j < sinks ? j : j - (first - sinks); }   // place of tile j in the workspace
+  __device__ __forceinline__ int tile(int i) const { return i < sinks ? i : first + i - sinks; }   // and the other way
+};
+__device__ __forceinline__ KvRange kv_range(const PromptArgs& a, int m, int T) {
+  KvRange r;
+  r.end = (T - 1) / kKvTile + 1;
+  r.sinks = min(a.form.sinks / kKvTile + (a.form.sinks % kKvTile != 0), r.end);
+  r.first = max(r.sinks, max(0, T - m - a.form.window + 1) / kKvTile);
+  return r;
+}
 __device__ __forceinline__ int kv_tiles_of(const PromptArgs& a, int m, int T) {
-  return m > 0 && T >= m && T <= a.max_seq_len ? (T - 1) / kKvTile + 1 : 0;
+  return m > 0 && T >= m && T <= a.max_seq_len ? kv_range(a, m, T).count() : 0;
 }
 
 struct Place {
-  int b, tile, kv0;         // sequence, tile within it, its first kv tile of the call
+  int b, tile, kv0;         // sequence, tile within it (of kv tiles: place among those it has), its first kv tile of the call
+  int cu0, m, T;            // its first row, its queries, its length
 };
 enum { kFound = 0, kNowhere = 1, kMalformed = 2 };
 
@@ -75,14 +91,17 @@ __device__ int find_tile(const PromptArgs& a, int idx, Place& place) {
   }
   for (int base = 0; base < a.n; base += THREADS) {
     const int b = base + tid;
-    int qt = 0, kt = 0;
+    int qt = 0, kt = 0, c0 = 0, m = 0, T = 0;
     if (b < a.n) {
-      const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], T = a.seq_lens[b];
+      const int c1 = a.cu_q[b + 1];
+      c0 = a.cu_q[b];
+      T = a.seq_lens[b];
+      m = c1 - c0;
       if (c0 < 0 || c1 < c0 || c1 > a.num_q) {
         bad = 1;
       } else {
-        qt = q_tiles_of(a, c1 - c0);
-        kt = kv_tiles_of(a, c1 - c0, T);
+        qt = q_tiles_of(a, m);
+        kt = kv_tiles_of(a, m, T);
       }
     }
     int q = qt, k = kt;
@@ -111,7 +130,7 @@ __device__ int find_tile(const PromptArgs& a, int idx, Place& place) {
     q0 += q - qt;
     k0 += k - kt;
     const int first = BY_Q ? q0 : k0, count = BY_Q ? qt : kt;
-    if (idx >= first && idx - first < count) found = Place{b, idx - first, k0};
+    if (idx >= first && idx - first < count) found = Place{b, idx - first, k0, c0, m, T};
     __syncthreads();
   }
   if (__syncthreads_or(bad)) return kMalformed;
@@ -120,7 +139,8 @@ __device__ int find_tile(const PromptArgs& a, int idx, Place& place) {
 }
 
 // Why a sequence's part of the call cannot be done, 0 if it can; `arg` goes with it.
-__device__ __forceinline__ int refused(const PromptArgs& a, const Place& p, int m, int T, int slot, int h, int& arg) {
+__device__ __forceinline__ int refused(const PromptArgs& a, const Place& p, int slot, int h, int& arg) {
+  const int m = p.m, T = p.T;
   arg = p.b;
   if (slot < 0 || slot >= a.max_slots) {
     arg = slot;

@@ -10,9 +10,9 @@
 // that is not finite (then) is stored as zeros where it is not and gets a bit, so that queries which
 // do not see it never meet it.
 //
-// One CTA a tile: warps 0 .. 3 a key group of 32 tokens each, warps 4 .. 7 the values of
-// 32 tokens. Bound by the bytes it writes, most of which stay in the L2 cache for the
-// attention kernel.
+// A CTA takes one tensor of a tile, a warp a page of it (of a key group on KIVI pages, whose metadata
+// lie in two pages' records). Bound by the bytes it writes, most of which stay in the L2 cache
+// for the attention kernel.
 
 #include "s4kv_prompt.cuh"
 #include "s4kv_restore.cuh"
@@ -42,7 +42,7 @@ struct TileRows {
 #pragma unroll
       for (int i = 0; i < 4; ++i) wild = wild || (w[i] & 0x7c00u) == 0x7c00u || (w[i] & 0x7c000000u) == 0x7c000000u;
       if (wild) {
-        *bits |= 1u << (r & 31);
+        *bits |= 1u << (r & (kP - 1));
         w[0] = w[1] = w[2] = w[3] = 0u;
       }
     }
@@ -63,21 +63,18 @@ __global__ void __launch_bounds__(kThreads, 3) tiles_kernel(PromptArgs a) {
   stream_wait();
   Place p;
   const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const bool values = blockIdx.z;
   const int where = find_tile<kThreads, false>(a, blockIdx.x, p);
-  if (where == kMalformed && blockIdx.x == 0 && h == 0 && threadIdx.x == 0)
+  if (where == kMalformed && blockIdx.x == 0 && h == 0 && !values && threadIdx.x == 0)
     report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_CU, a.n);
   if (where != kFound) return;
-  const int m = a.cu_q[p.b + 1] - a.cu_q[p.b], T = a.seq_lens[p.b], slot = a.slot_ids ? a.slot_ids[p.b] : p.b;
+  const int m = p.m, T = p.T, slot = a.slot_ids ? a.slot_ids[p.b] : p.b;
   int arg;
-  if (refused(a, p, m, T, slot, h, arg)) return;   // (the attention kernel says so)
-  const int t_tile = p.tile * kKvTile;
-  // a tile that lies between the sinks and every query's window is not looked at
-  if (t_tile + kKvTile <= T - m - a.form.window + 1 && t_tile >= a.form.sinks) return;
-  const bool values = warp >= 4;
-  const int w = warp & 3, t0 = t_tile + 32 * w;   // this warp's 32 tokens
+  if (refused(a, p, slot, h, arg)) return;   // (the attention kernel says so)
+  const int tp = kv_range(a, m, T).tile(p.tile) * kKvTile + kP * warp;   // this warp's 16 tokens
   const long long at = (static_cast<long long>(p.kv0) + p.tile) * a.H + h;
   uint32_t bits = 0;
-  const TileRows rows{a.tiles + (2 * at + values) * kTileBytes, 32 * w, values ? &bits : nullptr};
+  const TileRows rows{a.tiles + (2 * at + values) * kTileBytes, kP * warp, values ? &bits : nullptr};
   const int* bt = a.block_table + static_cast<long long>(p.b) * a.bt_stride;
   const int Tk = FMT == 8 ? T : FMT == kI8 ? T / kP * kP : T & ~(kG - 1);
   const int Tv = FMT == 8 ? T : FMT == kI8 ? Tk : max(0, T - a.R);
@@ -90,32 +87,30 @@ __global__ void __launch_bounds__(kThreads, 3) tiles_kernel(PromptArgs a) {
     if (lane == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, pp);
     return nullptr;
   };
-  if (!kByte<FMT> && !values && t0 + kG <= Tk) {
-    if constexpr (!kByte<FMT>) {   // a whole key group: both pages' records hold its metadata
-      const char* r0 = record(t0 / kP);
-      const char* r1 = record(t0 / kP + 1);
-      if (r0 && r1) put_key_group<FMT>(r0, r1, 0, kG, rows);
-      else rows.clear(0, kG);
-    }
-  } else {
-#pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      const int tp = t0 + half * kP, end = min(max(T - tp, 0), kP);          // tokens [0, end) of this page are there
-      const int held = min(max(quant - tp, 0), end);                       // [0, held) in its record
-      const TileRows here{rows.tile, rows.r0 + half * kP, rows.bits};
-      if (held > 0) {
-        const char* rec = record(tp / kP);
-        if (!rec) here.clear(0, held);
-        else if (values) put_values<FMT>(a.fp8_scale + a.H + h, rec, 0, held, here);
-        else if constexpr (kByte<FMT>) put_keys<FMT>(a.fp8_scale + h, rec, 0, held, here);
+  const int end = min(max(T - tp, 0), kP);            // tokens [0, end) of this page are there
+  const int held = min(max(quant - tp, 0), end);    // [0, held) in its record
+  if (held > 0) {
+    const int page = tp / kP;
+    if (!kByte<FMT> && !values) {
+      if constexpr (!kByte<FMT>) {   // half of a key group
+        const int odd = page & 1;
+        const char* r0 = record(page & ~1);
+        const char* r1 = record(page | 1);
+        if (r0 && r1) put_key_group<FMT>(r0, r1, kP * odd, kP * odd + kP, TileRows{rows.tile, rows.r0 - kP * odd, nullptr});
+        else rows.clear(0, kP);
       }
-      if (FMT != 8 && end > held) put_ring(ring, mod, tp, held, end, a.dtype, here);
-      here.clear(end, kP);   // behind the last token: zeros, which a probability of zero leaves alone
+    } else {
+      const char* rec = record(page);
+      if (!rec) rows.clear(0, held);
+      else if (values) put_values<FMT>(a.fp8_scale + a.H + h, rec, 0, held, rows);
+      else if constexpr (kByte<FMT>) put_keys<FMT>(a.fp8_scale + h, rec, 0, held, rows);
     }
   }
+  if (FMT != 8 && end > held) put_ring(ring, mod, tp, held, end, a.dtype, rows);
+  rows.clear(end, kP);   // behind the last token: zeros, which a probability of zero leaves alone
   if (values) {
     bits = __reduce_or_sync(0xffffffffu, bits);
-    if (lane == 0) a.bad[4 * at + w] = bits;
+    if (lane == 0) reinterpret_cast<uint16_t*>(a.bad + 4 * at)[warp] = static_cast<uint16_t>(bits);
   }
 }
 
@@ -124,7 +119,7 @@ cudaError_t run(const PromptArgs& a, cudaStream_t st) {
   void (*f)(PromptArgs) = tiles_kernel<FMT>;
   const cudaError_t c = prefer_max_shared(reinterpret_cast<const void*>(f));
   if (c != cudaSuccess) return c;
-  return launch_behind(f, dim3(static_cast<unsigned>(a.kv_tiles), static_cast<unsigned>(a.H)), dim3(kThreads), 0, st, a);
+  return launch_behind(f, dim3(static_cast<unsigned>(a.kv_grid), static_cast<unsigned>(a.H), 2), dim3(kThreads), 0, st, a);
 }
 
 }  // namespace
