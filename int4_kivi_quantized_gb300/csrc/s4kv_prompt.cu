@@ -120,15 +120,8 @@ struct RowScore {
   float slope2;    // slope log2(e)
 };
 
-// tanh(x) = x P(x^2) for |x| <= kNearCap, where the scores of a model trained with a cap are: four
-// coefficients, off by 5.5e-7 relative, instead of the seven that |x| <= 1 takes.
-constexpr float kNearCap = 0.5f;
-constexpr int kNearCoefs = 4;
-__host__ __device__ constexpr float near_coef(int i) {
-  constexpr float c[kNearCoefs] = {0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.04440222680568695f};
-  return c[i];
-}
-// The same from S to log2 units: S Q(S^2) with Q's coefficients at hand per row.
+// The cap of a score near zero against it (s4kv_score.cuh), from S to log2 units: S Q(S^2) with Q's
+// coefficients at hand per row.
 struct NearCap {
   float c[kNearCoefs];
   __device__ __forceinline__ float2 inner(float2 s) const {   // Q(S^2)
@@ -140,8 +133,8 @@ struct NearCap {
   __device__ __forceinline__ float operator()(float s) const { return s * inner(make_float2(s, s)).x; }
 };
 
-// x from S to capped scores in log2 units. `top`: the row's largest |S|.
-__device__ __forceinline__ void through_cap(float (&x)[128], const RowScore& f, const NearCap& near, bool near_zero, float top) {
+// x from S to capped scores in log2 units.
+__device__ __forceinline__ void through_cap(float (&x)[128], const RowScore& f, const NearCap& near, bool near_zero) {
   if (near_zero) {
 #pragma unroll
     for (int i = 0; i < 128; i += 2) {
@@ -149,26 +142,10 @@ __device__ __forceinline__ void through_cap(float (&x)[128], const RowScore& f, 
       x[i] = y.x;
       x[i + 1] = y.y;
     }
-  } else if (__all_sync(0xffffffffu, top * f.mul <= 1.0f)) {
-    const float2 mul2 = make_float2(f.mul, f.mul), cap2 = make_float2(f.cap2, f.cap2);
+  } else {
+    const float by = f.mul * 2.8853900817779268f;   // 2 log2(e)
 #pragma unroll
-    for (int i = 0; i < 128; i += 2) {
-      const float2 u = __fmul2_rn(make_float2(x[i], x[i + 1]), mul2), w = __fmul2_rn(u, u);
-      float2 p = make_float2(tanh_coef(6), tanh_coef(6));
-#pragma unroll
-      for (int k = 5; k >= 0; --k) p = __ffma2_rn(p, w, make_float2(tanh_coef(k), tanh_coef(k)));
-      p = __fmul2_rn(__fmul2_rn(u, cap2), p);
-      x[i] = p.x;
-      x[i + 1] = p.y;
-    }
-  } else {   // cap - 2 cap / (1 + exp(2 x)): off by 2^-22 of the cap, which the largest scores here pass
-    const float by = f.mul * 2.8853900817779268f, down = -2.0f * f.cap2;
-#pragma unroll
-    for (int i = 0; i < 128; ++i) {
-      float r;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + exp2_fast(x[i] * by)));
-      x[i] = fmaf(down, r, f.cap2);
-    }
+    for (int i = 0; i < 128; ++i) x[i] = far_cap(x[i], by, f.cap2);
   }
 }
 
@@ -455,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
           const bool near_zero = __all_sync(0xffffffffu, far * f.mul <= kNearCap && fabsf(near.c[kNearCoefs - 1]) > 1e-36f);
           raw = raw && whole && near_zero;
           if (raw) top = near(top);
-          else through_cap(x, f, near, near_zero, far);
+          else through_cap(x, f, near, near_zero);
         }
         if constexpr (SLOPE) {
           const float rel = static_cast<float>(pos - t0);

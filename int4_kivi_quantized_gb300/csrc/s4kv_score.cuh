@@ -28,11 +28,15 @@ struct ScoredArgs : WindowArgs {
 };
 cudaError_t launch_scored(const ScoredArgs& a, int num_sms, cudaStream_t st);
 
-// tanh(x) = x P(x^2) for |x| <= 1, P the polynomial of least relative error on [0, 1] (a
-// weighted least-squares fit, 5.0e-8 in exact arithmetic, 1.6e-7 evaluated in binary32).
-__host__ __device__ constexpr float tanh_coef(int i) {
-  constexpr float c[7] = {0.9999999403953552f, -0.33332839608192444f, 0.13325203955173492f, -0.05345702916383743f,
-                          0.020289979875087738f, -0.006203378550708294f, 0.0010410223621875048f};
+// Capping scores. Those of a model that was trained with a cap lie well within it: for |x| <= kNearCap
+// tanh(x) = x P(x^2), P the cubic of least relative error there (a weighted least-squares fit,
+// 5.5e-7). Beyond, tanh(x) = 1 - 2 / (1 + exp(2 x)), whose exponential and reciprocal are off by
+// 2^-22 or so relative: 2^-22 of the cap in a score, for scores of half of it and more (and what
+// shares a warp's step with them). tanh.approx (2^-11 relative) would move a score of 50 by 0.02.
+constexpr float kNearCap = 0.5f;
+constexpr int kNearCoefs = 4;
+__host__ __device__ constexpr float near_coef(int i) {
+  constexpr float c[kNearCoefs] = {0.999999463558197f, -0.33326318860054016f, 0.13190296292304993f, -0.04440222680568695f};
   return c[i];
 }
 
@@ -54,18 +58,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// tanh(x) of any x. Beyond |x| = 1 as (1 - e) / (1 + e) with e = exp(-2 |x|) <= 0.14, which
-// loses nothing there; ex2 and the reciprocal are off by 2^-22 or so relative. A tanh.approx
-// (2^-11 relative) would move a score near a cap of 50 by 0.02.
-__device__ __forceinline__ float tanh_any(float x) {
-  const float w = x * x;
-  float p = tanh_coef(6);
-#pragma unroll
-  for (int i = 5; i >= 0; --i) p = fmaf(p, w, tanh_coef(i));
-  const float e = exp2_fast(fabsf(x) * -2.8853900817779268f);   // -2 log2(e)
-  const float far = copysignf(__fdividef(1.0f - e, 1.0f + e), x);
-  return fabsf(x) <= 1.0f ? x * p : far;                       // (NaN: far, which is NaN)
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
+// cap tanh(x) of any x: `by` times the score is 2 x log2(e). NaN stays NaN.
+__device__ __forceinline__ float far_cap(float score, float by, float cap) { return fmaf(-2.0f * cap, rcp_fast(1.0f + exp2_fast(score * by)), cap); }
 
 // The tokens that the query at position p of a sequence of T tokens sees; `at` is its place in
 // `first`. No token at all where lo > hi (and no sink is that early).

@@ -151,36 +151,38 @@ __device__ __forceinline__ bool visible_block(int n, int pos, const Cut& cut) {
   }
 }
 
-// Scores z in log2 units through the form: capped, less slope2 |pos - t| with t(i) the token of
-// z[i]. Called by the whole warp. The polynomial alone serves scores up to the cap, which is
-// what they are in earnest; a warp with a larger one takes both (tanh_any).
-template <int N, class TOKEN>
-__device__ __forceinline__ void through_form(float (&z)[N], const ScoredArgs& a, float slope2, int pos, TOKEN t) {
+// Scores z in log2 units through the form: capped, less slope2 |rel - on(i)|, rel the query's position
+// less a token, on(i) how far behind that one z[i]'s token is. Called by the whole warp.
+__device__ __forceinline__ float lane_token(int x) { return (x & 1) + 8.0f * (x >> 1); }   // of a lane's four tokens
+template <int N, class ON>
+__device__ __forceinline__ void through_form(float (&z)[N], const ScoredArgs& a, float slope2, int rel, ON on) {
   static_assert(N % 2 == 0, "scores in pairs");
   if (a.cap2 > 0.0f) {
     float top = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) top = fmaxf(top, fabsf(z[i]));
-    if (__all_sync(0xffffffffu, top <= a.cap2)) {
+    if (__all_sync(0xffffffffu, top <= kNearCap * a.cap2)) {
       const float2 by = make_float2(a.icap2, a.icap2);
 #pragma unroll
       for (int i = 0; i < N; i += 2) {
         const float2 x = make_float2(z[i], z[i + 1]), u = __fmul2_rn(x, by), w = __fmul2_rn(u, u);
-        float2 p = make_float2(tanh_coef(6), tanh_coef(6));
+        float2 p = make_float2(near_coef(kNearCoefs - 1), near_coef(kNearCoefs - 1));
 #pragma unroll
-        for (int k = 5; k >= 0; --k) p = __ffma2_rn(p, w, make_float2(tanh_coef(k), tanh_coef(k)));
+        for (int k = kNearCoefs - 2; k >= 0; --k) p = __ffma2_rn(p, w, make_float2(near_coef(k), near_coef(k)));
         p = __fmul2_rn(x, p);
         z[i] = p.x;
         z[i + 1] = p.y;
       }
     } else {
+      const float by = a.icap2 * 2.8853900817779268f;   // 2 log2(e)
 #pragma unroll
-      for (int i = 0; i < N; ++i) z[i] = a.cap2 * tanh_any(z[i] * a.icap2);
+      for (int i = 0; i < N; ++i) z[i] = far_cap(z[i], by, a.cap2);
     }
   }
   if (a.score.slopes) {
+    const float from = static_cast<float>(rel);
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = fmaf(-slope2, fabsf(static_cast<float>(pos - t(i))), z[i]);
+    for (int i = 0; i < N; ++i) z[i] = fmaf(-slope2, fabsf(from - on(i)), z[i]);
   }
 }
 
@@ -420,7 +422,7 @@ __device__ __forceinline__ void byte_block(const Args<SC>& args, const char* rec
   if constexpr (SC) {
 #pragma unroll
     for (int c = 0; c < CT; ++c)
-      through_form(z[c], args, slope2[8 * c + (lane >> 2)], pos[c], [&](int x) { return cut.tok0 + 2 * ti + (x & 1) + 8 * (x >> 1); });
+      through_form(z[c], args, slope2[8 * c + (lane >> 2)], pos[c] - cut.tok0 - 2 * ti, lane_token);
   }
   if (kMask) {
 #pragma unroll
@@ -619,7 +621,7 @@ __device__ __forceinline__ void ring_block(const Args<SC>& args, const uint16_t*
       z[c][2] = s1[2 * c] * scale;
       z[c][3] = s1[2 * c + 1] * scale;
       if constexpr (SC)
-        through_form(z[c], args, slope2[8 * c + gi], pos[c], [&](int x) { return cut.tok0 + 2 * ti + (x & 1) + 8 * (x >> 1); });
+        through_form(z[c], args, slope2[8 * c + gi], pos[c] - cut.tok0 - 2 * ti, lane_token);
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int t = cut.tok0 + 2 * ti + (x & 1) + 8 * (x >> 1);
@@ -692,10 +694,10 @@ __device__ __forceinline__ void ring_block(const Args<SC>& args, const uint16_t*
 // rows. The scores are then the operand of P V already: no pass through shared
 // memory. (m, l): state of column gi; s.o and s.bias as the decode kernel has them
 // (o at the powers of two that mma_unscale removes).
-// SC: the block's first token tok0, the column's position and slope.
+// SC: rel, the column's position less the block's first token, and its slope.
 template <int BITS, bool SC>
 __device__ __forceinline__ void kivi_block(const Args<SC>& args, const char* stage, MmaState& s, float& m, float& l,
-                                           const float (&q)[32], float scale, int tok0, int pos, float slope2) {
+                                           const float (&q)[32], float scale, int rel, float slope2) {
   using F = Rec<BITS>;
   constexpr int RS = kRecStrideB<BITS>;
   const int lane = threadIdx.x & 31, ti = lane & 3;
@@ -754,7 +756,7 @@ __device__ __forceinline__ void kivi_block(const Args<SC>& args, const char* sta
   if constexpr (SC) {
 #pragma unroll
     for (int p = 0; p < 2; ++p)
-      through_form(z[p], args, slope2, pos, [&](int x) { return tok0 + 16 * p + 2 * ti + (x & 1) + 8 * (x >> 1); });
+      through_form(z[p], args, slope2, rel - 16 * p - 2 * ti, lane_token);
   }
   float mx = fmaxf(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[0][2], z[0][3])), fmaxf(fmaxf(z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3])));
   if (__any_sync(0xffffffffu, mx > m + kLazy)) {
@@ -838,8 +840,9 @@ __device__ void kivi_cut_block(const Args<SC>& args, const Seg& sg, MmaState& s,
     const int ta = t0 + 16 * p + gi, tb = ta + 8;
     float y0[2] = {fmaf(acc[0], scale, bs0), fmaf(acc[2], scale, bs0)}, y1[2] = {fmaf(acc[1], scale, bs1), fmaf(acc[3], scale, bs1)};
     if constexpr (SC) {
-      through_form(y0, args, slope2[2 * ti * kPRow], pos0, [&](int x) { return x ? tb : ta; });
-      through_form(y1, args, slope2[(2 * ti + 1) * kPRow], pos1, [&](int x) { return x ? tb : ta; });
+      auto on = [](int x) { return 8.0f * x; };
+      through_form(y0, args, slope2[2 * ti * kPRow], pos0 - ta, on);
+      through_form(y1, args, slope2[(2 * ti + 1) * kPRow], pos1 - ta, on);
     }
     z[4 * p + 0] = visible<SC>(ta, pos0, cut) ? y0[0] : -INFINITY;
     z[4 * p + 1] = visible<SC>(ta, pos1, cut) ? y1[0] : -INFINITY;
@@ -1562,6 +1565,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(Args<SC> a) {
         }
         bool ok = true;
         float m = -INFINITY, l = 0.0f;
+        const int pos_gi = SC ? pos_of(col0 + gi) : 0;
+        const float slope_gi = SC ? ptile[gi * kPRow + kSlopeAt] : 0.0f;
         for (int i = 0; i < n; ++i) {
           const int s = i & 1;
           if (!((skip >> s) & 1u)) {
@@ -1569,8 +1574,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(Args<SC> a) {
               ok = false;
               break;
             }
+            const int u = u0 + i;   // a whole block
             kivi_block<FMT, SC>(a, reinterpret_cast<const char*>(s ? st1 : st0), ms, m, l, qv, a.sm_scale_log2,
-                                SC ? pl.block_of(u0 + i) * BT : 0, SC ? pos_of(col0 + gi) : 0, SC ? ptile[gi * kPRow + kSlopeAt] : 0.0f);
+                                SC ? pos_gi - (u < pl.A0 ? u : u + pl.F0 - pl.A0) * BT : 0, slope_gi);
           }
           if (i + kStages < n) issue(s, i + kStages);
         }

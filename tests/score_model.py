@@ -52,15 +52,23 @@ def attention(q, K, V, positions, seen, cap=0.0, slopes=None, scale=SCALE):
     return torch.stack(outs), torch.stack(Ps)
 
 
+def capped(S, cap):
+    """What a cap adds to the error of scores of size S (its slope is at most 1): the cubic near zero is off
+    by 5.5e-7 relative and its seven roundings by 2^-22 (less than 2^-20 together); where a score of
+    half the cap is about, 1 - 2 / (1 + exp(2 x)) by 2^-21 of the cap (an exponential and a reciprocal
+    of 2^-22, halved by their slope, the rounding of 2 x up to 2^-23 of it, two more)."""
+    near = torch.minimum(S, torch.full_like(S, cap)) * 2.0 ** -20
+    return near + (cap * 2.0 ** -21 if float(S.amax()) > cap / 2 else 0.0)
+
+
 def prompt_bound(q, K, V, positions, P, seen, out, out_dtype, cap=0.0, slopes=None, scale=SCALE):
     """How far a prompt kernel's out may be from `out`.
 
     Scores: keys restored in binary32 and rounded to f16, half a step 2^-11 of each (2^-25
     below f16's normal range); products of f16 operands exact, sums of 128 of them in binary32
     2^-19 of what they add, a bf16 query's elements below 2^-28 of its largest lost (2^-28 of the
-    largest for each of 128). A cap's slope is at most 1, its tanh off by 2^-21 of its value (a
-    polynomial of 1.6e-7, or two functions of 2^-22), so cap 2^-21 at most and 2^-21 of the
-    score. A bias |p - t| slope and what it is added to round to 2^-24 of themselves, three times.
+    largest for each of 128). A cap: capped().
+    A bias |p - t| slope and what it is added to round to 2^-24 of themselves, three times.
     log2 units: times log2 e.
     P V: P rounded to f16, 2^-11 (2^-25 below the normal range, against a sum of P of at least
     1), values 2^-11 (2^-25), exponentials and binary32 sums 2^-19; the output half a step of its
@@ -75,7 +83,7 @@ def prompt_bound(q, K, V, positions, P, seen, out, out_dtype, cap=0.0, slopes=No
     small = (qa.sum(-1) * 2.0 ** -25 + 128 * qa.amax(-1) * 2.0 ** -28 * fin(K).abs().amax()) * scale
     dz = S * (2.0 ** -11 + 2.0 ** -19) + small
     if cap:
-        dz = dz + torch.minimum(S, torch.full_like(S, cap)) * 2.0 ** -21 + 2.0 ** -21
+        dz = dz + capped(S, cap)
     if slopes is not None:
         t = torch.arange(K.shape[0], device=q.device)
         far = torch.stack([torch.where(see[i], (t - p).abs(), torch.zeros_like(t)).amax() for i, p in enumerate(positions)])
@@ -110,7 +118,7 @@ def attend_bound(q, K, V, mk, mv, positions, P, seen, out, out_dtype, bits, cap=
     S = torch.where(see[:, None], S, torch.zeros_like(S)).amax(-1) * scale
     dz = torch.zeros_like(S)
     if cap:
-        dz = dz + torch.minimum(S, torch.full_like(S, cap)) * 2.0 ** -21 + 2.0 ** -21
+        dz = dz + capped(S, cap)
     if slopes is not None:
         t = torch.arange(K.shape[0], device=q.device)
         far = torch.stack([torch.where(see[i], (t - p).abs(), torch.zeros_like(t)).amax() for i, p in enumerate(positions)])
