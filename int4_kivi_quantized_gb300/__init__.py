@@ -390,18 +390,22 @@ class Scores:
         wide = 0x7fffffff
         self.window, self.num_sinks = min(int(window), wide), min(int(num_sinks), wide)
 
-    def c(self, first, prefix):
-        return s4kv_scores(self.cap, _address(self.slopes), self.window, self.num_sinks, _address(first), _address(prefix))
+        self._alone = ctypes.byref(s4kv_scores(self.cap, _address(slopes), self.window, self.num_sinks, None, None))
+
+    def ref(self, first, prefix):
+        """The s4kv_scores of a call, by reference."""
+        if first is None and prefix is None:
+            return self._alone
+        return ctypes.byref(s4kv_scores(self.cap, _address(self.slopes), self.window, self.num_sinks, _address(first), _address(prefix)))
 
 
 def _on_its_device(f):
     """A method that runs with the cache's device as the current one."""
     @functools.wraps(f)
     def call(self, *args, **kwargs):
-        import torch
         if self._current_device() == self._index:
             return f(self, *args, **kwargs)
-        with torch.cuda.device(self._index):
+        with self._torch.cuda.device(self._index):
             return f(self, *args, **kwargs)
     return call
 
@@ -424,6 +428,7 @@ class KVCache:
     def __init__(self, num_layers, num_pages, num_kv_heads, residual_v, max_slots, dtype="fp16",
                  device="cuda", bits=4):
         import torch
+        self._torch = torch   # (an import statement takes a few hundred nanoseconds of a call)
         self.dtype = dtype
         self.cdtype = S4KV_F16 if dtype == "fp16" else S4KV_BF16
         self.torch_dtype = torch.float16 if dtype == "fp16" else torch.bfloat16
@@ -544,7 +549,7 @@ class KVCache:
         the current stream still uses what it was handed."""
         if stream is None:
             return make(*args, **kwargs)
-        import torch
+        torch = self._torch
         st = torch.cuda.ExternalStream(stream, device=self.pool.device) if isinstance(stream, int) else stream
         with torch.cuda.stream(st):
             t = make(*args, **kwargs)
@@ -553,7 +558,7 @@ class KVCache:
 
     def _scratch(self, nbytes, stream):
         """Scratch of one call, allocated on its stream: calls on other streams and captured graphs share none of it."""
-        import torch
+        torch = self._torch
         if stream is None:
             return torch.empty(nbytes, dtype=torch.uint8, device=self.pool.device)
         st = torch.cuda.ExternalStream(stream, device=self.pool.device) if isinstance(stream, int) else stream
@@ -569,7 +574,7 @@ class KVCache:
 
     def _out(self, out, name, shape, out_dtype, stream, like=None):
         """`out`, checked, or a new tensor (like: a checked tensor of this shape, which torch is quicker to copy)."""
-        import torch
+        torch = self._torch
         if out_dtype == self.cdtype:
             dt = self.torch_dtype
         elif out_dtype == S4KV_F32:
@@ -591,7 +596,7 @@ class KVCache:
         """append() with the new keys rotated by their positions on the way (rope: a Rope). With q
         [tokens, H_q, 128], the new tokens' queries are rotated too, into q_out (a new tensor if
         None; q itself is allowed), which is returned."""
-        import torch
+        torch = self._torch
         i32, dt, n = torch.int32, self.torch_dtype, seq_lens_before.shape[0]
         tokens = self._tensor(k, "k", dt, (None, self.H, 128))[0]
         self._tensor(v, "v", dt, (tokens, self.H, 128))
@@ -623,7 +628,7 @@ class KVCache:
                slot_ids=None, sm_scale=0.0, stream=None):
         """Causal attention of the last nq tokens, q [B, nq, H_q, 128], within the newest `window` tokens
         of each query's position and the first `num_sinks` tokens -> out [B, nq, H_q, 128]."""
-        import torch
+        torch = self._torch
         B, nq, Hq, _ = self._tensor(q, "q", self.torch_dtype, (None, None, None, 128))
         rows, width = self._tensor(block_table, "block_table", torch.int32, (None, None))
         self._tensor(seq_lens, "seq_lens", torch.int32, (B,))
@@ -644,8 +649,8 @@ class KVCache:
         return out
 
     def _form(self, scores, first, prefix, queries, n, Hq):
-        """The s4kv_scores of a call: `first` has the shape `queries`, `prefix` one entry a sequence."""
-        import torch
+        """The s4kv_scores of a call, by reference: `first` has the shape `queries`, `prefix` one entry a sequence."""
+        torch = self._torch
         if scores is None:
             scores = _PLAIN
         if scores.slopes is not None:
@@ -654,7 +659,7 @@ class KVCache:
             self._tensor(first, "first", torch.int32, queries)
         if prefix is not None:
             self._tensor(prefix, "prefix", torch.int32, (n,))
-        return scores.c(first, prefix)
+        return scores.ref(first, prefix)
 
     @_on_its_device
     def attend(self, layer, q, block_table, seq_lens, max_seq_len, scores, first=None, prefix=None, out=None,
@@ -662,7 +667,7 @@ class KVCache:
         """Causal attention of the last nq tokens (1 to 16), q [B, nq, H_q, 128] -> out of the same shape,
         with a score form (scores: a Scores). first [B, nq]: the first token that each query's document
         has; prefix [B]: how many first tokens see one another whole."""
-        import torch
+        torch = self._torch
         B, nq, Hq, _ = self._tensor(q, "q", self.torch_dtype, (None, None, None, 128))
         rows, width = self._tensor(block_table, "block_table", torch.int32, (None, None))
         self._tensor(seq_lens, "seq_lens", torch.int32, (B,))
@@ -675,7 +680,7 @@ class KVCache:
         max_seq_len = int(max_seq_len)
         nbytes = self._window_bytes(B, nq, Hq, max_seq_len)
         ws = self._scratch(nbytes, stream)
-        _check(_lib.s4kv_score_attention(self.h, int(layer), ctypes.byref(form), q.data_ptr(), nq, Hq, block_table.data_ptr(),
+        _check(_lib.s4kv_score_attention(self.h, int(layer), form, q.data_ptr(), nq, Hq, block_table.data_ptr(),
                                          width, seq_lens.data_ptr(), _address(slot_ids), B, float(sm_scale), out.data_ptr(),
                                          out_dtype, ws.data_ptr(), nbytes, max_seq_len, self._handle(stream)),
                "s4kv_score_attention")
@@ -689,7 +694,7 @@ class KVCache:
         first [tokens]: the first token that each query's document has; prefix [n]: how many first
         tokens see one another whole. max_seq_len and sum_seq_lens bound the sequences' lengths and
         their sum (n max_seq_len without it): scratch of 512 bytes a token and kv head is taken."""
-        import torch
+        torch = self._torch
         i32, n = torch.int32, seq_lens.shape[0]
         tokens, Hq, _ = self._tensor(q, "q", self.torch_dtype, (None, None, 128))
         self._tensor(cu_q, "cu_q", i32, (n + 1,))
@@ -705,7 +710,7 @@ class KVCache:
         total = n * max_seq_len if sum_seq_lens is None else int(sum_seq_lens)
         nbytes = s4kv_prompt_workspace_bytes(self.h, n, tokens, Hq, max_seq_len, total)
         ws = self._scratch(max(16, nbytes), stream)
-        _check(_lib.s4kv_prompt_attention(self.h, int(layer), ctypes.byref(form), q.data_ptr(), tokens, cu_q.data_ptr(), Hq,
+        _check(_lib.s4kv_prompt_attention(self.h, int(layer), form, q.data_ptr(), tokens, cu_q.data_ptr(), Hq,
                                           block_table.data_ptr(), width, seq_lens.data_ptr(), _address(slot_ids), n,
                                           float(sm_scale), out.data_ptr(), out_dtype, ws.data_ptr(), nbytes, max_seq_len,
                                           total, self._handle(stream)), "s4kv_prompt_attention")
@@ -716,7 +721,7 @@ class KVCache:
                out_dtype=S4KV_F32, stream=None):
         """Restores tokens first[i] .. of sequence i (0 without first) into rows [cu_rows[i], cu_rows[i+1])
         of two dense tensors [num_rows, H_kv, 128], which are returned as (k, v)."""
-        import torch
+        torch = self._torch
         i32, n = torch.int32, seq_lens.shape[0]
         rows, width = self._tensor(block_table, "block_table", i32, (None, None))
         self._tensor(seq_lens, "seq_lens", i32, (n,))
@@ -738,7 +743,7 @@ class KVCache:
 
     def _pages(self, refs, block_table, slot_ids, n):
         """Checks what the calls on pages share; the table's (rows, width)."""
-        import torch
+        torch = self._torch
         self._tensor(refs, "refs", torch.int32, (self.cfg.num_pages,))
         rows, width = self._tensor(block_table, "block_table", torch.int32, (None, None))
         if slot_ids is not None:
@@ -748,7 +753,7 @@ class KVCache:
         return rows, width
 
     def _taken(self, taken, n, stream):
-        import torch
+        torch = self._torch
         if taken is None:
             return self._made(stream, torch.empty, (n,), dtype=torch.int32, device=self.pool.device)
         self._tensor(taken, "taken", torch.int32, (n,))
@@ -759,7 +764,7 @@ class KVCache:
         """Free pages (refs [num_pages]: the table entries that name each; 0: free) for sequences that
         grow from `lens` to `new_lens` tokens, into their rows of block_table [slots, entries], lowest
         page first. Returns `taken` [n]: how many each got, -1 where too few are free."""
-        import torch
+        torch = self._torch
         n = lens.shape[0]
         self._tensor(lens, "lens", torch.int32, (n,))
         self._tensor(new_lens, "new_lens", torch.int32, (n,))
@@ -774,7 +779,7 @@ class KVCache:
     def release_pages(self, refs, block_table, first, last, slot_ids=None, stream=None):
         """Gives up the pages of tokens first .. last - 1 of each sequence (whole pages from `first`
         on, the one that holds `last` - 1 included): their entries become -1, their counts go down."""
-        import torch
+        torch = self._torch
         n = first.shape[0]
         self._tensor(first, "first", torch.int32, (n,))
         self._tensor(last, "last", torch.int32, (n,))
@@ -787,7 +792,7 @@ class KVCache:
         """Continues the sequences of slots src (seq_lens tokens) in slots dst too, in every layer: pages
         that are done with are shared (refs up by one), the others taken and copied, rings and
         lengths copied. block_table has a row for each slot. Returns `taken` [n] as take_pages does."""
-        import torch
+        torch = self._torch
         n = src.shape[0]
         self._tensor(src, "src", torch.int32, (n,))
         self._tensor(dst, "dst", torch.int32, (n,))
@@ -799,7 +804,7 @@ class KVCache:
         return taken
 
     def dequant(self, layer, slot, block_table_row, seq_len, stream=None):
-        import torch
+        torch = self._torch
         k = self._made(stream, torch.empty, (self.H, seq_len, 128), dtype=torch.float32, device=self.pool.device)
         v = self._made(stream, torch.empty_like, k)
         s4kv_dequant_debug(self.h, layer, slot, block_table_row, seq_len, k, v, stream)
