@@ -161,12 +161,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
     sm.lo = 0x7fffffff;
     sm.hi = -1;
   }
+  __syncthreads();
   stream_wait();
   Place pl;
-  // the last tiles of a sequence, whose rows see the most, start first
-  const int where = find_tile<kThreads, true>(a, static_cast<int>(gridDim.x - 1 - blockIdx.x), pl);
+  // the last tiles of a sequence, whose rows see the most, start first, of every kv head
+  const int q_tile = static_cast<int>((gridDim.x - 1 - blockIdx.x) / a.H), h = static_cast<int>(blockIdx.x % a.H);
+  const int where = find_tile<kThreads, true>(a, q_tile, pl);
   if (where != kFound) return;
-  const int h = blockIdx.y, z = blockIdx.z, b = pl.b, g = a.g, cu0 = pl.cu0, m = pl.m, T = pl.T;
+  const int z = blockIdx.y, b = pl.b, g = a.g, cu0 = pl.cu0, m = pl.m, T = pl.T;
   const int row0 = pl.tile * kQRows;
   const int rows = static_cast<int>(min(static_cast<long long>(kQRows), static_cast<long long>(m) * g - row0));
   const int tiles = rows > 128 ? 2 : 1;
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
       if (ok && cnt > 0) ok = __all_sync(0xffffffffu, wait(&sm.odone[s], (cnt - 1) & 1));
       tc_fence_after();
       const bool some = ok && cnt > 0;
-      const long long item = (static_cast<long long>(gridDim.x - 1 - blockIdx.x) * a.H + h) * a.splits + z;
+      const long long item = (static_cast<long long>(q_tile) * a.H + h) * a.splits + z;
       const float inv = a.splits > 1 ? 1.0f : l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
       // Through the queries' place in shared memory (nothing reads them any more), so that a warp writes whole
       // rows: 16 chunks of 16 bytes, chunk c of row r at c xor (r mod 16). 32 bits: in two goes.
@@ -667,12 +669,12 @@ template <bool CAP, bool SLOPE>
 cudaError_t run(const PromptArgs& a, cudaStream_t st) {
   cudaError_t e = ready<CAP, SLOPE>();
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(a.q_tiles), static_cast<unsigned>(a.H), static_cast<unsigned>(a.splits));
+  const dim3 grid(static_cast<unsigned>(a.q_tiles) * a.H, static_cast<unsigned>(a.splits));
   e = launch_behind(prompt_kernel<CAP, SLOPE>, grid, dim3(kThreads), kSmemBytes, st, a);
   if (e != cudaSuccess || a.splits == 1) return e;
   e = prefer_max_shared(reinterpret_cast<const void*>(prompt_join_kernel));
   if (e != cudaSuccess) return e;
-  return launch_behind(prompt_join_kernel, dim3(grid.x, grid.y, kQRows / 32), dim3(256), 0, st, a);
+  return launch_behind(prompt_join_kernel, dim3(static_cast<unsigned>(a.q_tiles), static_cast<unsigned>(a.H), kQRows / 32), dim3(256), 0, st, a);
 }
 
 }  // namespace

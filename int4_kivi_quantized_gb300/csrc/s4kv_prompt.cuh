@@ -84,6 +84,28 @@ __device__ int find_tile(const PromptArgs& a, int idx, Place& place) {
   __shared__ int tot[2][W];
   __shared__ Place found;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (a.n <= 32) {   // a sequence a lane, every warp for itself
+    const int b = lane, c0 = b < a.n ? a.cu_q[b] : 0, c1 = b < a.n ? a.cu_q[b + 1] : 0, T = b < a.n ? a.seq_lens[b] : 0;
+    const bool wrong = c0 < 0 || c1 < c0 || c1 > a.num_q || (b == 0 && c0 != 0) || (b == a.n - 1 && c1 != a.num_q);
+    if (__any_sync(0xffffffffu, wrong)) return kMalformed;
+    const int m = c1 - c0, qt = q_tiles_of(a, m), kt = kv_tiles_of(a, m, T);
+    int q = qt, k = kt;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, q, o), z = __shfl_up_sync(0xffffffffu, k, o);
+      if (lane >= o) {
+        q += y;
+        k += z;
+      }
+    }
+    const int first = BY_Q ? q - qt : k - kt;
+    const unsigned here = __ballot_sync(0xffffffffu, idx >= first && idx - first < (BY_Q ? qt : kt));
+    if (!here) return kNowhere;
+    const int l = __ffs(here) - 1;
+    place = Place{l, idx - __shfl_sync(0xffffffffu, first, l), __shfl_sync(0xffffffffu, k - kt, l), __shfl_sync(0xffffffffu, c0, l),
+                  __shfl_sync(0xffffffffu, m, l), __shfl_sync(0xffffffffu, T, l)};
+    return kFound;
+  }
   int bad = 0, carry_q = 0, carry_k = 0;
   if (tid == 0) {
     bad = a.cu_q[0] != 0 || a.cu_q[a.n] != a.num_q;
