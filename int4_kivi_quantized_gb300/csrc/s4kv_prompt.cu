@@ -417,10 +417,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
             for (int e = 0; e < 4; ++e) t4[e] = max3(t4[e], x[j + 2 * e], x[j + 2 * e + 1]);
           return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
         };
-        // Scores stay S until their exponentials where nothing has to be done to each before (kRaw): no
-        // slopes, and with a cap, every score near zero against it and seen.
-        bool raw = !SLOPE;
-        float top = 0.0f;   // in log2 units
+        // What is left to do to x at the exponentials: x in + at gives log2 units (`in` > 0), so that S
+        // stays S as long as it can; or (raw) the cap near zero, where every score of the warp is seen
+        // and so near it.
+        bool raw = CAP && !SLOPE && whole;
+        float in = f.mul, at = 0.0f, far = 0.0f, top = 0.0f;
         if constexpr (CAP) {
           float t4[4] = {INFINITY, INFINITY, INFINITY, INFINITY};
 #pragma unroll
@@ -429,28 +430,24 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
             for (int e = 0; e < 4; ++e) t4[e] = min3(t4[e], x[j + 2 * e], x[j + 2 * e + 1]);
           const float least = fminf(fminf(t4[0], t4[1]), fminf(t4[2], t4[3]));
           top = largest();
-          const float far = fmaxf(top, -least);
+          far = fmaxf(top, -least);
           // (the last coefficient has the seventh power of f.mul: a normal number, or it is not used)
           const bool near_zero = __all_sync(0xffffffffu, far * f.mul <= kNearCap && fabsf(near.c[kNearCoefs - 1]) > 1e-36f);
-          raw = raw && whole && near_zero;
-          if (raw) top = near(top);
-          else through_cap(x, f, near, near_zero);
+          raw = raw && near_zero;
+          if (!raw) through_cap(x, f, near, near_zero);
+          in = 1.0f;
         }
         if constexpr (SLOPE) {
           const float rel = static_cast<float>(pos - t0);
-          const float in = CAP ? 1.0f : f.mul;
-          if (__all_sync(0xffffffffu, rel >= 127.0f)) {   // every token before the query: the distance falls along the row
-            const float2 in2 = make_float2(in, in), by2 = make_float2(f.slope2, f.slope2), at2 = make_float2(-f.slope2 * rel, -f.slope2 * rel);
+          const float by = CAP ? f.slope2 : f.slope2 / f.mul;   // in x's units
+          if (__all_sync(0xffffffffu, rel >= 127.0f && fabsf(by) < 1e30f)) {   // every token before the query: the distance falls along the row
+            at = -f.slope2 * rel;
 #pragma unroll
-            for (int j = 0; j < 128; j += 2) {
-              const float2 bias = __ffma2_rn(by2, make_float2(static_cast<float>(j), static_cast<float>(j + 1)), at2);
-              const float2 y = CAP ? __fadd2_rn(make_float2(x[j], x[j + 1]), bias) : __ffma2_rn(make_float2(x[j], x[j + 1]), in2, bias);
-              x[j] = y.x;
-              x[j + 1] = y.y;
-            }
+            for (int j = 0; j < 128; ++j) x[j] = fmaf(by, static_cast<float>(j), x[j]);
           } else {
 #pragma unroll
             for (int j = 0; j < 128; ++j) x[j] = fmaf(-f.slope2, fabsf(static_cast<float>(j) - rel), x[j] * in);
+            in = 1.0f;
           }
         }
         if (!whole) {
@@ -474,8 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
                 if ((poison >> j) & 1u) x[32 * k + j] = __int_as_float(0x7fffffff);
           }
         }
-        if (!CAP || !raw) top = largest();
-        if (!CAP && !SLOPE) top *= f.mul;
+        if (raw) top = near(top);
+        else top = fmaf(largest(), in, at);
         if (__any_sync(0xffffffffu, top > mx + kLazyP)) {
           const float mn = top > mx + kLazyP ? top : mx;
           const float by = mx == mn ? 1.0f : mx == -INFINITY ? 0.0f : exp2_fast(mx - mn);   // (nothing so far: l and O are zeros)
@@ -499,14 +496,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
         }
         const float base = mx == -INFINITY ? 0.0f : mx;   // (a row that has seen nothing: every p is zero)
         float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-        auto exponentials = [&](auto how) {   // how: 0 of x - base, 1 of x mul - base, 2 of the cap near zero - base
-          constexpr int kHow = decltype(how)::value;
-          const float2 base2 = make_float2(-base, -base), mul2 = make_float2(f.mul, f.mul);
+        auto exponentials = [&](auto capped) {
+          const float2 in2 = make_float2(in, in), off2 = make_float2(at - base, at - base);
           auto pair = [&](int j) -> uint32_t {
             float2 y = make_float2(x[2 * j], x[2 * j + 1]);
-            if (kHow == 0) y = __fadd2_rn(y, base2);
-            if (kHow == 1) y = __ffma2_rn(y, mul2, base2);
-            if (kHow == 2) y = __ffma2_rn(y, near.inner(y), base2);
+            y = __ffma2_rn(y, decltype(capped)::value ? near.inner(y) : in2, off2);
             y = make_float2(exp2_fast(y.x), exp2_fast(y.y));
             sum[j & 1] = __fadd2_rn(sum[j & 1], y);
             return pack_f16x2(y.x, y.y);
@@ -519,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
             tmem_st32(s_at + 32 * k, w);
           }
         };
-        if (CAP && !SLOPE && raw) exponentials(std::integral_constant<int, 2>{});
-        else exponentials(std::integral_constant<int, CAP || SLOPE ? 0 : 1>{});
+        if (CAP && !SLOPE && raw) exponentials(std::true_type{});
+        else exponentials(std::false_type{});
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_wait_st();
         tc_fence_before();
