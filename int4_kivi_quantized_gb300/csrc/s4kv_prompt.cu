@@ -192,6 +192,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
     mbar_init(&sm.drain, 1);
   }
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  uint4 v[16];   // the queries on their way: a warp's 32 rows, two at a time
+  if (warp < kRowWarps) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int r = 32 * warp + 2 * k + (lane >> 4);
+      v[k] = r < rows ? reinterpret_cast<const uint4*>(a.q + out_row(r) * kD)[lane & 15] : make_uint4(0u, 0u, 0u, 0u);
+    }
+  }
   const int slot = a.slot_ids ? a.slot_ids[b] : b;
   int arg;
   const int why = refused(a, pl, slot, h, arg);
@@ -213,35 +221,45 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
       atomicMin(&sm.lo, lo);
       atomicMax(&sm.hi, hi);
     }
+    // f16 operands, swizzled. bf16 has the wider range: a row is taken at the power of two that brings its
+    // largest element to 2^3 .. 2^4: exact, elements down to 2^-28 of the largest keep every bit,
+    // and powers of what then scales the scores stay normal numbers.
     const int c = lane & 15;
-    uint4 v[16];   // every load first
+    float up = 1.0f;   // of row lane % 16 of this half warp's
+    if (a.dtype == S4KV_BF16) {
+      uint32_t top[16];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int r = 32 * warp + 2 * k + (lane >> 4);
-      v[k] = r < rows ? reinterpret_cast<const uint4*>(a.q + out_row(r) * kD)[c] : make_uint4(0u, 0u, 0u, 0u);
+      for (int k = 0; k < 16; ++k) {
+        constexpr uint32_t kAbs = 0x7fff7fffu;
+        const uint32_t t = __vimax3_u16x2(__vimax3_u16x2(v[k].x & kAbs, v[k].y & kAbs, v[k].z & kAbs), v[k].w & kAbs, 0u);
+        top[k] = max(t & 0xffffu, t >> 16);
+      }
+      // over the 16 lanes: each step halves the rows that a lane goes on with
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) {
+        const bool upper = lane & o;
+#pragma unroll
+        for (int k = 0; k < o; ++k) {
+          const uint32_t keep = upper ? top[k + o] : top[k], send = upper ? top[k] : top[k + o];
+          top[k] = max(keep, __shfl_xor_sync(0xffffffffu, send, o));
+        }
+      }
+      const int e = static_cast<int>(top[0] >> 7), pw = top[0] == 0 || e == 255 ? 0 : min(3 + 127 - e, 126);
+      up = power_of_two(pw);
+      sm.up[32 * warp + 2 * c + (lane >> 4)] = power_of_two(-pw);
+    } else {
+      sm.up[tid] = 1.0f;
     }
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       const int r = 32 * warp + 2 * k + (lane >> 4);
-      float down = 1.0f;
+      uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
       if (a.dtype == S4KV_BF16) {
-        uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-        uint32_t top = 0;   // the largest magnitude's bits, in the upper half
+        const float by = __shfl_sync(0xffffffffu, up, (lane & 16) | k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = max(top, max(w[i] & 0x7fff0000u, (w[i] << 16) & 0x7fff0000u));
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // to 2^3 .. 2^4, for the same reason as query_power's 2^14: powers of the scores' scale stay normal numbers
-        const int e = static_cast<int>(top >> 23), pw = top == 0 || e == 255 ? 0 : min(3 + 127 - e, 126);
-        const float up = power_of_two(pw);
-        down = power_of_two(-pw);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
-        v[k] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < 4; ++i) w[i] = pack_f16x2(__uint_as_float(w[i] << 16) * by, __uint_as_float(w[i] & 0xffff0000u) * by);
       }
-      *reinterpret_cast<uint4*>(q_tiles + (r >> 7) * kQBytes + sw128_off(r & 127, 8 * c, 128)) = v[k];
-      if (c == 0) sm.up[r] = down;
+      *reinterpret_cast<uint4*>(q_tiles + (r >> 7) * kQBytes + sw128_off(r & 127, 8 * c, 128)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     fence_proxy_async();
   }
