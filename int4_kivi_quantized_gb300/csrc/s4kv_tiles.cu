@@ -38,10 +38,12 @@ struct TileRows {
     }
     const int r = r0 + token;
     if (bits) {
-      bool wild = false;
+      // what is finite is a zero times zero
+      __half2 z = __floats2half2_rn(0.0f, 0.0f);
+      const __half2 zero = z;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) wild = wild || (w[i] & 0x7c00u) == 0x7c00u || (w[i] & 0x7c000000u) == 0x7c000000u;
-      if (wild) {
+      for (int i = 0; i < 4; ++i) z = __hfma2(*reinterpret_cast<const __half2*>(&w[i]), zero, z);
+      if (*reinterpret_cast<const uint32_t*>(&z) & 0x7fff7fffu) {
         *bits |= 1u << (r & (kP - 1));
         w[0] = w[1] = w[2] = w[3] = 0u;
       }
@@ -59,7 +61,7 @@ struct TileRows {
 };
 
 template <int FMT>
-__global__ void __launch_bounds__(kThreads, 3) tiles_kernel(PromptArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) tiles_kernel(PromptArgs a) {
   stream_wait();
   Place p;
   const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -69,8 +71,6 @@ __global__ void __launch_bounds__(kThreads, 3) tiles_kernel(PromptArgs a) {
     report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_CU, a.n);
   if (where != kFound) return;
   const int m = p.m, T = p.T, slot = a.slot_ids ? a.slot_ids[p.b] : p.b;
-  int arg;
-  if (refused(a, p, slot, h, arg)) return;   // (the attention kernel says so)
   const int tp = kv_range(a, m, T).tile(p.tile) * kKvTile + kP * warp;   // this warp's 16 tokens
   const long long at = (static_cast<long long>(p.kv0) + p.tile) * a.H + h;
   uint32_t bits = 0;
@@ -81,26 +81,34 @@ __global__ void __launch_bounds__(kThreads, 3) tiles_kernel(PromptArgs a) {
   const int quant = values ? Tv : Tk, mod = FMT == kI8 ? kP : values ? a.R : kG;
   const uint16_t* ring = values ? reinterpret_cast<const uint16_t*>(a.vring) + slot * a.vring_slot + h * a.vring_head
                                 : reinterpret_cast<const uint16_t*>(a.kring) + slot * a.kring_slot + h * a.kring_head;
-  auto record = [&](int logical) -> const char* {   // null (reported) outside the pool
-    const int pp = bt[logical];
+  const int end = min(max(T - tp, 0), kP);            // tokens [0, end) of this page are there
+  const int held = min(max(quant - tp, 0), end);    // [0, held) in its record
+  // the table's entries, on their way while the sequence is checked
+  const bool group = !kByte<FMT> && !values;   // half of a key group: both its pages
+  const int page = tp / kP;
+  int pp[2] = {-1, -1};
+  if (held > 0 && static_cast<long long>(a.bt_stride) * kP >= T) {
+    pp[0] = bt[group ? page & ~1 : page];
+    pp[1] = group ? bt[page | 1] : pp[0];
+  }
+  int arg;
+  if (refused(a, p, slot, h, arg)) return;   // (the attention kernel says so)
+  auto record = [&](int pp) -> const char* {   // null (reported) outside the pool
     if (pp >= 0 && pp < a.num_pages) return a.pages + (static_cast<long long>(pp) * a.H + h) * Rec<FMT>::kBytes;
     if (lane == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, pp);
     return nullptr;
   };
-  const int end = min(max(T - tp, 0), kP);            // tokens [0, end) of this page are there
-  const int held = min(max(quant - tp, 0), end);    // [0, held) in its record
   if (held > 0) {
-    const int page = tp / kP;
-    if (!kByte<FMT> && !values) {
-      if constexpr (!kByte<FMT>) {   // half of a key group
+    if (group) {
+      if constexpr (!kByte<FMT>) {
         const int odd = page & 1;
-        const char* r0 = record(page & ~1);
-        const char* r1 = record(page | 1);
+        const char* r0 = record(pp[0]);
+        const char* r1 = record(pp[1]);
         if (r0 && r1) put_key_group<FMT>(r0, r1, kP * odd, kP * odd + kP, TileRows{rows.tile, rows.r0 - kP * odd, nullptr});
         else rows.clear(0, kP);
       }
     } else {
-      const char* rec = record(page);
+      const char* rec = record(pp[0]);
       if (!rec) rows.clear(0, held);
       else if (values) put_values<FMT>(a.fp8_scale + a.H + h, rec, 0, held, rows);
       else if constexpr (kByte<FMT>) put_keys<FMT>(a.fp8_scale + h, rec, 0, held, rows);
