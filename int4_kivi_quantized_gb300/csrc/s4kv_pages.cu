@@ -18,6 +18,7 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kEach = 16;                     // neighbouring counts of a thread
 constexpr int kTile = kThreads * kEach;
+constexpr int kList = 4096;
 
 __device__ __forceinline__ unsigned add_to(unsigned a, unsigned b) { return min(a + b, 0x7fffffffu); }   // (both below 2^31)
 
@@ -64,7 +65,11 @@ __device__ __forceinline__ Want want_of(const PageArgs& a, int i) {
 template <bool FORK>
 __global__ void __launch_bounds__(kThreads, 1) give_kernel(PageArgs a) {
   __shared__ unsigned pre[kMaxPageJobs + 1];                  // pages wanted by the sequences before
-  __shared__ unsigned seen[kMaxPageRows / 32], twice[kMaxPageRows / 32], source[FORK ? kMaxPageRows / 32 : 1];   // rows, a bit each
+  __shared__ unsigned seen[kMaxPageRows / 32];                // rows, a bit each
+  __shared__ unsigned list[kList];                            // two more such sets, then pages by rank
+  unsigned* const twice = list;
+  unsigned* const source = list + kMaxPageRows / 32;
+  static_assert(kList >= 2 * (kMaxPageRows / 32), "both sets");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < (a.rows + 31) / 32; i += kThreads) {
     seen[i] = twice[i] = 0u;
@@ -176,21 +181,38 @@ __global__ void __launch_bounds__(kThreads, 1) give_kernel(PageArgs a) {
   unsigned rank0 = 0;
   for (int base = 0; rank0 < granted && base < a.num_pages; base += kTile) {
     unsigned z = base == 0 ? z0 : look(base), here;
-    unsigned k = rank0 + block_scan(__popc(z), here);
-    rank0 += here;
-    while (z && k < granted) {
-      const int p = base + tid * kEach + __ffs(z) - 1;
-      z &= z - 1;
-      int lo = 0, hi = a.n - 1;   // the last sequence with pre <= k
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pre[mid] <= k) lo = mid; else hi = mid - 1;
+    const unsigned k0 = rank0 + block_scan(__popc(z), here), end = min(rank0 + here, granted);
+    // through a list by rank, so that the pages of one thread's counts are every thread's to enter
+    for (unsigned r = rank0; r < end; r += kList) {
+      __syncthreads();
+      unsigned k = k0;
+      for (unsigned y = z; y && k < end; y &= y - 1, ++k)
+        if (k - r < kList) list[k - r] = base + tid * kEach + __ffs(y) - 1;
+      __syncthreads();
+      constexpr int kMine = kList / kThreads;
+      Want w[kMine];
+#pragma unroll
+      for (int c = 0; c < kMine; ++c) {
+        k = r + tid + c * kThreads;
+        if (k >= end) continue;
+        int lo = 0, hi = a.n - 1;   // the last sequence with pre <= k
+        while (lo < hi) {
+          const int mid = (lo + hi + 1) >> 1;
+          if (pre[mid] <= k) lo = mid; else hi = mid - 1;
+        }
+        w[c] = want_of<FORK>(a, lo);
+        w[c].e0 += k - pre[lo];
       }
-      const Want w = want_of<FORK>(a, lo);
-      a.table[static_cast<long long>(w.row) * a.bt_stride + w.e0 + (k - pre[lo])] = p;
-      a.refs[p] = 1;
-      ++k;
+#pragma unroll
+      for (int c = 0; c < kMine; ++c) {
+        k = r + tid + c * kThreads;
+        if (k >= end) continue;
+        const int p = list[k - r];
+        a.table[static_cast<long long>(w[c].row) * a.bt_stride + w[c].e0] = p;
+        a.refs[p] = 1;
+      }
     }
+    rank0 += here;
   }
 }
 
