@@ -419,6 +419,17 @@ __device__ __forceinline__ void byte_block(const Args<SC>& args, const char* rec
       }
     }
   }
+  bool sees[CT][4];
+  if (kMask) {
+#pragma unroll
+    for (int c = 0; c < CT; ++c)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        sees[c][x] = visible<SC>(cut.tok0 + 2 * ti + (x & 1) + 8 * (x >> 1), pos[c], cut);
+        // (what an FP8 page holds behind the last token has no say in how the others are capped)
+        if (SC && !sees[c][x]) z[c][x] = 0.0f;
+      }
+  }
   if constexpr (SC) {
 #pragma unroll
     for (int c = 0; c < CT; ++c)
@@ -428,10 +439,7 @@ __device__ __forceinline__ void byte_block(const Args<SC>& args, const char* rec
 #pragma unroll
     for (int c = 0; c < CT; ++c)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int t = cut.tok0 + 2 * ti + (x & 1) + 8 * (x >> 1);
-        z[c][x] = visible<SC>(t, pos[c], cut) ? z[c][x] : -INFINITY;
-      }
+      for (int x = 0; x < 4; ++x) z[c][x] = sees[c][x] ? z[c][x] : -INFINITY;
   }
   byte_softmax<NC, kMask>(s, z);
   uint32_t b[CT][2];
