@@ -113,6 +113,23 @@ def test_sequences_without_a_chunk_are_not_looked_at():
 
 
 @pytest.mark.parametrize("which", ["prompt", "attend"])
+def test_ends_of_the_integers(which):
+    """first and prefix at both ends of their type: everything, nothing, and as without them."""
+    p = Pair()
+    call = getattr(p, which)
+    n = (220,) if which == "prompt" else (3, 2)
+    fill = lambda shape, x: torch.full(shape, x, dtype=torch.int32, device="cuda")  # noqa: E731
+    least, most = -2 ** 31, 2 ** 31 - 1
+    p.scores = s4.Scores(20.0)
+    good, whole = call(), call(prefix=p.f.seq)
+    assert torch.equal(call(first=fill(n, least)), good)
+    assert torch.equal(call(prefix=fill((3,), least)), good)
+    assert torch.equal(call(prefix=fill((3,), most)), whole) and not torch.equal(good, whole)
+    assert not call(first=fill(n, most)).any()
+    p.f.ok()
+
+
+@pytest.mark.parametrize("which", ["prompt", "attend"])
 def test_waits_that_run_out(which):
     p = Pair()
     call = getattr(p, which)
