@@ -392,6 +392,11 @@ class Scores:
 
         self._alone = ctypes.byref(s4kv_scores(self.cap, _address(slopes), self.window, self.num_sinks, None, None))
 
+    def __setattr__(self, name, value):
+        if hasattr(self, "_alone"):   # (which holds the slopes' address)
+            raise AttributeError("a Scores does not change: make another")
+        object.__setattr__(self, name, value)
+
     def ref(self, first, prefix):
         """The s4kv_scores of a call, by reference."""
         if first is None and prefix is None:

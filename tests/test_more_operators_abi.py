@@ -36,6 +36,14 @@ def test_score_forms_are_checked():
             s4.Scores(**kw)
 
 
+def test_score_forms_do_not_change():
+    f = s4.Scores(50.0, torch.ones(4))
+    for name in ("cap", "slopes", "window", "num_sinks"):
+        with pytest.raises(AttributeError):
+            setattr(f, name, None)
+    assert f.cap == 50.0 and f.slopes.shape == (4,)
+
+
 def test_plain_spans_are_the_documented_ones():
     see = lambda *a, **k: [r.nonzero().flatten().tolist() for r in seen_of(*a, **k)]  # noqa: E731
     assert see(6, [3, 5]) == [[0, 1, 2, 3], [0, 1, 2, 3, 4, 5]]
