@@ -84,6 +84,7 @@ template <int FMT> constexpr int kLeastUnits = kByte<FMT> ? 4 : 3;           // 
 // sequences of 1024 to 8192 tokens 57.6 / 55.7 / 55.9 / 56.2 us, 16 of 777 to 8191 with
 // 16 columns 44.4 / 40.7 / 39.1 / 38.9. KIVI pages, where the cut blocks' cost says it
 // already: 0 / 1 / 3: 64 sequences behind a window of 4096 83.8 / 84.1 / 85.4.
+constexpr int kRingUnits = 4;   // SC, INT8 pages: what the unfinished block costs, in records
 template <int FMT> constexpr int kSegCost = kByte<FMT> ? 6 : 0;
 
 template <int FMT, int NC, bool SC>
@@ -204,8 +205,17 @@ struct Plan {
   }
 };
 
+// Of the spans of a tile's queries: the earliest and the latest start, the earliest end (the latest is T - 1).
+struct Reach {
+  int w_first, w_last, end;
+  __device__ __forceinline__ void add(const Span& s, int T) {
+    w_first = min(w_first, s.lo);
+    w_last = max(w_last, min(s.lo, T));
+    end = min(end, s.hi);
+  }
+};
 template <int FMT, bool SC>
-__device__ __forceinline__ Plan<FMT> plan_of(int T, const Args<SC>& a, int b) {
+__device__ __forceinline__ Plan<FMT> plan_by(int T, const Args<SC>& a, const Reach& r) {
   constexpr int BT = kBlock<FMT>;
   Plan<FMT> p;
   if (T < a.nq || T <= 0 || T > a.max_seq_len) {   // nothing to attend to (T = 0), or a bad length
@@ -215,31 +225,52 @@ __device__ __forceinline__ Plan<FMT> plan_of(int T, const Args<SC>& a, int b) {
   }
   // blocks that are quantized whole
   const int main = FMT == kI8 ? T / BT : FMT == 8 ? T / BT : (min(T & ~(kG - 1), max(0, T - a.R)) / kG);
-  const int first = T - a.nq;                               // position of the first query
-  int w_first = max(0, first - a.window + 1), w_last = max(0, T - a.window), reach = first;
-  if constexpr (SC) {   // the earliest and the latest start of a query's span, the earliest end (the latest is T - 1)
-    w_first = T - 1;
-    w_last = 0;
-    reach = T - 1;
-    for (int i = 0; i < a.nq; ++i) {
-      const Span s = span_of(a.score, first + i, T, static_cast<long long>(b) * a.nq + i, b);
-      w_first = min(w_first, s.lo);
-      w_last = max(w_last, min(s.lo, T));
-      reach = min(reach, s.hi);
-    }
-  }
   p.E = (T - 1) / BT + 1;
-  p.W0 = w_first / BT;
+  p.W0 = r.w_first / BT;
   p.A1 = min((a.sinks + BT - 1) / BT, p.W0);
   p.A0 = min(min(a.sinks / BT, p.A1), main);
-  if constexpr (SC) p.A0 = min(p.A0, (reach + 1) / BT);
-  p.F0 = (w_last + BT - 1) / BT;
-  p.F1 = min(main, (reach + 1) / BT);
+  if constexpr (SC) p.A0 = min(p.A0, (r.end + 1) / BT);
+  p.F0 = (r.w_last + BT - 1) / BT;
+  p.F1 = min(main, (r.end + 1) / BT);
   if (p.F0 >= p.F1) p.F0 = p.F1 = p.W0;
   p.nf = p.A0 + p.F1 - p.F0;
   p.nx = (p.A1 - p.A0) + (p.F0 - p.W0) + (p.E - p.F1);
   p.work = p.nf + static_cast<long long>(kByte<FMT> ? 1 : a.tail_cost) * p.nx;
+  if (SC && FMT == kI8 && T % BT != 0) p.work += kRingUnits - 1;
   return p;
+}
+
+// The plan of sequence b, by one thread.
+template <int FMT, bool SC>
+__device__ __forceinline__ Plan<FMT> plan_of(int T, const Args<SC>& a, int b) {
+  const int first = T - a.nq;                               // position of the first query
+  if constexpr (SC) {
+    Reach r{T - 1, 0, T - 1};
+#pragma unroll 4
+    for (int i = 0; i < a.nq; ++i) r.add(span_of(a.score, first + i, T, static_cast<long long>(b) * a.nq + i, b), T);
+    return plan_by<FMT, SC>(T, a, r);
+  } else {
+    return plan_by<FMT, SC>(T, a, Reach{max(0, first - a.window + 1), max(0, T - a.window), first});
+  }
+}
+// By a whole warp, a query a lane; `mine`: the span of the lane's.
+template <int FMT, bool SC>
+__device__ __forceinline__ Plan<FMT> plan_of_warp(int T, const Args<SC>& a, int b, Span& mine) {
+  mine = Span{0x7fffffff, -1};
+  if constexpr (SC) {
+    const int lane = threadIdx.x & 31;
+    Reach r{T - 1, 0, T - 1};
+    if (lane < a.nq) {
+      mine = span_of(a.score, T - a.nq + lane, T, static_cast<long long>(b) * a.nq + lane, b);
+      r.add(mine, T);
+    }
+    r.w_first = __reduce_min_sync(0xffffffffu, r.w_first);
+    r.w_last = __reduce_max_sync(0xffffffffu, r.w_last);
+    r.end = __reduce_min_sync(0xffffffffu, r.end);
+    return plan_by<FMT, SC>(T, a, r);
+  } else {
+    return plan_of<FMT, SC>(T, a, b);
+  }
 }
 
 __device__ __forceinline__ void mma16816_c(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
@@ -1107,6 +1138,13 @@ __device__ __forceinline__ void combine_cluster(const WindowArgs& a, const WSmem
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// x / y, x >= 0 and y > 0, in 32 bits where they do (a 64-bit division takes several hundred cycles).
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  return (x | y) >> 32 ? x / y : static_cast<unsigned>(x) / static_cast<unsigned>(y);
+}
+// Where part i of n parts of C starts.
+__device__ __forceinline__ long long part_of(long long C, int i, int n) { return quotient(i * C, n); }
+
 // FMT: page format. NC: columns a warp holds (8, or 16 on 8-bit pages).
 // ONE: a cluster of CTAs holds one segment and combines it itself (grid.x = CTAs of
 // a cluster, grid.y = segments); otherwise the slices of the whole line, as above.
@@ -1131,19 +1169,20 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(Args<SC> a) {
   int b, seg, T, gw, n_act;
   long long r0, r1, seg_start, C = 0;
   Plan<FMT> pl;
+  Span own_span;   // of query `lane` of sequence b
   if constexpr (ONE) {
     const int per = a.H * a.tiles;
     b = static_cast<int>(blockIdx.y) / per;
     seg = static_cast<int>(blockIdx.y) - b * per;
     T = a.seq_lens[b];
-    pl = plan_of<FMT, SC>(T, a, b);
+    pl = plan_of_warp<FMT, SC>(T, a, b, own_span);
     gw = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
     n_act = static_cast<int>(gridDim.x) * kWarps;
     if (a.max_warps > 0 && a.max_warps < n_act) n_act = a.max_warps;
     if (pl.work < n_act) n_act = static_cast<int>(pl.work);
     seg_start = 0;
-    r0 = gw * pl.work / n_act;
-    r1 = (gw + 1) * pl.work / n_act;
+    r0 = part_of(pl.work, gw, n_act);
+    r1 = part_of(pl.work, gw + 1, n_act);
     if (gw >= n_act) r1 = 0;
     if (lane < NC) {
       one.wm[warp][lane] = -INFINITY;
@@ -1187,8 +1226,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(Args<SC> a) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     gw = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
     if (gw >= n_act) return;
-    r0 = gw * C / n_act;
-    r1 = (gw + 1) * C / n_act;
+    r0 = part_of(C, gw, n_act);
+    r1 = part_of(C, gw + 1, n_act);
     {   // first sequence touching this slice
       int lo = 0, hi = a.B - 1;
       while (lo < hi) {
@@ -1198,8 +1237,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(Args<SC> a) {
       b = lo;
     }
     T = a.seq_lens[b];
-    pl = plan_of<FMT, SC>(T, a, b);
-    seg = static_cast<int>((r0 - pre[b]) / pl.cost());   // h * tiles + tile, within the sequence
+    pl = plan_of_warp<FMT, SC>(T, a, b, own_span);
+    seg = static_cast<int>(quotient(r0 - pre[b], pl.cost()));   // h * tiles + tile, within the sequence
     seg_start = pre[b] + seg * pl.cost();
     if (kSegCost<FMT> > 0 && r0 - seg_start >= pl.work) {   // nothing of this segment is left
       seg_start += pl.cost();
@@ -1207,7 +1246,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(Args<SC> a) {
         seg = 0;
         if (++b >= a.B) return;
         T = a.seq_lens[b];
-        pl = plan_of<FMT, SC>(T, a, b);
+        pl = plan_of_warp<FMT, SC>(T, a, b, own_span);
       }
     }
   }
@@ -1232,7 +1271,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(Args<SC> a) {
       }
   };
 
-  const int ncols = a.nq * a.g;
+  const int ncols = a.nq * a.g, by_g = 65536 / a.g + 1;   // col / g = col by_g >> 16: col g < 65536
 
   while (seg_start < r1) {
     const long long seg_end = seg_start + pl.work;   // of its blocks
@@ -1241,18 +1280,49 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(Args<SC> a) {
     const int h = seg / a.tiles, col0 = (seg - h * a.tiles) * NC;
     const int slot = a.slot_ids ? a.slot_ids[b] : b;
     const bool slot_ok = slot >= 0 && slot < a.max_slots;
+    // what the segment needs from memory, all of it on its way at once: the stored length, the column's slope,
+    // the pages of its first units and (8-bit pages) the queries
+    const bool shape_ok = T > 0 && T >= a.nq && T <= a.max_seq_len && static_cast<long long>(a.bt_stride) * kP >= T;
     const int lens_v = slot_ok ? __ldcg(a.lens + slot * a.H + h) : 0;
     // positions: of a column past the last one, the last query's
-    auto pos_of = [&](int col) { return T - a.nq + min(col, ncols - 1) / a.g; };
+    auto pos_of = [&](int col) { return T - a.nq + (min(col, ncols - 1) * by_g >> 16); };
     auto qrow_of = [&](int col) -> const uint16_t* {
       if (col >= ncols) return nullptr;
-      const int i = col / a.g;
+      const int i = col * by_g >> 16;
       return a.q + ((static_cast<long long>(b) * a.nq + i) * a.Hq + h * a.g + (col - i * a.g)) * kD;
     };
     auto out_row = [&](int col) -> long long {
-      const int i = col / a.g;
+      const int i = col * by_g >> 16;
       return (static_cast<long long>(b) * a.nq + i) * a.Hq + h * a.g + (col - i * a.g);
     };
+    float slope = 0.0f;   // of column `lane`
+    if constexpr (SC) {
+      if (lane < NC && a.score.slopes && col0 + lane < ncols) slope = a.score.slopes[h * a.g + col0 + lane - ((col0 + lane) * by_g >> 16) * a.g] * 1.4426950408889634f;
+    }
+    const int* bt = a.block_table + static_cast<long long>(b) * a.bt_stride;
+    int u0 = 0, u1 = 0, n = 0, first_pp = 0;   // (8-bit pages)
+    bool ring = false;
+    constexpr bool kEarly = FMT == kI8 || NC == 16;   // (FP8, 8 columns: 2% slower with them early)
+    uint4 qrows[CT][4];
+    const uint16_t* qrow[CT];
+    auto fetch_q = [&](int c) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        qrows[c][j] = qrow[c] ? reinterpret_cast<const uint4*>(qrow[c])[4 * ti + j] : make_uint4(0u, 0u, 0u, 0u);
+    };
+    if constexpr (kByte<FMT>) {
+      const int units = pl.nf + pl.nx;   // the last one may be the unfinished block, of more than one position
+      u0 = min(static_cast<int>(lo), units);
+      u1 = min(static_cast<int>(hi), units);
+      ring = FMT == kI8 && (T % kP) != 0 && u0 < u1 && u1 == units;
+      n = u1 - u0 - (ring ? 1 : 0);                                  // records to stream
+      if (shape_ok && lane < n) first_pp = bt[pl.block_of(u0 + lane)];
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        qrow[c] = qrow_of(col0 + 8 * c + gi);
+        if (kEarly) fetch_q(c);
+      }
+    }
     Cut cut;
     cut.tok0 = 0;
     cut.window = a.window;
@@ -1270,13 +1340,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(Args<SC> a) {
       Span mine{0x7fffffff, -1};
       if (lane < a.nq && T > 0) {
         const int p = T - a.nq + lane;
-        mine = span_of(a.score, p, T, static_cast<long long>(b) * a.nq + lane, b);
-        *reinterpret_cast<Span*>(spans + lane * cut.step) = mine;
-        if (p < cut.first || p > cut.last) mine = Span{0x7fffffff, -1};
+        *reinterpret_cast<Span*>(spans + lane * cut.step) = own_span;
+        if (p >= cut.first && p <= cut.last) mine = own_span;
       }
-      if (lane < NC)
-        slopes[lane * kEach] = a.score.slopes && col0 + lane < ncols ? a.score.slopes[h * a.g + (col0 + lane) % a.g] * 1.4426950408889634f
-                                                        : 0.0f;
+      if (lane < NC) slopes[lane * kEach] = slope;
       cut.lo = __reduce_min_sync(0xffffffffu, mine.lo);
       cut.hi = __reduce_max_sync(0xffffffffu, mine.hi);
       __syncwarp();
@@ -1292,13 +1359,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(Args<SC> a) {
       if (lane == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_TABLE, b);
     }
     valid = valid && !aborted;
-    const int* bt = a.block_table + static_cast<long long>(b) * a.bt_stride;
-    auto page = [&](int lp) -> int {   // pool page of logical page lp, -1 (reported) if outside the pool
-      const int pp = bt[lp];
+    auto in_pool = [&](int pp) -> int {   // a pool page, -1 (reported) if outside the pool
       if (pp >= 0 && pp < a.num_pages) return pp;
       report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, pp);
       return -1;
     };
+    auto page = [&](int lp) -> int { return in_pool(bt[lp]); };   // of logical page lp
     const uint16_t* kring = reinterpret_cast<const uint16_t*>(a.kring) + (slot_ok ? slot : 0) * a.kring_slot + h * a.kring_head;
     const uint16_t* vring = reinterpret_cast<const uint16_t*>(a.vring) + (slot_ok ? slot : 0) * a.vring_slot + h * a.vring_head;
 
@@ -1306,22 +1372,17 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(Args<SC> a) {
       ByteState<NC> st;
       byte_init(st);
       if (valid) {
-        const int u0 = static_cast<int>(lo), u1 = static_cast<int>(hi);
-        const bool ring = FMT == kI8 && (T % kP) != 0 && u1 == pl.nf + pl.nx;   // the last unit is the unfinished block
-        const int n = u1 - u0 - (ring ? 1 : 0);                                  // records to stream
         auto pages_of = [&](int k) -> int {   // pool pages of units u0 + 32 k + lane
           const int x = 32 * k + lane;
           return x < n ? page(pl.block_of(u0 + x)) : 0;
         };
-        int curp = pages_of(0), nxtp = n > 32 ? pages_of(1) : 0, cur_k = 0;
+        int curp = lane < n ? in_pool(first_pp) : 0, nxtp = n > 32 ? pages_of(1) : 0, cur_k = 0;
         int pos[CT], opos[CT][2];
-        const uint16_t* qrow[CT];
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
           pos[c] = pos_of(col0 + 8 * c + gi);
           opos[c][0] = pos_of(col0 + 8 * c + 2 * ti);
           opos[c][1] = pos_of(col0 + 8 * c + 2 * ti + 1);
-          qrow[c] = qrow_of(col0 + 8 * c + gi);
         }
         uint32_t skip = 0;
         auto issue = [&](int s, int i) {   // i = 0, 1, 2, ... in order
@@ -1353,10 +1414,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(Args<SC> a) {
         float zoff[CT], zscale0 = 0.0f;
 #pragma unroll
         for (int c = 0; c < CT; ++c) {
-          uint4 row[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            row[j] = qrow[c] ? reinterpret_cast<const uint4*>(qrow[c])[4 * ti + j] : make_uint4(0u, 0u, 0u, 0u);
+          if (!kEarly) fetch_q(c);
+          const uint4 (&row)[4] = qrows[c];
           float up = 1.0f;
           float zscale = a.sm_scale_log2 * (FMT == kI8 ? 16777216.0f : ks);
           if (a.dtype == S4KV_BF16) {
@@ -1685,7 +1744,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) window_kernel(Args<SC> a) {
       seg = 0;
       if (++b >= a.B) break;
       T = a.seq_lens[b];
-      pl = plan_of<FMT, SC>(T, a, b);
+      pl = plan_of_warp<FMT, SC>(T, a, b, own_span);
     }
   }
   if (pend) fail(-1);   // never expected: every issued copy is waited for
