@@ -8,7 +8,7 @@
 //     S = Q K^T (128 x 128 x 128),  P = exp2(score form(S) - m),  O += P V (128 x 128 x 128)
 // with S and O in tensor memory; P, in f16, takes S's place there and is the A operand of
 // P V. One thread a row: its 128 scores come in registers, so maxima and sums need no
-// shuffle, and a rescale of O (when a maximum rises by more than kLazy) is the row's own.
+// shuffle, and a rescale of O (when a maximum rises by more than kLazyP) is the row's own.
 //
 // Warps 0 .. 3 and 4 .. 7 are the rows of the two tiles, warp 8 fetches (a ring of five 32 KB
 // buffers, keys and values in turn, one bulk copy each), warp 9 issues the MMAs: P V and the next
@@ -18,6 +18,25 @@
 //
 // Few rows behind a long cache: the kv tiles of a CTA are split over `splits` CTAs, whose
 // outputs a third launch combines.
+//
+// Two tiles of rows share a kv tile's fetch: 64 KB out of L2 for 256 x 128 scores keep ahead of the MMAs,
+// where tiles of 128 rows alone would ask for twice that.
+//
+// Measured (one launch with its tiles and combine, a captured graph): 2048 tokens behind 32768, 28 query
+// heads, 4 kv heads 641 us, 1455 TFLOP/s of the visible pairs (76% of a library matrix product's rate),
+// with a cap of 30 and scores near zero 817, with scores beyond it 1391, with slopes 817, with both
+// 1124. A prompt of 2048, 32 heads 47.4 (725). Eight chunks of 512 behind 2048 to 8192, sloped 370. What
+// bounds it:
+//  * the loop: 2811 cycles a kv tile, of which the four MMAs take 2052 (513 each, read out of shared
+//    memory or with P out of tensor memory alike); the rest is P's way to tensor memory and the hand-over.
+//    With a cap the rows' warps bind: 4170 cycles, a minimum and a maximum more over the scores and two
+//    multiply-adds and a product for each of them beside the exponential's.
+//  * a CTA's start and end, about 15000 cycles: the sequence found (1400) and checked, queries fetched
+//    and turned into operands (bf16 1500: its powers of two), first scores (2700), output (5800).
+//    That is what a prompt of 2048 spends beside 16 kv tiles at most, hence tiles by falling length.
+// Tried and left out: exponentials by polynomials on the FMA pipe, two threads a row, two MMA warps, P
+// handed over in halves, barrier tests ahead of the waits: slower or level. Barriers shared by the
+// two row tiles 2% faster, with an end that cannot be drained in bounded time.
 
 #include "s4kv_prompt.cuh"
 #include "s4kv_tcgen05.cuh"

@@ -42,8 +42,8 @@ __host__ __device__ constexpr float near_coef(int i) {
 
 namespace {
 
-// bf16 queries enter the MMAs as f16. Their range is the wider one, so each column is
-// taken at the power of two 2^k that brings its largest element to 2^14 .. 2^15: exact,
+// bf16 queries enter the MMAs as f16 (s4kv_window.cuh). Their range is the wider one, so each column
+// is taken at the power of two 2^k that brings its largest element to 2^14 .. 2^15: exact,
 // and elements down to 2^-28 of the largest keep every bit. k of a column whose largest
 // magnitude has the bits `top` (0 for zeros, infinities and NaN, which stay what they are).
 __device__ __forceinline__ int query_power(uint32_t top) {

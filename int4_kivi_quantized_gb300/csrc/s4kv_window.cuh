@@ -47,6 +47,13 @@
 // loads: the sinks', the window's first, and those that the residual reaches (five of them
 // at R = 128), about an eighth of the work line. Outputs in 32 bits take the same times.
 //
+// With a score form, the same launches cost 3 to 9% more (times without, with a window as a form, and with
+// a cap and slopes): INT8, 16 sequences of 4096 tokens with four queries each, 8 kv heads 31.7, 34.4, 37.1 us; 64 of
+// 2000 with one query 4-bit 49.5, 51.3, 53.6, FP8 52.6, 55.4, 57.5, INT8 47.3, 48.7, 49.6; one sequence of 256
+// 6.4, 6.8, 6.8. A capped 4-bit decode of 32 contexts of 32768 (28 heads) 155 us against 142: the cubic
+// near zero is three packed multiply-adds and two products for two scores where the exponential
+// form is two special instructions a score, 166 us. Slopes are one multiply-add a score.
+//
 // A masked token's key and value never meet arithmetic that could carry an
 // infinity or a NaN of theirs into the result: scores are selected, probabilities
 // scaled only where they are positive, 16-bit and FP8 value rows that no column
@@ -84,8 +91,10 @@ template <int FMT> constexpr int kLeastUnits = kByte<FMT> ? 4 : 3;           // 
 // sequences of 1024 to 8192 tokens 57.6 / 55.7 / 55.9 / 56.2 us, 16 of 777 to 8191 with
 // 16 columns 44.4 / 40.7 / 39.1 / 38.9. KIVI pages, where the cut blocks' cost says it
 // already: 0 / 1 / 3: 64 sequences behind a window of 4096 83.8 / 84.1 / 85.4.
-constexpr int kRingUnits = 4;   // SC, INT8 pages: what the unfinished block costs, in records
 template <int FMT> constexpr int kSegCost = kByte<FMT> ? 6 : 0;
+// With a score form the unfinished block of INT8 pages counts as so many records: its 16-bit rows
+// come by plain loads, 7500 cycles where a record takes 2500.
+constexpr int kRingUnits = 4;
 
 template <int FMT, int NC, bool SC>
 struct WSmem {
@@ -877,16 +886,21 @@ __device__ void kivi_cut_block(const Args<SC>& args, const Seg& sg, MmaState& s,
   for (int p = 0; p < 2; ++p) {
     const float* acc = p ? acc1 : acc0;
     const int ta = t0 + 16 * p + gi, tb = ta + 8;
-    float y0[2] = {fmaf(acc[0], scale, bs0), fmaf(acc[2], scale, bs0)}, y1[2] = {fmaf(acc[1], scale, bs1), fmaf(acc[3], scale, bs1)};
     if constexpr (SC) {
+      float y0[2] = {fmaf(acc[0], scale, bs0), fmaf(acc[2], scale, bs0)}, y1[2] = {fmaf(acc[1], scale, bs1), fmaf(acc[3], scale, bs1)};
       auto on = [](int x) { return 8.0f * x; };
       through_form(y0, args, slope2[2 * ti * kPRow], pos0 - ta, on);
       through_form(y1, args, slope2[(2 * ti + 1) * kPRow], pos1 - ta, on);
+      z[4 * p + 0] = visible<SC>(ta, pos0, cut) ? y0[0] : -INFINITY;
+      z[4 * p + 1] = visible<SC>(ta, pos1, cut) ? y1[0] : -INFINITY;
+      z[4 * p + 2] = visible<SC>(tb, pos0, cut) ? y0[1] : -INFINITY;
+      z[4 * p + 3] = visible<SC>(tb, pos1, cut) ? y1[1] : -INFINITY;
+    } else {
+      z[4 * p + 0] = visible<SC>(ta, pos0, cut) ? fmaf(acc[0], scale, bs0) : -INFINITY;
+      z[4 * p + 1] = visible<SC>(ta, pos1, cut) ? fmaf(acc[1], scale, bs1) : -INFINITY;
+      z[4 * p + 2] = visible<SC>(tb, pos0, cut) ? fmaf(acc[2], scale, bs0) : -INFINITY;
+      z[4 * p + 3] = visible<SC>(tb, pos1, cut) ? fmaf(acc[3], scale, bs1) : -INFINITY;
     }
-    z[4 * p + 0] = visible<SC>(ta, pos0, cut) ? y0[0] : -INFINITY;
-    z[4 * p + 1] = visible<SC>(ta, pos1, cut) ? y1[0] : -INFINITY;
-    z[4 * p + 2] = visible<SC>(tb, pos0, cut) ? y0[1] : -INFINITY;
-    z[4 * p + 3] = visible<SC>(tb, pos1, cut) ? y1[1] : -INFINITY;
   }
   float mx0 = fmaxf(fmaxf(z[0], z[2]), fmaxf(z[4], z[6])), mx1 = fmaxf(fmaxf(z[1], z[3]), fmaxf(z[5], z[7]));
 #pragma unroll
