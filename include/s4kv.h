@@ -439,7 +439,8 @@ int s4kv_score_attention(s4kv_cache* cache, int layer, const s4kv_scores* scores
  * combine. Restored keys and values beyond 65504 in magnitude count as infinities there.
  * A query that sees a token whose value row is not finite (or so large) gets NaN; tokens
  * that it does not see never reach its row, whatever they hold. Short chunks of equal length
- * (1 to 16 tokens) are read faster by s4kv_score_attention. */
+ * (1 to 16 tokens) are read faster by s4kv_score_attention up to 48 query columns (tokens
+ * times query heads of a kv head), on 8-bit pages up to 64; beyond, the two are level. */
 int s4kv_prompt_workspace_bytes(const s4kv_cache* cache, int n, int num_q, int num_q_heads, int max_seq_len,
                                 long long sum_seq_lens, size_t* bytes);
 int s4kv_prompt_attention(s4kv_cache* cache, int layer, const s4kv_scores* scores, const void* q, int num_q,

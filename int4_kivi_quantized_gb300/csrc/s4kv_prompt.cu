@@ -29,8 +29,8 @@
 // bounds it:
 //  * the loop: 2811 cycles a kv tile, of which the four MMAs take 2052 (513 each, read out of shared
 //    memory or with P out of tensor memory alike); the rest is P's way to tensor memory and the hand-over.
-//    With a cap the rows' warps bind: 4170 cycles, a minimum and a maximum more over the scores and two
-//    multiply-adds and a product for each of them beside the exponential's.
+//    With a cap the rows' warps bind: 4170 cycles, a minimum more over the scores, and for two of them a
+//    product and three multiply-adds (packed) beside the exponentials'.
 //  * a CTA's start and end, about 15000 cycles: the sequence found (1400) and checked, queries fetched
 //    and turned into operands (bf16 1500: its powers of two), first scores (2700), output (5800).
 //    That is what a prompt of 2048 spends beside 16 kv tiles at most, hence tiles by falling length.

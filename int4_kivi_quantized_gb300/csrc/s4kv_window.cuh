@@ -1895,17 +1895,18 @@ void one_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int cluster,
   cfg->numAttrs = cluster > 1 ? 2 : 1;
 }
 
-// Clusters of 16 CTAs that the current device holds at once.
+// Clusters of `size` CTAs that the current device holds at once.
 template <int FMT, int NC, bool SC>
-int clusters_of_16() {
-  static int known[kMaxDevices] = {};   // 1 + the answer
+int clusters_of(int size) {   // 2, 4, 8 or 16
+  static int known_of[17][kMaxDevices] = {};   // 1 + the answer
+  int(&known)[kMaxDevices] = known_of[size];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices || one_ready<FMT, NC, SC>() != cudaSuccess) return 0;
   std::lock_guard<std::mutex> guard(g_lock);
   if (known[dev] == 0) {
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    one_config<FMT, NC, SC>(&cfg, attr, 16, 1, nullptr);
+    one_config<FMT, NC, SC>(&cfg, attr, size, 1, nullptr);
     int n = 0;
     if (cudaOccupancyMaxActiveClusters(&n, window_kernel<FMT, NC, true, SC>, &cfg) != cudaSuccess) {
       cudaGetLastError();
@@ -1936,11 +1937,10 @@ int cluster_of(const WindowArgs& a, int num_sms) {
   const long long blocks = (a.max_seq_len < seen ? a.max_seq_len : seen) / kBlock<FMT> + 2;   // of a segment, at most
   int c = 1;
   while (c < 8 && 2 * c * segs <= num_sms && blocks > static_cast<long long>(c) * kWarps) c *= 2;
-  if (c == 8 && segs <= 6 && blocks > 16LL * kWarps) {
-    // clusters of 16 fill a GPC each: only where every one of them is resident at once
-    const int resident = clusters_of_16<FMT, NC, SC>();
-    if (segs <= resident) c = 16;
-  }
+  if (c == 8 && segs <= 6 && blocks > 16LL * kWarps) c = 16;   // (clusters of 16 fill a GPC each)
+  // only what is resident at once: of 16 clusters of 8 some wait for a second pass (two sequences of 3000
+  // tokens, 8 kv heads, one query: 4-bit 21.1 us, clusters of 4 12.2, slices 15.8; INT8 16.2, 10.9, 12.7)
+  while (c > 1 && segs > clusters_of<FMT, NC, SC>(c)) c /= 2;
   if (a.form == 0 && blocks * kBlock<FMT> > static_cast<long long>(c) * kWarps * kOneTokens) return 0;
   return c;
 }
