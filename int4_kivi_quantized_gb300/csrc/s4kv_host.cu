@@ -890,7 +890,8 @@ int s4kv_prompt_attention(s4kv_cache* cache, int layer, const s4kv_scores* score
   a.kv_grid = a.form.window < kNoWindow && left < z.kv_tiles ? static_cast<int>(left) : z.kv_tiles;
   a.splits = prompt_splits(z, a.H, cache->num_sms, (seen + kKvTile - 1) / kKvTile);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (z.kv_tiles > 0 && launch_tiles(a, st) != cudaSuccess) return S4KV_ERR_CUDA;
+  if (a.kv_grid == 0) a.kv_grid = 1;   // (no sequence may have a token: offsets are still looked at)
+  if (launch_tiles(a, st) != cudaSuccess) return S4KV_ERR_CUDA;
   return launch_prompt(a, st) == cudaSuccess ? S4KV_OK : S4KV_ERR_CUDA;
 }
 

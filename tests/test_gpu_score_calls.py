@@ -112,6 +112,30 @@ def test_sequences_without_a_chunk_are_not_looked_at():
     p.f.ok()
 
 
+def test_bounds_of_zero():
+    """A call that says that no sequence has a token: the offsets are still looked at, the sequences reported."""
+    p = Pair()
+    got = p.prompt(longest=0, total=0)
+    assert p.status() == (s4.S4KV_ERR_DEVICE, s4.S4KV_DEV_BAD_LENGTH) and not got.any()
+    p.prompt(longest=0, total=0, cu=p.f.i32([0, 50, 40, 220]))
+    assert p.status() == (s4.S4KV_ERR_DEVICE, s4.S4KV_DEV_BAD_CU)
+    got = p.attend(longest=0)
+    assert p.status() == (s4.S4KV_ERR_DEVICE, s4.S4KV_DEV_BAD_LENGTH) and not got.any()
+
+
+def test_calls_of_no_sequences():
+    p = Pair()
+    c, none, no_rows = p.f.cache, p.f.i32([]), p.f.bt[:0]
+    assert c.prompt(0, p.q[:0], p.f.i32([0]), no_rows, none, 0, 0).shape == (0, 8, 128)
+    assert c.attend(0, p.q1[:0], no_rows, none, 0, p.scores).shape == (0, 2, 8, 128)
+    refs = torch.zeros(c.cfg.num_pages, dtype=torch.int32, device="cuda")
+    assert c.take_pages(refs, no_rows, none, none).shape == (0,)
+    assert c.fork(refs, p.f.bt[:1].contiguous(), none, none, none).shape == (0,)
+    c.release_pages(refs, no_rows, none, none)
+    assert not refs.any()
+    p.f.ok()
+
+
 @pytest.mark.parametrize("which", ["prompt", "attend"])
 def test_ends_of_the_integers(which):
     """first and prefix at both ends of their type: everything, nothing, and as without them."""
