@@ -379,9 +379,10 @@ class Scores:
     within the newest `window` tokens (0: all) and the first `num_sinks`."""
 
     def __init__(self, cap=0.0, slopes=None, window=0, num_sinks=0):
-        import torch
-        if slopes is not None and (slopes.dim() != 1 or slopes.dtype != torch.float32 or not slopes.is_contiguous()):
-            raise ValueError("the slopes are a contiguous fp32 tensor [H_q]")
+        if slopes is not None:
+            import torch
+            if slopes.dim() != 1 or slopes.dtype != torch.float32 or not slopes.is_contiguous():
+                raise ValueError("the slopes are a contiguous fp32 tensor [H_q]")
         if cap != 0 and not 2.0 ** -60 <= cap <= 2.0 ** 60:
             raise ValueError("a cap is 2^-60 .. 2^60, or 0 for none")
         if window < 0 or num_sinks < 0:
@@ -757,11 +758,12 @@ class KVCache:
             raise ValueError("block_table has fewer rows than there are sequences")
         return rows, width
 
-    def _taken(self, taken, n, stream):
+    def _taken(self, taken, like, stream):
+        """`taken`, checked, or a new tensor like the checked one."""
         torch = self._torch
         if taken is None:
-            return self._made(stream, torch.empty, (n,), dtype=torch.int32, device=self.pool.device)
-        self._tensor(taken, "taken", torch.int32, (n,))
+            return torch.empty_like(like) if stream is None else self._made(stream, torch.empty_like, like)
+        self._tensor(taken, "taken", torch.int32, like.shape)
         return taken
 
     @_on_its_device
@@ -774,7 +776,7 @@ class KVCache:
         self._tensor(lens, "lens", torch.int32, (n,))
         self._tensor(new_lens, "new_lens", torch.int32, (n,))
         rows, width = self._pages(refs, block_table, slot_ids, n)
-        taken = self._taken(taken, n, stream)
+        taken = self._taken(taken, lens, stream)
         _check(_lib.s4kv_take_pages(self.h, refs.data_ptr(), block_table.data_ptr(), width, rows, lens.data_ptr(),
                                     new_lens.data_ptr(), _address(slot_ids), n, taken.data_ptr(), self._handle(stream)),
                "s4kv_take_pages")
@@ -803,7 +805,7 @@ class KVCache:
         self._tensor(dst, "dst", torch.int32, (n,))
         self._tensor(seq_lens, "seq_lens", torch.int32, (n,))
         rows, width = self._pages(refs, block_table, src, n)
-        taken = self._taken(taken, n, stream)
+        taken = self._taken(taken, src, stream)
         _check(_lib.s4kv_fork(self.h, refs.data_ptr(), block_table.data_ptr(), width, rows, src.data_ptr(), dst.data_ptr(),
                               seq_lens.data_ptr(), n, taken.data_ptr(), self._handle(stream)), "s4kv_fork")
         return taken

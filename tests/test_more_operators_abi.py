@@ -2,12 +2,17 @@
 the plain model that the GPU tests compare with."""
 import ctypes
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
 
 import int4_kivi_quantized_gb300 as s4
 from score_model import attention, seen_of
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 def test_calls_without_a_cache_are_refused():
@@ -61,3 +66,13 @@ def test_plain_scores_are_the_formula():
     z0, z1 = 4 * math.tanh(6 / 4) - 0.5, 4 * math.tanh(-2 / 4)
     p0 = math.exp(z0) / (math.exp(z0) + math.exp(z1))
     assert abs(float(P[0, 0, 0]) - p0) < 1e-12 and abs(float(out[0, 0, 3]) - (p0 + 5 * (1 - p0))) < 1e-6
+
+
+def test_the_binding_is_imported_without_torch():
+    """Sizes and structures need the library alone."""
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "import int4_kivi_quantized_gb300 as s4\n"
+            "print(s4.s4kv_cache_bytes(s4.make_config(1, 10, 2, 64, 4))[1], s4.Scores(50.0).cap)")
+    got = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=ROOT)
+    assert got.returncode == 0, got.stderr
+    assert got.stdout.split()[1] == "50.0"
