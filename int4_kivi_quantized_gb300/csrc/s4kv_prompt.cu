@@ -49,8 +49,9 @@ namespace {
 
 constexpr int kRowWarps = 8, kLoadWarp = 8, kMmaWarp = 9;
 constexpr int kThreads = 384;        // (two more warps make a warpgroup of the last four)
-// Registers: 168 a thread at launch, 208 for the rows' two warpgroups and 88 for the third.
-constexpr int kRegsRow = 208, kRegsRest = 88;
+// Registers: 168 a thread at launch, 224 for the rows' two warpgroups and 56 for the third (208 and 88: the capped
+// rows spill more, 32k 831 us against 820).
+constexpr int kRegsRow = 224, kRegsRest = 56;
 static_assert(2 * kRegsRow + kRegsRest <= 3 * 168, "the shares are what the launch holds");
 constexpr int kBufs = 5;
 constexpr float kLazyP = 8.0f;       // P up to 2^8 before its sum divides it: exact enough in f16, and rescales are rare
@@ -181,11 +182,15 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
     sm.hi = -1;
   }
   __syncthreads();
-  stream_wait();
+  // What the caller's work made is there: the tiles' launch has waited for it, and lets this one start then. This
+  // kernel reads it past the first cache, and waits for the tiles themselves further down (on every path, so
+  // that its end is theirs).
   Place pl;
   // the last tiles of a sequence, whose rows see the most, start first, of every kv head
   const int q_tile = static_cast<int>((gridDim.x - 1 - blockIdx.x) / a.H), h = static_cast<int>(blockIdx.x % a.H);
   const int where = find_tile<kThreads, true>(a, q_tile, pl);
+  // (no branch: a path of its own would cost the loop registers)
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %0, 0;\n\t@p griddepcontrol.wait;\n\t}" ::"r"(where) : "memory");
   if (where != kFound) return;
   const int z = blockIdx.y, b = pl.b, g = a.g, cu0 = pl.cu0, m = pl.m, T = pl.T;
   const int row0 = pl.tile * kQRows;
@@ -216,10 +221,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
       const int r = 32 * warp + 2 * k + (lane >> 4);
-      v[k] = r < rows ? reinterpret_cast<const uint4*>(a.q + out_row(r) * kD)[lane & 15] : make_uint4(0u, 0u, 0u, 0u);
+      v[k] = r < rows ? __ldcg(reinterpret_cast<const uint4*>(a.q + out_row(r) * kD) + (lane & 15)) : make_uint4(0u, 0u, 0u, 0u);
     }
   }
-  const int slot = a.slot_ids ? a.slot_ids[b] : b;
+  const int slot = a.slot_ids ? __ldcg(a.slot_ids + b) : b;
   int arg;
   const int why = refused(a, pl, slot, h, arg);
   if (why && tid == 0) report(a.status, S4KV_ERR_DEVICE, why, arg);
@@ -286,6 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)), "n"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  stream_wait();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (a combine kernel)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

@@ -84,8 +84,10 @@ __device__ int find_tile(const PromptArgs& a, int idx, Place& place) {
   __shared__ int tot[2][W];
   __shared__ Place found;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the attention kernel looks while the launch before it still runs, and so past the first cache)
+  auto look = [](const int* x) { return BY_Q ? __ldcg(x) : *x; };
   if (a.n <= 32) {   // a sequence a lane, every warp for itself
-    const int b = lane, c0 = b < a.n ? a.cu_q[b] : 0, c1 = b < a.n ? a.cu_q[b + 1] : 0, T = b < a.n ? a.seq_lens[b] : 0;
+    const int b = lane, c0 = b < a.n ? look(a.cu_q + b) : 0, c1 = b < a.n ? look(a.cu_q + b + 1) : 0, T = b < a.n ? look(a.seq_lens + b) : 0;
     const bool wrong = c0 < 0 || c1 < c0 || c1 > a.num_q || (b == 0 && c0 != 0) || (b == a.n - 1 && c1 != a.num_q);
     if (__any_sync(0xffffffffu, wrong)) return kMalformed;
     const int m = c1 - c0, qt = q_tiles_of(a, m), kt = kv_tiles_of(a, m, T);
@@ -108,16 +110,16 @@ __device__ int find_tile(const PromptArgs& a, int idx, Place& place) {
   }
   int bad = 0, carry_q = 0, carry_k = 0;
   if (tid == 0) {
-    bad = a.cu_q[0] != 0 || a.cu_q[a.n] != a.num_q;
+    bad = look(a.cu_q) != 0 || look(a.cu_q + a.n) != a.num_q;
     found.b = -1;
   }
   for (int base = 0; base < a.n; base += THREADS) {
     const int b = base + tid;
     int qt = 0, kt = 0, c0 = 0, m = 0, T = 0;
     if (b < a.n) {
-      const int c1 = a.cu_q[b + 1];
-      c0 = a.cu_q[b];
-      T = a.seq_lens[b];
+      const int c1 = look(a.cu_q + b + 1);
+      c0 = look(a.cu_q + b);
+      T = look(a.seq_lens + b);
       m = c1 - c0;
       if (c0 < 0 || c1 < c0 || c1 > a.num_q) {
         bad = 1;

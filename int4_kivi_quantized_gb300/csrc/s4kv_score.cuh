@@ -74,9 +74,9 @@ struct Span {
 __device__ __forceinline__ Span span_of(const ScoreForm& f, int p, int T, long long at, int b) {
   Span s;
   s.lo = max(0, p - f.window + 1);
-  if (f.first) s.lo = max(s.lo, f.first[at]);
+  if (f.first) s.lo = max(s.lo, __ldcg(f.first + at));
   s.hi = p;
-  if (f.prefix) s.hi = min(max(p, min(max(f.prefix[b], 0), T) - 1), T - 1);
+  if (f.prefix) s.hi = min(max(p, min(max(__ldcg(f.prefix + b), 0), T) - 1), T - 1);
   return s;
 }
 __device__ __forceinline__ bool sees(const Span& s, int t, int sinks) { return t <= s.hi && (t >= s.lo || t < sinks); }

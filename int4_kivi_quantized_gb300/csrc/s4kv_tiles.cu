@@ -69,6 +69,8 @@ struct TileRows {
 template <int FMT>
 __global__ void __launch_bounds__(kThreads, 4) tiles_kernel(PromptArgs a) {
   stream_wait();
+  // the attention kernel may start: it waits for this one where it needs the tiles
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   Place p;
   const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool values = blockIdx.z;

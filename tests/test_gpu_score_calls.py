@@ -112,6 +112,43 @@ def test_sequences_without_a_chunk_are_not_looked_at():
     p.f.ok()
 
 
+@pytest.mark.parametrize("which", ["prompt", "attend"])
+def test_inputs_written_right_before(which):
+    """Queries, offsets, lengths, first tokens and prefixes that the work queued just before has still to write, other
+    ones call by call: the launches that start early read none of them too soon."""
+    p = Pair(chunks=(40, 9, 171))
+    call = getattr(p, which)
+    n = (220,) if which == "prompt" else (3, 2)
+    q0 = p.q if which == "prompt" else p.q1
+    g = torch.Generator().manual_seed(3)
+    sets = []
+    for i in range(4):
+        first = torch.randint(0, 60, n, generator=g, dtype=torch.int32).cuda()
+        m = torch.tensor([0, 10 + 20 * i, 30 + 20 * i, 220], dtype=torch.int32).cuda()
+        sets.append(dict(q=(q0 * (0.5 + 0.25 * i)).contiguous(), first=first, prefix=p.f.i32([5 * i, 40, 3]), cu=m))
+    if which == "attend":
+        for s in sets:
+            s.pop("cu")
+    else:   # (the last chunk is longer than its sequence: reported, zeros)
+        for s in sets:
+            s["cu"] = p.f.i32([0, 40, 49, 220]) if s["cu"][3] - s["cu"][2] > 171 else s["cu"]
+    want = [call(**s).clone() for s in sets]
+    p.status()
+    held = {k: torch.zeros_like(v) for k, v in sets[0].items()}
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(3):
+        for s in sets:
+            torch.cuda._sleep(300_000)
+            for k, v in s.items():
+                held[k].copy_(v)
+            got.append(call(**held))
+    torch.cuda.synchronize()
+    p.status()
+    for i, x in enumerate(got):
+        assert torch.equal(x, want[i % 4]), i
+
+
 def test_bounds_of_zero():
     """A call that says that no sequence has a token: the offsets are still looked at, the sequences reported."""
     p = Pair()
