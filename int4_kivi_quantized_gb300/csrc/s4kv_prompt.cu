@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
     if (tid < rows) {
       const int i = token_of(tid);
       pos = T - m + i;
-      sp = span_of(a.form, pos, T, static_cast<long long>(cu0) + i, b);
+      sp = span_of<true>(a.form, pos, T, static_cast<long long>(cu0) + i, b);
     }
     const bool range = tid < rows && sp.lo <= sp.hi;
     const int lo = __reduce_min_sync(0xffffffffu, range ? sp.lo : 0x7fffffff);

@@ -71,12 +71,15 @@ __device__ __forceinline__ float far_cap(float score, float by, float cap) { ret
 struct Span {
   int lo, hi;
 };
+// EARLY: read past the first cache, by a kernel that may look while a launch before it still runs.
+template <bool EARLY = false>
 __device__ __forceinline__ Span span_of(const ScoreForm& f, int p, int T, long long at, int b) {
+  auto look = [](const int* x) { return EARLY ? __ldcg(x) : *x; };
   Span s;
   s.lo = max(0, p - f.window + 1);
-  if (f.first) s.lo = max(s.lo, __ldcg(f.first + at));
+  if (f.first) s.lo = max(s.lo, look(f.first + at));
   s.hi = p;
-  if (f.prefix) s.hi = min(max(p, min(max(__ldcg(f.prefix + b), 0), T) - 1), T - 1);
+  if (f.prefix) s.hi = min(max(p, min(max(look(f.prefix + b), 0), T) - 1), T - 1);
   return s;
 }
 __device__ __forceinline__ bool sees(const Span& s, int t, int sinks) { return t <= s.hi && (t >= s.lo || t < sinks); }
