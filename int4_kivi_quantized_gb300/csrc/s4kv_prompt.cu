@@ -23,9 +23,9 @@
 // where tiles of 128 rows alone would ask for twice that.
 //
 // Measured (one launch with its tiles and combine, a captured graph): 2048 tokens behind 32768, 28 query
-// heads, 4 kv heads 641 us, 1455 TFLOP/s of the visible pairs (76% of a library matrix product's rate),
-// with a cap of 30 and scores near zero 817, with scores beyond it 1391, with slopes 817, with both
-// 1124. A prompt of 2048, 32 heads 47.4 (725). Eight chunks of 512 behind 2048 to 8192, sloped 370. What
+// heads, 4 kv heads 635 us, 1466 TFLOP/s of the visible pairs (77% of a library matrix product's rate),
+// with a cap of 30 and scores near zero 816, with scores beyond it 1388, with slopes 812, with both
+// 1113. A prompt of 2048, 32 heads 45.4 (758). Eight chunks of 512 behind 2048 to 8192, sloped 368. What
 // bounds it:
 //  * the loop: 2811 cycles a kv tile, of which the four MMAs take 2052 (513 each, read out of shared
 //    memory or with P out of tensor memory alike); the rest is P's way to tensor memory and the hand-over.
@@ -33,7 +33,8 @@
 //    product and three multiply-adds (packed) beside the exponentials'.
 //  * a CTA's start and end, about 15000 cycles: the sequence found (1400) and checked, queries fetched
 //    and turned into operands (bf16 1500: its powers of two), first scores (2700), output (5800).
-//    That is what a prompt of 2048 spends beside 16 kv tiles at most, hence tiles by falling length.
+//    That is what a prompt of 2048 spends beside 16 kv tiles at most, hence tiles by falling length, and
+//    the start runs beside the tiles' launch where that leaves SMs free (a prompt of 512 19.6 -> 16.8 us).
 // Tried and left out: exponentials by polynomials on the FMA pipe, two threads a row, two MMA warps, P
 // handed over in halves, barrier tests ahead of the waits: slower or level. Barriers shared by the
 // two row tiles 2% faster, with an end that cannot be drained in bounded time.
