@@ -292,8 +292,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sm.tmem)), "n"(kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
-  stream_wait();
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (a combine kernel)
+  stream_wait();   // (no early start for what comes behind: its CTAs would crowd the SMs that end first)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
