@@ -23,9 +23,9 @@
 // where tiles of 128 rows alone would ask for twice that.
 //
 // Measured (one launch with its tiles and combine, a captured graph): 2048 tokens behind 32768, 28 query
-// heads, 4 kv heads 635 us, 1466 TFLOP/s of the visible pairs (77% of a library matrix product's rate),
-// with a cap of 30 and scores near zero 816, with scores beyond it 1388, with slopes 812, with both
-// 1113. A prompt of 2048, 32 heads 45.4 (758). Eight chunks of 512 behind 2048 to 8192, sloped 368. What
+// heads, 4 kv heads 638 us, 1462 TFLOP/s of the visible pairs (77% of a library matrix product's rate),
+// with a cap of 30 and scores near zero 822, with scores beyond it 1388, with slopes 815, with both
+// 1111. A prompt of 2048, 32 heads 44 to 46 (780 to 750). Eight chunks of 512 behind 2048 to 8192, sloped 368. What
 // bounds it:
 //  * the loop: 2811 cycles a kv tile, of which the four MMAs take 2052 (513 each, read out of shared
 //    memory or with P out of tensor memory alike); the rest is P's way to tensor memory and the hand-over.
