@@ -136,15 +136,23 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
 
 // One row's scores of a kv tile, from S to log2 units.
 struct RowScore {
-  float mul;       // no cap: S to log2 units. cap: S to x / cap
+  float mul;       // no cap: S to log2 units. cap: S to x / cap. A normal number
   float cap2;      // cap log2(e)
   float slope2;    // slope log2(e)
 };
 
 // The cap of a score near zero against it (s4kv_score.cuh), from S to log2 units: S Q(S^2) with Q's
-// coefficients at hand per row.
+// coefficients at hand per row. The last of them has the seventh power of x / (cap S): where it or the
+// first is no normal number (large and tiny caps, rows of small queries), u = S mul comes first.
 struct NearCap {
   float c[kNearCoefs];
+  __device__ __forceinline__ NearCap(float lin, float mul) {   // lin: S to x in log2 units
+    float by = lin;
+#pragma unroll
+    for (int k = 0; k < kNearCoefs; ++k, by *= mul * mul) c[k] = near_coef(k) * by;
+  }
+  __device__ __forceinline__ static bool normal(float x) { return fabsf(x) > 1e-36f && fabsf(x) < 1e36f; }
+  __device__ __forceinline__ bool folds() const { return normal(c[0]) && normal(c[kNearCoefs - 1]); }   // (those between lie between)
   __device__ __forceinline__ float2 inner(float2 s) const {   // Q(S^2)
     const float2 w = __fmul2_rn(s, s);
     float2 p = __ffma2_rn(w, make_float2(c[3], c[3]), make_float2(c[2], c[2]));
@@ -154,12 +162,23 @@ struct NearCap {
   __device__ __forceinline__ float operator()(float s) const { return s * inner(make_float2(s, s)).x; }
 };
 
-// x from S to capped scores in log2 units.
-__device__ __forceinline__ void through_cap(float (&x)[128], const RowScore& f, const NearCap& near, bool near_zero) {
-  if (near_zero) {
+// x from S to capped scores in log2 units, near zero (by the folded coefficients or not) or anywhere.
+__device__ __forceinline__ void through_cap(float (&x)[128], const RowScore& f, const NearCap& near, bool near_zero, bool folded, float lin) {
+  if (near_zero && folded) {
 #pragma unroll
     for (int i = 0; i < 128; i += 2) {
       const float2 s = make_float2(x[i], x[i + 1]), y = __fmul2_rn(s, near.inner(s));
+      x[i] = y.x;
+      x[i + 1] = y.y;
+    }
+  } else if (near_zero) {
+#pragma unroll
+    for (int i = 0; i < 128; i += 2) {
+      const float2 s = make_float2(x[i], x[i + 1]), u = __fmul2_rn(s, make_float2(f.mul, f.mul)), w = __fmul2_rn(u, u);
+      float2 p = make_float2(near_coef(3), near_coef(3));
+#pragma unroll
+      for (int k = kNearCoefs - 2; k >= 0; --k) p = __ffma2_rn(p, w, make_float2(near_coef(k), near_coef(k)));
+      const float2 y = __fmul2_rn(__fmul2_rn(s, make_float2(lin, lin)), p);
       x[i] = y.x;
       x[i + 1] = y.y;
     }
@@ -423,16 +442,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
       const uint32_t s_at = tmem + 128 * s + t_row, o_at = tmem + 256 + 128 * s + t_row;
       constexpr float kLog2e = 1.4426950408889634f;
       RowScore f;
-      const float scale = a.sm_scale * sm.up[tid];
-      f.mul = CAP ? scale / a.form.cap : scale * kLog2e;
+      const float scale = a.sm_scale * sm.up[tid], lin = scale * kLog2e;
+      f.mul = fminf(fmaxf(CAP ? scale / a.form.cap : lin, 0x1p-126f), 0x1p127f);   // (zero times it is zero, -inf -inf)
       f.cap2 = CAP ? a.form.cap * kLog2e : 0.0f;
       f.slope2 = SLOPE ? a.form.slopes[h * g + (row0 + tid) % g] * kLog2e : 0.0f;
-      NearCap near;
-      {
-        float by = f.cap2 * f.mul;
-#pragma unroll
-        for (int k = 0; k < kNearCoefs; ++k, by *= f.mul * f.mul) near.c[k] = near_coef(k) * by;
-      }
+      if (CAP) sm.up[tid] = lin;   // (this thread's own; seldom asked for)
+      const NearCap near(lin, f.mul);
+      const bool folded = CAP && __all_sync(0xffffffffu, near.folds());
       float mx = -INFINITY, l = 0.0f;
       bool ok = true;
       auto wild_of = [&](int i) { return *reinterpret_cast<const uint4*>(a.bad + 4 * tile_at(i)); };
@@ -475,10 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
           const float least = fminf(fminf(t4[0], t4[1]), fminf(t4[2], t4[3]));
           top = largest();
           far = fmaxf(top, -least);
-          // (the last coefficient has the seventh power of f.mul: a normal number, or it is not used)
-          const bool near_zero = __all_sync(0xffffffffu, far * f.mul <= kNearCap && fabsf(near.c[kNearCoefs - 1]) > 1e-36f);
-          raw = raw && near_zero;
-          if (!raw) through_cap(x, f, near, near_zero);
+          const bool near_zero = __all_sync(0xffffffffu, far * f.mul <= kNearCap);
+          raw = raw && near_zero && folded;
+          if (!raw) through_cap(x, f, near, near_zero, folded, sm.up[tid]);
           in = 1.0f;
         }
         if constexpr (SLOPE) {
