@@ -668,13 +668,16 @@ __device__ __forceinline__ void ring_block(const Args<SC>& args, const uint16_t*
       z[c][1] = s0[2 * c + 1] * scale;
       z[c][2] = s1[2 * c] * scale;
       z[c][3] = s1[2 * c + 1] * scale;
+      bool sees[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        sees[x] = visible<SC>(cut.tok0 + 2 * ti + (x & 1) + 8 * (x >> 1), pos[c], cut);
+        if (SC && !sees[x]) z[c][x] = 0.0f;   // (no say in how the others are capped)
+      }
       if constexpr (SC)
         through_form(z[c], args, slope2[8 * c + gi], pos[c] - cut.tok0 - 2 * ti, lane_token);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const int t = cut.tok0 + 2 * ti + (x & 1) + 8 * (x >> 1);
-        z[c][x] = visible<SC>(t, pos[c], cut) ? z[c][x] : -INFINITY;
-      }
+      for (int x = 0; x < 4; ++x) z[c][x] = sees[x] ? z[c][x] : -INFINITY;
     }
   }
   byte_softmax<NC, true>(s, z);
@@ -887,14 +890,17 @@ __device__ void kivi_cut_block(const Args<SC>& args, const Seg& sg, MmaState& s,
     const float* acc = p ? acc1 : acc0;
     const int ta = t0 + 16 * p + gi, tb = ta + 8;
     if constexpr (SC) {
-      float y0[2] = {fmaf(acc[0], scale, bs0), fmaf(acc[2], scale, bs0)}, y1[2] = {fmaf(acc[1], scale, bs1), fmaf(acc[3], scale, bs1)};
+      const bool a0 = visible<SC>(ta, pos0, cut), a1 = visible<SC>(ta, pos1, cut), b0 = visible<SC>(tb, pos0, cut), b1 = visible<SC>(tb, pos1, cut);
+      // (a masked score has no say in how the others are capped)
+      float y0[2] = {a0 ? fmaf(acc[0], scale, bs0) : 0.0f, b0 ? fmaf(acc[2], scale, bs0) : 0.0f};
+      float y1[2] = {a1 ? fmaf(acc[1], scale, bs1) : 0.0f, b1 ? fmaf(acc[3], scale, bs1) : 0.0f};
       auto on = [](int x) { return 8.0f * x; };
       through_form(y0, args, slope2[2 * ti * kPRow], pos0 - ta, on);
       through_form(y1, args, slope2[(2 * ti + 1) * kPRow], pos1 - ta, on);
-      z[4 * p + 0] = visible<SC>(ta, pos0, cut) ? y0[0] : -INFINITY;
-      z[4 * p + 1] = visible<SC>(ta, pos1, cut) ? y1[0] : -INFINITY;
-      z[4 * p + 2] = visible<SC>(tb, pos0, cut) ? y0[1] : -INFINITY;
-      z[4 * p + 3] = visible<SC>(tb, pos1, cut) ? y1[1] : -INFINITY;
+      z[4 * p + 0] = a0 ? y0[0] : -INFINITY;
+      z[4 * p + 1] = a1 ? y1[0] : -INFINITY;
+      z[4 * p + 2] = b0 ? y0[1] : -INFINITY;
+      z[4 * p + 3] = b1 ? y1[1] : -INFINITY;
     } else {
       z[4 * p + 0] = visible<SC>(ta, pos0, cut) ? fmaf(acc[0], scale, bs0) : -INFINITY;
       z[4 * p + 1] = visible<SC>(ta, pos1, cut) ? fmaf(acc[1], scale, bs1) : -INFINITY;
