@@ -89,8 +89,12 @@ __global__ void __launch_bounds__(kThreads, 4) tiles_kernel(PromptArgs a) {
   const int quant = values ? Tv : Tk, mod = FMT == kI8 ? kP : values ? a.R : kG;
   const uint16_t* ring = values ? reinterpret_cast<const uint16_t*>(a.vring) + slot * a.vring_slot + h * a.vring_head
                                 : reinterpret_cast<const uint16_t*>(a.kring) + slot * a.kring_slot + h * a.kring_head;
-  const int end = min(max(T - tp, 0), kP);            // tokens [0, end) of this page are there
-  const int held = min(max(quant - tp, 0), end);    // [0, held) in its record
+  // A tile may reach past the tokens that some query sees (those from `low` on, and the sinks), to pages that the
+  // sequence has given back: zeros, and the table is not looked at.
+  const int low = max(0, T - m - a.form.window + 1);
+  const bool seen = tp < a.form.sinks || tp + kP > low;
+  const int end = seen ? min(max(T - tp, 0), kP) : 0;   // tokens [0, end) of this page are there
+  const int held = min(max(quant - tp, 0), end);      // [0, held) in its record
   // the table's entries, on their way while the sequence is checked
   const bool group = !kByte<FMT> && !values;   // half of a key group: both its pages
   const int page = tp / kP;
