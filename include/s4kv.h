@@ -469,9 +469,11 @@ int s4kv_prompt_attention(s4kv_cache* cache, int layer, const s4kv_scores* score
  * s4kv_release_pages: entries ceil(first / 16) .. ceil(last / 16) - 1 of each row become -1, and their
  * pages' refs go down by one; entries that are -1 already are passed over. first = 0 and
  * last = the length gives a finished sequence's pages back. Behind a window: first = the sinks
- * rounded up, last = the window's start rounded down, to whole blocks (32 tokens of KIVI
- * pages, 16 of the others). An entry outside the pool, or of a page that nobody holds, is
- * S4KV_DEV_BAD_PAGE. */
+ * rounded up, last = the window's start (of the earliest query still to come) rounded down, to
+ * whole blocks (32 tokens of KIVI pages, 16 of the others). KIVI pages: last no further than
+ * T - residual_v and 32 floor(T / 32) either, as the values and keys from there on have still to be
+ * written (an append that finds no page for them reports S4KV_DEV_BAD_PAGE). An entry outside
+ * the pool, or of a page that nobody holds, is S4KV_DEV_BAD_PAGE. */
 int s4kv_take_pages(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int bt_stride, int rows, const int32_t* lens,
                     const int32_t* new_lens, const int32_t* slot_ids, int n, int32_t* taken, void* stream);
 int s4kv_release_pages(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int bt_stride, int rows, const int32_t* first,

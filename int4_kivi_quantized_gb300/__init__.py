@@ -785,7 +785,9 @@ class KVCache:
     @_on_its_device
     def release_pages(self, refs, block_table, first, last, slot_ids=None, stream=None):
         """Gives up the pages of tokens first .. last - 1 of each sequence (whole pages from `first`
-        on, the one that holds `last` - 1 included): their entries become -1, their counts go down."""
+        on, the one that holds `last` - 1 included): their entries become -1, their counts go down.
+        Of a sequence of T tokens that goes on, on KIVI pages, `last` is T - residual_v at most, rounded
+        down to 32 tokens: later values have still to be written."""
         torch = self._torch
         n = first.shape[0]
         self._tensor(first, "first", torch.int32, (n,))
