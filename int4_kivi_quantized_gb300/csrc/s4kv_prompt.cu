@@ -442,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
       const uint32_t s_at = tmem + 128 * s + t_row, o_at = tmem + 256 + 128 * s + t_row;
       constexpr float kLog2e = 1.4426950408889634f;
       RowScore f;
-      const float scale = a.sm_scale * sm.up[tid], lin = scale * kLog2e;
+      const float key_scale = a.bits == 8 ? a.fp8_scale[h] : 1.0f;   // (FP8: the tiles hold codes)
+      const float scale = a.sm_scale * sm.up[tid] * key_scale, lin = scale * kLog2e;
       f.mul = fminf(fmaxf(CAP ? scale / a.form.cap : lin, 0x1p-126f), 0x1p127f);   // (zero times it is zero, -inf -inf)
       f.cap2 = CAP ? a.form.cap * kLog2e : 0.0f;
       f.slope2 = SLOPE ? a.form.slopes[h * g + (row0 + tid) % g] * kLog2e : 0.0f;
@@ -605,7 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
       tc_fence_after();
       const bool some = ok && cnt > 0;
       const long long item = (static_cast<long long>(q_tile) * a.H + h) * a.splits + z;
-      const float inv = a.splits > 1 ? 1.0f : l > 0.0f ? 1.0f / l : l == l ? 0.0f : l;
+      const float value_scale = a.bits == 8 ? a.fp8_scale[a.H + h] : 1.0f;
+      const float inv = (a.splits > 1 ? 1.0f : l > 0.0f ? 1.0f / l : l == l ? 0.0f : l) * value_scale;
       // Through the queries' place in shared memory (nothing reads them any more), so that a warp writes whole
       // rows: 16 chunks of 16 bytes, chunk c of row r at c xor (r mod 16). 32 bits: in two goes.
       char* stage = q_tiles + s * kQBytes + (warp & 3) * 32 * 256;

@@ -6,9 +6,9 @@
 // that tcgen05 reads, as a K-major operand (keys) and as an MN-major one (values), so the attention
 // kernel fetches a tensor's tile with one bulk copy. f16 keeps 11 bits of a restored value
 // where the caches' bf16 would keep 8: a key's rounding then moves a score by 2^-11 of its
-// terms at most. Values beyond f16's range become infinities; a value row with an element
-// that is not finite (then) is stored as zeros where it is not and gets a bit, so that queries which
-// do not see it never meet it.
+// terms at most. FP8 codes are exact in f16 and stay codes, at any scale. Values beyond f16's range become
+// infinities; a value row with an element that is not finite (then) is stored as zeros where it is not and gets
+// a bit, so that queries which do not see it never meet it.
 //
 // A CTA takes one tensor of a tile, a warp a page of it (of a key group on KIVI pages, whose metadata
 // lie in two pages' records). 64 KB are written for every 8 to 17 KB read, and most of them stay in
@@ -121,9 +121,10 @@ __global__ void __launch_bounds__(kThreads, 4) tiles_kernel(PromptArgs a) {
       }
     } else {
       const char* rec = record(pp[0]);
+      const float one = 1.0f;   // FP8: codes, exact in f16; the attention kernel scales scores and outputs
       if (!rec) rows.clear(0, held);
-      else if (values) put_values<FMT>(a.fp8_scale + a.H + h, rec, 0, held, rows);
-      else if constexpr (kByte<FMT>) put_keys<FMT>(a.fp8_scale + h, rec, 0, held, rows);
+      else if (values) put_values<FMT>(&one, rec, 0, held, rows);
+      else if constexpr (kByte<FMT>) put_keys<FMT>(&one, rec, 0, held, rows);
     }
   }
   if (FMT != 8 && end > held) put_ring(ring, mod, tp, held, end, a.dtype, rows);
