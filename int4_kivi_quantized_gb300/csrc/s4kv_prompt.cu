@@ -55,7 +55,10 @@ constexpr int kThreads = 384;        // (two more warps make a warpgroup of the 
 constexpr int kRegsRow = 224, kRegsRest = 56;
 static_assert(2 * kRegsRow + kRegsRest <= 3 * 168, "the shares are what the launch holds");
 constexpr int kBufs = 5;
-constexpr float kLazyP = 8.0f;       // P up to 2^8 before its sum divides it: exact enough in f16, and rescales are rare
+// A row's reference stands kRoom below the largest score so far and rises when one passes it by more than
+// kRoom + kLazyP: P up to 2^15 in f16 before its sum divides it, so that rescales are rare, and what lies 2^-21
+// below the largest keeps its 11 bits, what lies 2^-32 below it one.
+constexpr float kLazyP = 8.0f, kRoom = 7.0f;
 constexpr int kQBytes = 128 * kD * 2;
 constexpr int kSmemBytes = 2 * kQBytes + kBufs * kTileBytes + 1024;
 // tensor memory columns: S (and P) of tile s at 128 s, O at 256 + 128 s
@@ -553,8 +556,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
         }
         if (raw) top = near(top);
         else top = fmaf(largest(), in, at);
-        if (__any_sync(0xffffffffu, top > mx + kLazyP)) {
-          const float mn = top > mx + kLazyP ? top : mx;
+        if (__any_sync(0xffffffffu, top > mx + (kRoom + kLazyP))) {
+          const float mn = top > mx + (kRoom + kLazyP) ? top - kRoom : mx;
           const float by = mx == mn ? 1.0f : mx == -INFINITY ? 0.0f : exp2_fast(mx - mn);   // (nothing so far: l and O are zeros)
           if (i > 0) {
             ok = __all_sync(0xffffffffu, wait(&sm.odone[s], (i - 1) & 1));
