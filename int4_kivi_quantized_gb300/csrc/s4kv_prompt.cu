@@ -365,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
           sent = it + 1;
         }
         // every copy has landed before the CTA ends
-        for (int it = max(0, sent - kBufs); it < sent; ++it) mbar_wait(&sm.full[it % kBufs], (it / kBufs) & 1, kDrainNs);
+        for (int it = max(0, sent - kBufs); it < sent; ++it)
+          if (!mbar_wait(&sm.full[it % kBufs], (it / kBufs) & 1, kDrainNs)) *flag = 1;
       }
       __syncwarp();
     } else if (warp == kMmaWarp) {
@@ -432,8 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
         // no MMA is in flight when the CTA ends
         if (elect_one()) umma_commit(&sm.drain);
         __syncwarp();
-        mbar_wait(&sm.drain, 0, kDrainNs);
-        if (!ok && lane == 0) report(a.status, S4KV_ERR_DEVICE_TIMEOUT, S4KV_DEV_TIMEOUT, b);
+        if (!mbar_wait(&sm.drain, 0, kDrainNs)) *flag = 1;
       }
       __syncwarp();
     }
@@ -661,6 +661,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // a wait of any role that ran out, the rows' last one too (their output is zeros then)
+  if (tid == 0 && *flag) report(a.status, S4KV_ERR_DEVICE_TIMEOUT, S4KV_DEV_TIMEOUT, b);
   if (warp == kLoadWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols));
 }
