@@ -154,7 +154,8 @@ enum {
   S4KV_DEV_BAD_PAGE = 1,       /* block-table entry outside [0, num_pages) */
   S4KV_DEV_BAD_LENGTH = 2,     /* length disagrees with the slot's stored length */
   S4KV_DEV_BAD_SLOT = 3,       /* slot id outside [0, max_slots) */
-  S4KV_DEV_BAD_TABLE = 4,      /* table too narrow for the sequence */
+  S4KV_DEV_BAD_TABLE = 4,      /* table too narrow for the sequence, or an entry to be
+                                  filled that is not -1 */
   S4KV_DEV_BAD_CU = 5,         /* cu_new not non-decreasing / total mismatch */
   S4KV_DEV_TIMEOUT = 6,        /* an mbarrier wait exceeded its limit */
   S4KV_DEV_BAD_POSITION = 7    /* a token past the rotation table, or a range past its sequence */
@@ -464,7 +465,9 @@ int s4kv_prompt_attention(s4kv_cache* cache, int layer, const s4kv_scores* score
  * served and not): its row is left as it was, and so are the rows behind it that want pages.
  * A sequence with a row outside the table (or named twice in the call, each of them), a
  * negative length or one that shrinks, or pages beyond bt_stride gets -1 and the status
- * S4KV_DEV_BAD_SLOT, _BAD_LENGTH, _BAD_TABLE; it counts for no pages.
+ * S4KV_DEV_BAD_SLOT, _BAD_LENGTH, _BAD_TABLE; it counts for no pages. One with an
+ * entry to fill that is not -1 (its page would be lost) gets -1 and S4KV_DEV_BAD_TABLE too; the
+ * pages that it would have got stay free, and count.
  *
  * s4kv_release_pages: entries ceil(first / 16) .. ceil(last / 16) - 1 of each row become -1, and their
  * pages' refs go down by one; entries that are -1 already are passed over. first = 0 and

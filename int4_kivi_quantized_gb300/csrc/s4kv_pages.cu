@@ -71,6 +71,7 @@ __global__ void __launch_bounds__(kThreads, 1) give_kernel(PageArgs a) {
   __shared__ unsigned pre[kMaxPageJobs + 1];                  // pages wanted by the sequences before
   __shared__ unsigned seen[kMaxPageRows / 32];                // rows, a bit each
   __shared__ unsigned list[kList];                            // two more such sets, then pages by rank
+  __shared__ unsigned filled[FORK ? 1 : kMaxPageJobs / 32];   // sequences, a bit each: an entry to fill names a page
   unsigned* const twice = list;
   unsigned* const source = list + kMaxPageRows / 32;
   static_assert(kList >= 2 * (kMaxPageRows / 32), "both sets");
@@ -79,6 +80,7 @@ __global__ void __launch_bounds__(kThreads, 1) give_kernel(PageArgs a) {
     seen[i] = twice[i] = 0u;
     if (FORK) source[i] = 0u;
   }
+  for (int i = tid; !FORK && i < (a.n + 31) / 32; i += kThreads) filled[i] = 0u;
   stream_wait();
   __syncthreads();
   auto row_ok = [&](int r) { return r >= 0 && r < a.rows; };
@@ -159,11 +161,59 @@ __global__ void __launch_bounds__(kThreads, 1) give_kernel(PageArgs a) {
     }
     return z;
   };
+  auto owner_of = [&](unsigned k) -> int {   // of the page of rank k: the last sequence with pre <= k
+    int lo = 0, hi = a.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= k) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  };
+  // The entries for the pages of ranks r + tid, r + tid + kThreads, ..: whose, and where (row -1: none).
+  constexpr int kMine = kList / kThreads;
+  auto entries_of = [&](unsigned r, unsigned end, Want (&w)[kMine], int (&who)[kMine]) {
+#pragma unroll
+    for (int c = 0; c < kMine; ++c) {
+      const unsigned k = r + tid + c * kThreads;
+      w[c].row = -1;
+      if (k >= end) continue;
+      who[c] = owner_of(k);
+      w[c] = want_of<FORK>(a, who[c]);
+      w[c].e0 += k - pre[who[c]];
+    }
+  };
+  auto entry = [&](const Want& w) -> int& { return a.table[static_cast<long long>(w.row) * a.bt_stride + w.e0]; };
+  __syncthreads();   // the sums are there
+  const unsigned most = min(total, static_cast<unsigned>(a.num_pages));   // ranks that there may be
+  Want first_w[kMine];
+  int first_who[kMine];
+  entries_of(0, most, first_w, first_who);
+  unsigned z0 = 0;
+  if (!FORK) {   // entries that name a page (a fork's new row is overwritten)
+    int old[kMine];
+#pragma unroll
+    for (int c = 0; c < kMine; ++c) old[c] = first_w[c].row >= 0 ? entry(first_w[c]) : -1;
+    if (total > 0) z0 = look(0);
+#pragma unroll
+    for (int c = 0; c < kMine; ++c)
+      if (old[c] != -1) atomicOr(&filled[first_who[c] >> 5], 1u << (first_who[c] & 31));
+    for (unsigned r = kList; r < most; r += kList) {
+      Want w[kMine];
+      int who[kMine];
+      entries_of(r, most, w, who);
+#pragma unroll
+      for (int c = 0; c < kMine; ++c) old[c] = w[c].row >= 0 ? entry(w[c]) : -1;
+#pragma unroll
+      for (int c = 0; c < kMine; ++c)
+        if (old[c] != -1) atomicOr(&filled[who[c] >> 5], 1u << (who[c] & 31));
+    }
+  } else if (total > 0) {
+    z0 = look(0);
+  }
   // enough of them, or all there are (the last tile looked at is at hand again if it is the first)
-  unsigned found = 0, z0 = 0;
+  unsigned found = 0;
   for (int base = 0; found < total && base < a.num_pages; base += kTile) {
-    const unsigned z = look(base);
-    if (base == 0) z0 = z;
+    const unsigned z = base == 0 ? z0 : look(base);
     unsigned here;
     block_scan(__popc(z), here);
     found = add_to(found, here);
@@ -180,7 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1) give_kernel(PageArgs a) {
   }
   for (int i = tid; i < a.n; i += kThreads) {
     const Want w = want_of<FORK>(a, i);
-    if (a.taken[i] == 0 && w.e1 > w.e0) a.taken[i] = pre[i + 1] <= granted ? w.e1 - w.e0 : -1;
+    if (a.taken[i] != 0 || w.e1 <= w.e0) continue;
+    const bool room = pre[i + 1] <= granted, full = !FORK && bit(filled, i);
+    if (room && full) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_TABLE, i);
+    a.taken[i] = room && !full ? w.e1 - w.e0 : -1;
   }
   unsigned rank0 = 0;
   for (int base = 0; rank0 < granted && base < a.num_pages; base += kTile) {
@@ -193,26 +246,23 @@ __global__ void __launch_bounds__(kThreads, 1) give_kernel(PageArgs a) {
       for (unsigned y = z; y && k < end; y &= y - 1, ++k)
         if (k - r < kList) list[k - r] = base + tid * kEach + __ffs(y) - 1;
       __syncthreads();
-      constexpr int kMine = kList / kThreads;
       Want w[kMine];
+      int who[kMine];
+      if (r == 0) {
 #pragma unroll
-      for (int c = 0; c < kMine; ++c) {
-        k = r + tid + c * kThreads;
-        if (k >= end) continue;
-        int lo = 0, hi = a.n - 1;   // the last sequence with pre <= k
-        while (lo < hi) {
-          const int mid = (lo + hi + 1) >> 1;
-          if (pre[mid] <= k) lo = mid; else hi = mid - 1;
+        for (int c = 0; c < kMine; ++c) {
+          w[c] = first_w[c];
+          who[c] = first_who[c];
         }
-        w[c] = want_of<FORK>(a, lo);
-        w[c].e0 += k - pre[lo];
+      } else {
+        entries_of(r, end, w, who);
       }
 #pragma unroll
       for (int c = 0; c < kMine; ++c) {
         k = r + tid + c * kThreads;
-        if (k >= end) continue;
+        if (k >= end || (!FORK && bit(filled, who[c]))) continue;   // (filled: its pages stay free)
         const int p = list[k - r];
-        a.table[static_cast<long long>(w[c].row) * a.bt_stride + w[c].e0] = p;
+        entry(w[c]) = p;
         a.refs[p] = 1;
       }
     }
