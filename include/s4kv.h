@@ -491,8 +491,10 @@ int s4kv_release_pages(s4kv_cache* cache, int32_t* refs, int32_t* block_table, i
  * release its pages first.
  * A source may be forked many times in a call, and goes on itself. A dst named twice, or a
  * source of the same call, or either outside the table is S4KV_DEV_BAD_SLOT, a stored length other
- * than seq_lens[i] S4KV_DEV_BAD_LENGTH, a row too narrow S4KV_DEV_BAD_TABLE: taken -1, and
- * nothing of that fork is done, as for one without enough free pages (which reports nothing).
+ * than seq_lens[i] S4KV_DEV_BAD_LENGTH, a row too narrow S4KV_DEV_BAD_TABLE, an entry outside the
+ * pool (-1 too) of a page that has to be copied S4KV_DEV_BAD_PAGE: taken -1, and nothing of that
+ * fork is done, as for one without enough free pages (which reports nothing). An entry outside
+ * the pool of a page to be shared is reported as S4KV_DEV_BAD_PAGE and becomes -1 in dst's row.
  * Appends to src and calls that read dst must be ordered with it. Two kernel launches. */
 int s4kv_fork(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int bt_stride, int rows, const int32_t* src,
               const int32_t* dst, const int32_t* seq_lens, int n, int32_t* taken, void* stream);

@@ -101,13 +101,20 @@ __global__ void __launch_bounds__(kThreads, 1) give_kernel(PageArgs a) {
     if (pages_for(FORK ? a.seq_lens[i] : a.to[i]) > a.bt_stride) return S4KV_DEV_BAD_TABLE;
     return 0;
   };
-  if (FORK) {   // a warp a fork: every layer and head of the source holds as many tokens
+  if (FORK) {   // a warp a fork: every layer and head of the source holds as many tokens, and what has to be copied is there
     for (int i = warp; i < a.n; i += kThreads / 32) {
       int arg, why = refused(i, arg);
       if (!why) {
-        bool other = false;
-        for (int k = lane; k < a.layers * a.H; k += 32)
-          other = other || __ldcg(a.lens + (static_cast<size_t>(k / a.H) * a.max_slots + a.from[i]) * a.H + k % a.H) != a.seq_lens[i];
+        const int src = a.from[i], T = a.seq_lens[i], words = a.layers * a.H;
+        const Held x = held_of(a.bits, T, a.R);
+        auto page = [&](int e) { return e < x.held ? a.table[static_cast<long long>(src) * a.bt_stride + e] : 0; };
+        auto length = [&](int k) { return k < words ? __ldcg(a.lens + (static_cast<size_t>(k / a.H) * a.max_slots + src) * a.H + k % a.H) : T; };
+        auto outside = [&](int p) { return p < 0 || p >= a.num_pages; };
+        const int p0 = page(x.done + lane), n0 = length(lane);   // (asked for together)
+        bool hole = outside(p0), other = n0 != T;
+        for (int e = x.done + 32 + lane; e < x.held; e += 32) hole = hole || outside(page(e));
+        for (int k = 32 + lane; k < words; k += 32) other = other || length(k) != T;
+        if (__any_sync(0xffffffffu, hole)) why = S4KV_DEV_BAD_PAGE;
         if (__any_sync(0xffffffffu, other)) why = S4KV_DEV_BAD_LENGTH;
       }
       if (lane == 0) {
@@ -328,10 +335,7 @@ __global__ void __launch_bounds__(kCopy) fork_kernel(PageArgs a) {
     const int e = x.done + part;
     if (e >= x.held) return;
     const int p = from[e], q = to[e];
-    if (p < 0 || p >= a.num_pages) {
-      if (threadIdx.x == 0) report(a.status, S4KV_ERR_DEVICE, S4KV_DEV_BAD_PAGE, p);
-      return;
-    }
+    if (p < 0 || p >= a.num_pages) return;   // (not so when the launch before this one looked: the table may not change meanwhile)
     copy_bytes(base + q * a.page_bytes, base + p * a.page_bytes, static_cast<int>(a.page_bytes));
   } else if (part < a.pages_at_most + a.H) {
     const int h = part - a.pages_at_most;
