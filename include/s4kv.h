@@ -455,8 +455,8 @@ int s4kv_prompt_attention(s4kv_cache* cache, int layer, const s4kv_scores* score
  * caller's: how many block-table entries name each page, 0 for a free one; all zeros
  * before the first call. block_table: int32 [rows][bt_stride], a row for each slot; an
  * entry that names no page is -1. slot_ids: int32 [n] or NULL (row i for sequence i).
- * n up to 4096, rows up to 65536. Calls on the same refs must be ordered, on one stream
- * for instance. One kernel launch each.
+ * n up to 4096, rows up to 65536. taken may not overlap the arrays that are read (INVALID_ARG).
+ * Calls on the same refs must be ordered, on one stream for instance. One kernel launch each.
  *
  * s4kv_take_pages: sequence i grows from lens[i] to new_lens[i] tokens: entries
  * ceil(lens / 16) .. ceil(new_lens / 16) - 1 of its row get free pages (refs 1), the lowest

@@ -915,6 +915,11 @@ int page_args(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int bt_str
   a->num_pages = cache->cfg.num_pages;
   return S4KV_OK;
 }
+// taken[n] is written while the others are still read: it may not lie over them.
+bool apart(const int32_t* taken, int n, const int32_t* read) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(taken), y = reinterpret_cast<uintptr_t>(read), bytes = static_cast<uintptr_t>(n) * 4;
+  return !read || x + bytes <= y || y + bytes <= x;
+}
 }  // namespace
 
 int s4kv_take_pages(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int bt_stride, int rows, const int32_t* lens,
@@ -923,6 +928,7 @@ int s4kv_take_pages(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int 
   const int rc = page_args(cache, refs, block_table, bt_stride, rows, lens, new_lens, n, &a);
   if (rc != S4KV_OK || n == 0) return rc;
   if (!taken || (!slot_ids && n > rows)) return S4KV_ERR_INVALID_ARG;
+  if (!apart(taken, n, lens) || !apart(taken, n, new_lens) || !apart(taken, n, slot_ids)) return S4KV_ERR_INVALID_ARG;
   a.slot_ids = slot_ids;
   a.taken = taken;
   return launch_take(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? S4KV_OK : S4KV_ERR_CUDA;
@@ -945,6 +951,7 @@ int s4kv_fork(s4kv_cache* cache, int32_t* refs, int32_t* block_table, int bt_str
   if (rc != S4KV_OK || n == 0) return rc;
   const s4kv_config& c = cache->cfg;
   if (!seq_lens || !taken || rows > c.max_slots) return S4KV_ERR_INVALID_ARG;
+  if (!apart(taken, n, src) || !apart(taken, n, dst) || !apart(taken, n, seq_lens)) return S4KV_ERR_INVALID_ARG;
   if (c.num_layers > 65535) return S4KV_ERR_UNSUPPORTED;   // (a grid's second dimension)
   a.seq_lens = seq_lens;
   a.taken = taken;
