@@ -461,8 +461,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
         const int t0 = kv_of(i) * kKvTile;
         const uint4 wild = next;
         if (i + 1 < cnt) next = wild_of(i + 1);
-        const bool all_see = __all_sync(0xffffffffu, t0 + kKvTile - 1 <= sp.hi && (t0 >= sp.lo || t0 + kKvTile <= a.form.sinks));
-        const bool whole = all_see && (wild.x | wild.y | wild.z | wild.w) == 0;
+        const bool row_sees = t0 + kKvTile - 1 <= sp.hi && (t0 >= sp.lo || t0 + kKvTile <= a.form.sinks);
+        const bool clean = (wild.x | wild.y | wild.z | wild.w) == 0;
+        const bool all_see = CAP && __all_sync(0xffffffffu, row_sees);   // (caps alone ask for it: two votes cost 1% of a sloped prompt)
+        const bool whole = CAP ? all_see && clean : __all_sync(0xffffffffu, row_sees && clean);
         ok = __all_sync(0xffffffffu, wait(&sm.sfull[s], i & 1));
         if (!ok) break;
         tc_fence_after();
