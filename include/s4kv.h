@@ -402,7 +402,8 @@ typedef struct {
   float cap;               /* 0: no cap; 2^-60 .. 2^60 otherwise */
   const float* slopes;     /* device, fp32 [num_q_heads] (finite), or NULL */
   int window;              /* newest tokens visible, the query's own included; 0: no window */
-  int num_sinks;           /* first tokens visible whatever window and first say */
+  int num_sinks;           /* first tokens of the sequence, visible whatever window and first say: in a row
+                              of packed documents the first document's, to all of them (0 there) */
   const int32_t* first;    /* device, by query token: the first token of its document, or NULL */
   const int32_t* prefix;   /* device, by sequence: its first tokens see one another whole, or NULL */
 } s4kv_scores;
@@ -437,11 +438,18 @@ int s4kv_score_attention(s4kv_cache* cache, int layer, const s4kv_scores* scores
  * Every page format; num_q_heads / H_kv 1..8, n up to 4096, num_q * group up to 2^30.
  * Two kernel launches, or three: the cached tokens that a chunk can see are restored
  * to f16 once, matrix operands from then on; chunks of few rows split the cache's length and
- * combine. Restored keys and values beyond 65504 in magnitude count as infinities there.
+ * combine. Pages are read from the window's start of a chunk's first query on, and those of the
+ * sinks (first takes none away); the others' entries may be -1. f16 keeps 11 bits of a restored key
+ * or value: beyond 65504 in magnitude it counts as an infinity, below 6.1e-5 it is a multiple of
+ * 6e-8. FP8 codes are exact, at any scale. Of a bf16 query, elements below 2^-20 of the row's
+ * largest lose bits (up to 2^-28 of the largest each).
  * A query that sees a token whose value row is not finite (or so large) gets NaN; tokens
- * that it does not see never reach its row, whatever they hold. Short chunks of equal length
+ * that it does not see never reach its row, in no bit, whatever they hold. Offsets that are not
+ * what they should be are S4KV_DEV_BAD_CU, and out is left as it was. Short chunks of equal length
  * (1 to 16 tokens) are read faster by s4kv_score_attention up to 48 query columns (tokens
- * times query heads of a kv head), on 8-bit pages up to 64; beyond, the two are level. */
+ * times query heads of a kv head), on 8-bit pages up to 64; beyond, the two are level. The same
+ * holds for single tokens in a batch of prompts: their context is restored whole, so that a
+ * program gives them a call of their own. */
 int s4kv_prompt_workspace_bytes(const s4kv_cache* cache, int n, int num_q, int num_q_heads, int max_seq_len,
                                 long long sum_seq_lens, size_t* bytes);
 int s4kv_prompt_attention(s4kv_cache* cache, int layer, const s4kv_scores* scores, const void* q, int num_q,

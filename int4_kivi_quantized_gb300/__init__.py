@@ -376,7 +376,8 @@ class Rope:
 class Scores:
     """A model's score form for attend and prompt: scores capped at cap tanh(x / cap) (0: as they
     are), less slopes[head] |p - t| (fp32 [H_q] on the cache's device, kept alive by this object),
-    within the newest `window` tokens (0: all) and the first `num_sinks`."""
+    within the newest `window` tokens (0: all) and the sequence's first `num_sinks` (which every document
+    packed behind them sees, too)."""
 
     def __init__(self, cap=0.0, slopes=None, window=0, num_sinks=0):
         if slopes is not None:
@@ -770,7 +771,8 @@ class KVCache:
     def take_pages(self, refs, block_table, lens, new_lens, slot_ids=None, taken=None, stream=None):
         """Free pages (refs [num_pages]: the table entries that name each; 0: free) for sequences that
         grow from `lens` to `new_lens` tokens, into their rows of block_table [slots, entries], lowest
-        page first. Returns `taken` [n]: how many each got, -1 where too few are free."""
+        page first. Returns `taken` [n]: how many each got, -1 where too few are free or an entry to
+        fill names a page already. `taken` lies apart from the other tensors."""
         torch = self._torch
         n = lens.shape[0]
         self._tensor(lens, "lens", torch.int32, (n,))

@@ -4,14 +4,15 @@
 // Giving out pages is a scan: sequence i's pages are the free ones of rank need_1 + .. +
 // need_(i-1) on, and the page of rank k is the k-th zero of refs. One CTA does it, as a scheduler's
 // step asks for some hundred pages: it stops at the tile of refs where enough are found. What
-// bounds it is latency: the launch, the lengths, one or two tiles, the entries. Measured: 32 sequences
-// 8.3 us, 512 that take 1536 pages 10.5 (14 when the thread that found a page entered it too); with the
-// release behind it 12.4 and 16.5 in a captured graph. Bytes at the memory's rate would be 0.5.
+// bounds it is latency: the launch, the lengths, one or two tiles, the entries. Measured under the profiler, cold
+// caches: 32 sequences 9.4 us, 512 that take 1536 pages 11.9; with the release behind it, many in a captured
+// graph, 8.4 and 10.9 (7.6 and 10.0 without a look at the entries first; entered by the thread that found a page
+// 3.5 more for the 512). Bytes at the memory's rate would be 0.5.
 //
 // A fork then copies what both sequences would go on writing (the pages from the first
 // unfinished one on, the rings), a CTA for each page, or head's rings, of each layer, 16 bytes a
 // thread and load, eight loads in flight: bound by those bytes, read and written once. Measured: four
-// forks of one 4-bit sequence of 1000 tokens, 4 layers, 8 heads: 10 us and 6.8; 64 forks of 16 prompts
+// forks of one 4-bit sequence of 1000 tokens, 4 layers, 8 heads: 10.3 us and 7.0; 64 forks of 16 prompts
 // of 700 to 2048 10 us and 25.
 
 #include "s4kv_pages.cuh"

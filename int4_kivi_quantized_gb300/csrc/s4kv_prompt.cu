@@ -8,7 +8,7 @@
 //     S = Q K^T (128 x 128 x 128),  P = exp2(score form(S) - m),  O += P V (128 x 128 x 128)
 // with S and O in tensor memory; P, in f16, takes S's place there and is the A operand of
 // P V. One thread a row: its 128 scores come in registers, so maxima and sums need no
-// shuffle, and a rescale of O (when a maximum rises by more than kLazyP) is the row's own.
+// shuffle, and a rescale of O (when a maximum rises by more than kLazyP above the last one) is the row's own.
 //
 // Warps 0 .. 3 and 4 .. 7 are the rows of the two tiles, warp 8 fetches (a ring of five 32 KB
 // buffers, keys and values in turn, one bulk copy each), warp 9 issues the MMAs: P V and the next
@@ -23,9 +23,9 @@
 // where tiles of 128 rows alone would ask for twice that.
 //
 // Measured (one launch with its tiles and combine, a captured graph): 2048 tokens behind 32768, 28 query
-// heads, 4 kv heads 638 us, 1462 TFLOP/s of the visible pairs (77% of a library matrix product's rate),
-// with a cap of 30 and scores near zero 822, with scores beyond it 1388, with slopes 815, with both
-// 1111. A prompt of 2048, 32 heads 44 to 46 (780 to 750). Eight chunks of 512 behind 2048 to 8192, sloped 368. What
+// heads, 4 kv heads 626 us, 1490 TFLOP/s of the visible pairs (78% of a library matrix product's rate),
+// with a cap of 30 and scores near zero 823, with scores beyond it 1390, with slopes 807, with both
+// 1115. A prompt of 2048, 32 heads 44 to 46 (780 to 750). Eight chunks of 512 behind 2048 to 8192, sloped 351. What
 // bounds it:
 //  * the loop: 2811 cycles a kv tile, of which the four MMAs take 2052 (513 each, read out of shared
 //    memory or with P out of tensor memory alike); the rest is P's way to tensor memory and the hand-over.
@@ -269,8 +269,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(PromptArgs a) {
       atomicMax(&sm.hi, hi);
     }
     // f16 operands, swizzled. bf16 has the wider range: a row is taken at the power of two that brings its
-    // largest element to 2^3 .. 2^4: exact, elements down to 2^-28 of the largest keep every bit,
-    // and powers of what then scales the scores stay normal numbers.
+    // largest element to 2^3 .. 2^4: exact, elements down to 2^-17, 2^-20 of the largest, keep every bit, smaller
+    // ones are off by 2^-25 at most (2^-28 of the largest), and powers of what then scales the scores stay
+    // normal numbers where they can.
     const int c = lane & 15;
     float up = 1.0f;   // of row lane % 16 of this half warp's
     if (a.dtype == S4KV_BF16) {

@@ -28,7 +28,7 @@ struct ScoredArgs : WindowArgs {
 };
 cudaError_t launch_scored(const ScoredArgs& a, int num_sms, cudaStream_t st);
 
-// Capping scores. Those of a model that was trained with a cap lie well within it: for |x| <= kNearCap
+// Capping scores, x the score by the cap. Those of a model that was trained with a cap lie well within it: for |x| <= kNearCap
 // tanh(x) = x P(x^2), P the cubic of least relative error there (a weighted least-squares fit,
 // 5.5e-7). Beyond, tanh(x) = 1 - 2 / (1 + exp(2 x)), whose exponential and reciprocal are off by
 // 2^-22 or so relative: 2^-22 of the cap in a score, for scores of half of it and more (and what
